@@ -266,6 +266,154 @@ semicrf_status semicrf_nll_backward(const semicrf_dims *dims, const double *S, c
                                     const double *grad_nll, void *ws, size_t ws_bytes, float *dX, double *dA,
                                     double *dD, void *stream);
 
+/* ---- Operators around the loss -------------------------------------------------
+ *
+ * What makes the emissions of long sequences (linear attention with a decay for
+ * each head, group norm with an activation) and what turns gradients into new
+ * parameters (AdamW).  The pages have no counterpart to them.  Ownership, streams
+ * and errors as above: caller-owned device memory, asynchronous, arguments checked
+ * on the host before any launch.  Device findings (a length outside its range) go
+ * to the status word at the start of the call's workspace; such a length is taken
+ * as the nearest one in range.
+ */
+
+/* Element types. */
+#define SEMICRF_F32 0
+#define SEMICRF_BF16 1
+#define SEMICRF_F16 2
+#define SEMICRF_F64 3 /* gradients given to semicrf_adamw only */
+
+/*
+ * Linear attention with a decay for each head.  For every sequence b and head h,
+ * with lam = exp(log_decay[h]) and positions p = 0 .. L_b - 1 in walking order
+ * (reverse: from the last valid position to the first),
+ *   S_p = lam S_{p-1} + k_p v_p^T,     o_p = scale q_p S_p.
+ *   q, k       dtype [B, T, H, dk], v, o dtype [B, T, H, dv]: strides of b, t and h
+ *              in elements, the last axis dense
+ *   log_decay  float32 [H], at most 0 (not checked)
+ *   lengths    int32 [B], in [0, T], or NULL (all T); o = 0 at t >= L_b, where
+ *              nothing is read
+ *   state_in   float32 [B, H, dk, dv], S before the first position, or NULL (zero)
+ *   state_out  float32 [B, H, dk, dv], S behind the last position, or NULL
+ * Sums and the state are float32, whatever dtype; each output is rounded once.  A
+ * value that is not finite may spread to every position of its sequence and head.
+ */
+typedef struct {
+    int32_t B, T, H, dk, dv;
+    int32_t dtype;   /* SEMICRF_F32, _BF16 or _F16 */
+    int32_t reverse; /* 0 or 1 */
+    float scale;
+    int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3]; /* of b, t, h */
+} semicrf_attention_dims;
+
+/* Compiled limit of dk and dv. */
+#define SEMICRF_MAX_HEAD 256
+
+/* Bytes of workspace (256-byte aligned) of the forward (backward = 0) or the
+ * backward call; 0 for invalid dims. */
+size_t semicrf_linear_attention_workspace_bytes(const semicrf_attention_dims *dims, int32_t backward);
+
+semicrf_status semicrf_linear_attention(const semicrf_attention_dims *dims, const void *q, const void *k,
+                                        const void *v, const float *log_decay, const int32_t *lengths,
+                                        const float *state_in, void *o, float *state_out, void *ws,
+                                        size_t ws_bytes, void *stream);
+
+/*
+ * Gradients for the upstream grad_o (dtype, strides o_stride) and grad_state
+ * (of state_out, float32 [B, H, dk, dv], or NULL): dq, dk [B, T, H, dk] and dv
+ * [B, T, H, dv], contiguous, dtype (0 at t >= L_b), and grad_state_in float32
+ * [B, H, dk, dv] (or NULL).  log_decay is a constant of the model: no gradient.
+ */
+semicrf_status semicrf_linear_attention_backward(const semicrf_attention_dims *dims, const void *q, const void *k,
+                                                 const void *v, const float *log_decay, const int32_t *lengths,
+                                                 const float *state_in, const void *grad_o, const float *grad_state,
+                                                 void *dq, void *dk, void *dv, float *grad_state_in, void *ws,
+                                                 size_t ws_bytes, void *stream);
+
+/*
+ * One position: state = lam state + k v^T in place and o = scale q state.  q, k, v
+ * and o are [B, H, d]; of the strides those of b and h are used, T is 1.
+ */
+semicrf_status semicrf_linear_attention_step(const semicrf_attention_dims *dims, const void *q, const void *k,
+                                             const void *v, const float *log_decay, float *state, void *o,
+                                             void *stream);
+
+/* Activations of the group norm. */
+#define SEMICRF_ACT_NONE 0
+#define SEMICRF_ACT_SILU 1 /* z / (1 + exp(-z)) */
+#define SEMICRF_ACT_GELU 2 /* z Phi(z), Phi the normal distribution function */
+
+/*
+ * Group norm with an activation, channels last:
+ *   y[n,s,c] = act(xh w[c] + b[c]),   xh = (x[n,s,c] - mean[n,g]) rstd[n,g]
+ * with mean and variance over the positions s < L_n and the C/G channels of c's
+ * group g, rstd = 1 / sqrt(variance + eps).
+ *   x, y      dtype [N, S, C], contiguous
+ *   weight, bias  [C] in float32 or in x's dtype (both the same), or NULL (1 and 0)
+ *   lengths   int32 [N] in [0, S], or NULL (all S); y = 0 at s >= L_n, where nothing
+ *             is read
+ *   stats     float32 [N, G, 2]: mean and rstd, kept for the backward
+ */
+typedef struct {
+    int32_t N, S, C, G;
+    int32_t dtype;        /* SEMICRF_F32, _BF16 or _F16 */
+    int32_t weight_dtype; /* SEMICRF_F32 or dtype */
+    int32_t activation;
+    float eps;
+} semicrf_norm_dims;
+
+size_t semicrf_group_norm_workspace_bytes(const semicrf_norm_dims *dims, int32_t backward);
+
+semicrf_status semicrf_group_norm(const semicrf_norm_dims *dims, const void *x, const void *weight, const void *bias,
+                                  const int32_t *lengths, void *y, float *stats, void *ws, size_t ws_bytes,
+                                  void *stream);
+
+/* Gradients for the upstream dy (dtype [N, S, C], contiguous): dx (0 at s >= L_n),
+ * and float32 [C] dweight and dbias (either may be NULL), summed over n and s. */
+semicrf_status semicrf_group_norm_backward(const semicrf_norm_dims *dims, const void *dy, const void *x,
+                                           const void *weight, const void *bias, const int32_t *lengths,
+                                           const float *stats, void *dx, float *dweight, float *dbias, void *ws,
+                                           size_t ws_bytes, void *stream);
+
+/*
+ * One AdamW step over `count` tensors (a host array), in place:
+ *   g = grad_scale grad;  m = beta1 m + (1-beta1) g;  v = beta2 v + (1-beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr (m / (1-beta1^step)) / (sqrt(v / (1-beta2^step)) + eps)
+ * param: float32, bfloat16 or float16; grad: those or float64 (dA and dD of this
+ * library).  exp_avg (m) and exp_avg_sq (v): float32 with NULL scales, or uint8 codes
+ * with a float32 scale for each 256 consecutive values (all tensors of a call alike).
+ * A code's value is scale times a small float of 3 mantissa bits: m has a sign bit
+ * and 4 exponent bits (bias 15), v 5 exponent bits (bias 31); a block's scale is its
+ * largest magnitude / 1.875, codes are nearest even, and a v above 0 has a code above 0.
+ * A block with a value that is not finite reads as NaN from then on.
+ * step counts from 1; step_ptr (int64) and lr_ptr (float32), where not NULL, are
+ * device scalars read by the kernel instead of step and lr, so that a captured step
+ * follows them.  Tensors must not overlap.
+ */
+typedef struct {
+    void *param;
+    const void *grad;
+    void *exp_avg, *exp_avg_sq;
+    float *exp_avg_scale, *exp_avg_sq_scale; /* ceil(n / 256) floats each, or NULL */
+    int64_t n;
+    int32_t param_dtype, grad_dtype;
+} semicrf_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay, grad_scale;
+    int64_t step;
+    const int64_t *step_ptr;
+    const float *lr_ptr;
+} semicrf_adamw_config;
+
+semicrf_status semicrf_adamw(const semicrf_adamw_tensor *tensors, int32_t count, const semicrf_adamw_config *config,
+                             void *stream);
+
+/* The values 8-bit states stand for: exp_avg (second = 0) or exp_avg_sq (second = 1)
+ * of every tensor, written in float32 to its `param` [n]. */
+semicrf_status semicrf_adamw_state_values(const semicrf_adamw_tensor *tensors, int32_t count, int32_t second,
+                                          void *stream);
+
 /* Zero the device status word in ws (asynchronous on stream). */
 semicrf_status semicrf_clear_device_status(void *ws, void *stream);
 

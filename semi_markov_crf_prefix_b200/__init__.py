@@ -24,7 +24,23 @@ __all__ = ["workspace_bytes", "new_workspace", "new_host_stage", "forward_backwa
            "posteriors", "gold_score", "gold_backward", "nll", "nll_backward", "semicrf_nll",
            "logz_and_grads", "device_status", "clear_device_status", "last_launch_count",
            "SemiCRFError", "status_string", "MAX_C", "MAX_K", "WS_TRAIN", "WS_VITERBI", "WS_SCAN",
-           "load_library", "chain_plan"]
+           "load_library", "chain_plan",
+           "linear_attention", "linear_attention_forward", "linear_attention_backward", "linear_attention_step",
+           "linear_attention_workspace_bytes", "group_norm", "group_norm_forward", "group_norm_backward",
+           "group_norm_workspace_bytes", "adamw_step", "adamw_state_values", "new_adamw_state"]
+
+# the operators around the loss import torch when first used, as the rest of this module does
+_LAZY = {name: "encoder" for name in __all__ if name.startswith(("linear_attention", "group_norm"))}
+_LAZY.update({name: "optim" for name in __all__ if "adamw" in name})
+
+
+def __getattr__(name):
+    if name in _LAZY:
+        import importlib
+        value = getattr(importlib.import_module("." + _LAZY[name], __name__), name)
+        globals()[name] = value
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def load_library():

@@ -1,0 +1,435 @@
+// adamw.cu -- one AdamW step over many tensors in one launch:
+//   m = b1 m + (1-b1) g,  v = b2 v + (1-b2) g^2,
+//   p = p (1 - lr wd) - lr (m / (1-b1^t)) / (sqrt(v / (1-b2^t)) + eps)
+// with the states m, v in float32 or in 8 bits.
+//
+// 8 bits: 256 consecutive values share a float32 scale, their largest magnitude / 1.875.
+// A code is a small float with 3 mantissa bits, nearest even; m: sign and 4 exponent
+// bits (bias 15), v: 5 exponent bits (bias 31), so that v keeps the square of m's range;
+// a v that is not zero never gets code 0, which would make the next step's quotient huge.
+// The moments are formed in float64: a value next to the border of two codes then falls
+// on the side the formula says, and 3 conversions and 7 float64 operations a value stay
+// below the time of its 16 bytes.
+#include <math.h>
+
+#include "device_util.cuh"
+#include "encoder_internal.h"
+
+namespace semicrf {
+namespace {
+
+constexpr int kThreads = 256, kPer = 8;            // values of one thread at a time
+constexpr int kBlock = 256;                        // values that share a scale
+constexpr int kSpan = 2 * kThreads * kPer;         // values of one thread block
+constexpr int kFew = 48, kMany = 448;              // tensors of one launch (3.4 and 32 KB of arguments)
+
+struct Entry {
+    semicrf_adamw_tensor t;
+    long long first;   // first thread block
+};
+
+template <int N>
+struct AdamArgs {
+    Entry e[N];
+    int count;
+    semicrf_adamw_config c;
+};
+
+template <typename R, typename T>
+__device__ __forceinline__ R cvt(T v)
+{
+    if constexpr (sizeof(T) == 2)
+        return (R)to_f<T>(v);
+    else
+        return (R)v;
+}
+
+// 8 values from index i on (cnt of them exist); vec: whole and 16-byte aligned.
+template <typename R, typename T>
+__device__ __forceinline__ void load8(const void *p, long long i, int cnt, bool vec, R (&o)[kPer])
+{
+    const T *s = static_cast<const T *>(p) + i;
+    constexpr int n = 16 / sizeof(T);
+    if (vec) {
+        Pack<T, n> h[kPer / n];
+#pragma unroll
+        for (int j = 0; j < kPer / n; ++j) h[j] = reinterpret_cast<const Pack<T, n> *>(s)[j];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) o[j] = cvt<R, T>(h[j / n].v[j % n]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) o[j] = j < cnt ? cvt<R, T>(s[j]) : (R)0;
+    }
+}
+
+template <typename R>
+__device__ __forceinline__ void load_as(const void *p, int type, long long i, int cnt, bool vec, R (&o)[kPer])
+{
+    if (type == SEMICRF_F32)
+        load8<R, float>(p, i, cnt, vec, o);
+    else if (type == SEMICRF_BF16)
+        load8<R, __nv_bfloat16>(p, i, cnt, vec, o);
+    else if (type == SEMICRF_F16)
+        load8<R, __half>(p, i, cnt, vec, o);
+    else
+        load8<R, double>(p, i, cnt, vec, o);
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(void *p, long long i, int cnt, bool vec, const float (&o)[kPer])
+{
+    T *s = static_cast<T *>(p) + i;
+    constexpr int n = 16 / sizeof(T);
+    if (vec) {
+#pragma unroll
+        for (int j = 0; j < kPer / n; ++j) {
+            Pack<T, n> h;
+#pragma unroll
+            for (int e = 0; e < n; ++e) h.v[e] = from_f<T>(o[j * n + e]);
+            reinterpret_cast<Pack<T, n> *>(s)[j] = h;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (j < cnt) s[j] = from_f<T>(o[j]);
+    }
+}
+
+__device__ __forceinline__ bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Code of y >= 0: exponent bits over 3 mantissa bits, nearest even, from the double's
+// bits (the low word only decides ties).
+template <int BIAS>
+__device__ __forceinline__ uint32_t code_of(double y)
+{
+    const uint32_t hi = (uint32_t)__double2hiint(y);
+    if ((int)(hi >> 20) - 1023 + BIAS < 1) return (uint32_t)__double2int_rn(y * pow2(BIAS + 2));
+    const uint32_t h = hi | (__double2loint(y) != 0);
+    return ((h + 0xffffu + ((h >> 17) & 1u)) >> 17) - ((1023u - BIAS) << 3);
+}
+
+// The value of a code, without its block's scale.
+template <int BIAS>
+__device__ __forceinline__ double value_of(uint32_t c)
+{
+    const uint32_t e = c >> 3, f = c & 7;
+    const double v = __hiloint2double((int)(((max(e, 1u) + 1023u - BIAS) << 20) | (f << 17)), 0);
+    return e ? v : v - pow2(1 - BIAS);
+}
+
+__device__ __forceinline__ float block_scale(float most)
+{
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+    return (float)((double)__uint_as_float(bits) / 1.875);
+}
+
+struct Factors {
+    float b1, b2, n1, n2, decay, lr, root2, eps;
+};
+
+__device__ __forceinline__ float next_param(float p, float m, float v, const Factors &f)
+{
+    return fmaf(p, f.decay, -f.lr * m / fmaf(sqrtf(v), f.root2, f.eps));
+}
+
+// One call of a warp: 256 consecutive values, which is one block of scales.
+__device__ __forceinline__ void step8(const semicrf_adamw_tensor &t, const semicrf_adamw_config &c, const Factors &f,
+                                      long long i, int cnt, bool vec, float (&p)[kPer])
+{
+    double g[kPer];
+    load_as<double>(t.grad, t.grad_dtype, i, cnt, vec, g);
+    const int lane = threadIdx.x & 31;
+    const long long blk = (i - lane * kPer) / kBlock;
+    const bool any = cnt > 0;
+    uint8_t *mc = static_cast<uint8_t *>(t.exp_avg) + i, *vc = static_cast<uint8_t *>(t.exp_avg_sq) + i;
+    Pack<uint8_t, 8> cm, cv;
+    const bool wide = vec && reinterpret_cast<uintptr_t>(mc) % 8 == 0 && reinterpret_cast<uintptr_t>(vc) % 8 == 0;
+    if (wide) {
+        cm = *reinterpret_cast<const Pack<uint8_t, 8> *>(mc);
+        cv = *reinterpret_cast<const Pack<uint8_t, 8> *>(vc);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            cm.v[j] = j < cnt ? mc[j] : 0;
+            cv.v[j] = j < cnt ? vc[j] : 0;
+        }
+    }
+    // a warp enters with its first lane inside the tensor, so the block's scale exists
+    const double sm = t.exp_avg_scale[blk], sv = t.exp_avg_sq_scale[blk];
+    const double n1 = 1.0 - c.beta1, n2 = 1.0 - c.beta2;
+    double m[kPer], v[kPer];
+    float mm = 0.f, mv = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        double gj = g[j] * c.grad_scale;
+        double old = value_of<15>(cm.v[j] & 127u);
+        old = cm.v[j] & 128u ? -old : old;
+        m[j] = fma(n1, gj, c.beta1 * (old * sm));
+        v[j] = fma(n2 * gj, gj, c.beta2 * (value_of<31>(cv.v[j]) * sv));
+        const float fm = (float)m[j], fv = (float)v[j];
+        p[j] = next_param(p[j], fm, fv, f);
+        mm = __uint_as_float(max(__float_as_uint(mm), __float_as_uint(fabsf(fm))));   // NaN above infinity
+        mv = __uint_as_float(max(__float_as_uint(mv), __float_as_uint(fabsf(fv))));
+    }
+    const float scm = block_scale(mm), scv = block_scale(mv);
+    const double im = scm > 0.f ? 1.0 / (double)scm : scm == 0.f ? 0.0 : (double)scm;
+    const double iv = scv > 0.f ? 1.0 / (double)scv : scv == 0.f ? 0.0 : (double)scv;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const uint32_t a = min(code_of<15>(fabs(m[j]) * im), 127u);
+        uint32_t b = min(code_of<31>(v[j] * iv), 255u);
+        if (v[j] > 0.0 && scv > 0.f) b = max(b, 1u);
+        cm.v[j] = (uint8_t)(a | (m[j] < 0.0 ? 128u : 0u));
+        cv.v[j] = (uint8_t)b;
+    }
+    if (wide) {
+        *reinterpret_cast<Pack<uint8_t, 8> *>(mc) = cm;
+        *reinterpret_cast<Pack<uint8_t, 8> *>(vc) = cv;
+    } else if (any) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (j < cnt) {
+                mc[j] = cm.v[j];
+                vc[j] = cv.v[j];
+            }
+    }
+    __syncwarp();
+    if (lane == 0) {
+        t.exp_avg_scale[blk] = scm;
+        t.exp_avg_sq_scale[blk] = scv;
+    }
+}
+
+__device__ __forceinline__ void step32(const semicrf_adamw_tensor &t, const semicrf_adamw_config &c, const Factors &f,
+                                       long long i, int cnt, bool vec, float (&p)[kPer])
+{
+    float g[kPer], m[kPer], v[kPer];
+    load_as<float>(t.grad, t.grad_dtype, i, cnt, vec, g);
+    load8<float, float>(t.exp_avg, i, cnt, vec, m);
+    load8<float, float>(t.exp_avg_sq, i, cnt, vec, v);
+    const float gs = (float)c.grad_scale;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const float gj = g[j] * gs;
+        m[j] = fmaf(f.b1, m[j], f.n1 * gj);
+        v[j] = fmaf(f.b2, v[j], f.n2 * gj * gj);
+        p[j] = next_param(p[j], m[j], v[j], f);
+    }
+    store8<float>(t.exp_avg, i, cnt, vec, m);
+    store8<float>(t.exp_avg_sq, i, cnt, vec, v);
+}
+
+template <int N>
+__device__ __forceinline__ int entry_of(const AdamArgs<N> &a, long long block)
+{
+    int lo = 0, hi = a.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (a.e[mid].first <= block)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+template <int N, bool EIGHT>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(const __grid_constant__ AdamArgs<N> a)
+{
+    const Entry &en = a.e[entry_of<N>(a, blockIdx.x)];
+    const semicrf_adamw_tensor &t = en.t;
+    const semicrf_adamw_config &c = a.c;
+    __shared__ Factors sf;
+    if (threadIdx.x == 0) {
+        const double step = (double)(c.step_ptr ? *c.step_ptr : c.step), lr = c.lr_ptr ? (double)*c.lr_ptr : c.lr;
+        sf.b1 = (float)c.beta1;
+        sf.b2 = (float)c.beta2;
+        sf.n1 = (float)(1.0 - c.beta1);
+        sf.n2 = (float)(1.0 - c.beta2);
+        sf.decay = (float)(1.0 - lr * c.weight_decay);
+        sf.lr = (float)(lr / (1.0 - pow(c.beta1, step)));
+        sf.root2 = (float)(1.0 / sqrt(1.0 - pow(c.beta2, step)));
+        sf.eps = (float)c.eps;
+    }
+    __syncthreads();
+    const Factors f = sf;
+    const bool all = aligned16(t.param) && aligned16(t.grad) &&
+                     (EIGHT || (aligned16(t.exp_avg) && aligned16(t.exp_avg_sq)));
+    const long long from = (blockIdx.x - en.first) * (long long)kSpan;
+#pragma unroll 1
+    for (int k = 0; k < kSpan / (kThreads * kPer); ++k) {
+        const long long i = from + (long long)k * kThreads * kPer + threadIdx.x * kPer;
+        // whole warps leave together: 256 values, one block of scales
+        if (i - (threadIdx.x & 31) * kPer >= t.n) break;
+        const int cnt = (int)max(0LL, min((long long)kPer, t.n - i));
+        const bool vec = all && cnt == kPer;
+        float p[kPer];
+        load_as<float>(t.param, t.param_dtype, i, cnt, vec, p);
+        if (EIGHT)
+            step8(t, c, f, i, cnt, vec, p);
+        else
+            step32(t, c, f, i, cnt, vec, p);
+        if (t.param_dtype == SEMICRF_F32)
+            store8<float>(t.param, i, cnt, vec, p);
+        else if (t.param_dtype == SEMICRF_BF16)
+            store8<__nv_bfloat16>(t.param, i, cnt, vec, p);
+        else
+            store8<__half>(t.param, i, cnt, vec, p);
+    }
+}
+
+// Codes to the values they stand for: t.param receives exp_avg (or exp_avg_sq) in float32.
+template <int N, bool SECOND>
+__global__ __launch_bounds__(kThreads) void adamw_values_kernel(const __grid_constant__ AdamArgs<N> a)
+{
+    const Entry &en = a.e[entry_of<N>(a, blockIdx.x)];
+    const semicrf_adamw_tensor &t = en.t;
+    const uint8_t *codes = static_cast<const uint8_t *>(SECOND ? t.exp_avg_sq : t.exp_avg);
+    const float *scale = SECOND ? t.exp_avg_sq_scale : t.exp_avg_scale;
+    const long long from = (blockIdx.x - en.first) * (long long)kSpan;
+#pragma unroll
+    for (int k = 0; k < kSpan / (kThreads * kPer); ++k) {
+        const long long i = from + (long long)k * kThreads * kPer + threadIdx.x * kPer;
+        if (i >= t.n) break;
+        const int cnt = (int)min((long long)kPer, t.n - i);
+        const float s = scale[i / kBlock];
+        const bool vec = cnt == kPer && aligned16(t.param);
+        Pack<uint8_t, 8> c;
+        if (vec && reinterpret_cast<uintptr_t>(codes + i) % 8 == 0) {
+            c = *reinterpret_cast<const Pack<uint8_t, 8> *>(codes + i);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) c.v[j] = j < cnt ? codes[i + j] : 0;
+        }
+        float o[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const float mag = (float)(SECOND ? value_of<31>(c.v[j]) : value_of<15>(c.v[j] & 127u)) * s;
+            o[j] = !SECOND && (c.v[j] & 128u) ? -mag : mag;
+        }
+        store8<float>(t.param, i, cnt, vec, o);
+    }
+}
+
+template <int N, typename F>
+cudaError_t launch_some(const semicrf_adamw_tensor *t, int count, const semicrf_adamw_config &c, cudaStream_t st, int *n,
+                        F &&kernel)
+{
+    static thread_local AdamArgs<N> a;   // 32 KB at most: kept off the stack
+    a.c = c;
+    a.count = 0;
+    long long blocks = 0;
+    for (int i = 0; i < count; ++i) {
+        if (t[i].n == 0) continue;
+        a.e[a.count].t = t[i];
+        a.e[a.count++].first = blocks;
+        blocks += (t[i].n + kSpan - 1) / kSpan;
+    }
+    if (!blocks) return cudaSuccess;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    prof_before(st);
+    kernel(a, (unsigned)blocks);
+    prof_after(st);
+    ++*n;
+    return cudaGetLastError();
+}
+
+template <typename F>
+cudaError_t launch_all(const semicrf_adamw_tensor *t, int count, const semicrf_adamw_config &c, cudaStream_t st, int *n,
+                       F &&kernel)
+{
+    *n = 0;
+    for (int i = 0; i < count;) {
+        const int left = count - i;
+        cudaError_t e;
+        if (left <= kFew) {
+            e = launch_some<kFew>(t + i, left, c, st, n, kernel);
+            i = count;
+        } else {
+            const int some = left < kMany ? left : kMany;
+            e = launch_some<kMany>(t + i, some, c, st, n, kernel);
+            i += some;
+        }
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+semicrf_status ended(cudaError_t e, int launches)
+{
+    if (e != cudaSuccess) return SEMICRF_ERR_CUDA;
+    record_launches(launches);
+    return SEMICRF_OK;
+}
+
+bool tensors_ok(const semicrf_adamw_tensor *t, int count)
+{
+    if (count < 0 || (count > 0 && !t)) return false;
+    for (int i = 0; i < count; ++i)
+        if (t[i].n < 0) return false;
+    return true;
+}
+
+}  // namespace
+}  // namespace semicrf
+
+using namespace semicrf;
+
+extern "C" semicrf_status semicrf_adamw(const semicrf_adamw_tensor *tensors, int32_t count,
+                                        const semicrf_adamw_config *config, void *stream)
+{
+    prof_reset();
+    if (!config || !tensors_ok(tensors, count)) return SEMICRF_ERR_INVALID_ARG;
+    const semicrf_adamw_config &c = *config;
+    // (negated comparisons: NaN is refused too)
+    if (!(c.beta1 >= 0.0 && c.beta1 < 1.0) || !(c.beta2 >= 0.0 && c.beta2 < 1.0) || !(c.eps >= 0.0) ||
+        !(c.weight_decay >= 0.0) || !isfinite(c.grad_scale) || (!c.lr_ptr && !(c.lr >= 0.0)) ||
+        (!c.step_ptr && c.step < 1))
+        return SEMICRF_ERR_INVALID_ARG;
+    int eight = 0, filled = 0;
+    for (int i = 0; i < count; ++i) {
+        const semicrf_adamw_tensor &t = tensors[i];
+        if (t.param_dtype < SEMICRF_F32 || t.param_dtype > SEMICRF_F16 || t.grad_dtype < SEMICRF_F32 ||
+            t.grad_dtype > SEMICRF_F64)
+            return SEMICRF_ERR_INVALID_ARG;
+        if (t.n == 0) continue;
+        if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq || !t.exp_avg_scale != !t.exp_avg_sq_scale)
+            return SEMICRF_ERR_INVALID_ARG;
+        ++filled;
+        eight += t.exp_avg_scale != nullptr;
+    }
+    if (eight && eight != filled) return SEMICRF_ERR_INVALID_ARG;   // one kind of state a call
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int n = 0;
+    cudaError_t e = launch_all(tensors, count, c, st, &n, [&](const auto &a, unsigned blocks) {
+        constexpr int N = sizeof(a.e) / sizeof(Entry);
+        if (eight)
+            adamw_kernel<N, true><<<blocks, kThreads, 0, st>>>(a);
+        else
+            adamw_kernel<N, false><<<blocks, kThreads, 0, st>>>(a);
+    });
+    return ended(e, n);
+}
+
+extern "C" semicrf_status semicrf_adamw_state_values(const semicrf_adamw_tensor *tensors, int32_t count, int32_t second,
+                                                     void *stream)
+{
+    prof_reset();
+    if (!tensors_ok(tensors, count) || (second != 0 && second != 1)) return SEMICRF_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {
+        const semicrf_adamw_tensor &t = tensors[i];
+        if (t.n && (!t.param || !(second ? t.exp_avg_sq : t.exp_avg) || !(second ? t.exp_avg_sq_scale : t.exp_avg_scale)))
+            return SEMICRF_ERR_INVALID_ARG;
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int n = 0;
+    const semicrf_adamw_config none = {};
+    cudaError_t e = launch_all(tensors, count, none, st, &n, [&](const auto &a, unsigned blocks) {
+        constexpr int N = sizeof(a.e) / sizeof(Entry);
+        if (second)
+            adamw_values_kernel<N, true><<<blocks, kThreads, 0, st>>>(a);
+        else
+            adamw_values_kernel<N, false><<<blocks, kThreads, 0, st>>>(a);
+    });
+    return ended(e, n);
+}

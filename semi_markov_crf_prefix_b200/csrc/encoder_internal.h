@@ -1,0 +1,110 @@
+// encoder_internal.h -- what the translation units of the operators around the loss
+// (linear attention, group norm, AdamW) share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "semicrf.h"
+
+namespace semicrf {
+
+void prof_reset();
+void prof_before(cudaStream_t st);
+void prof_after(cudaStream_t st);
+void record_launches(int n);
+int device_sm_count();
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f<double>(double v) { return (float)v; }
+
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+// N values as one load or store of N * sizeof(T) bytes (16 at most), which the address must be aligned to.
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Pack {
+    T v[N];
+};
+
+// ---- linear attention ----
+
+// One walk over all sequences and heads: S_p = lam S_{p-1} + c k_p v_p^T, o_p = b q_p S_p.  The forward is
+// one walk; the backward is three (exchanged operands, two of them against the direction of time).
+struct LaWalk {
+    const void *q, *k, *v;
+    void *o;
+    long long qs[3], ks[3], vs[3], os[3];   // strides of sequence, position, head (elements); the last axis is dense
+    int dk, dv;
+    const float *s_in;                      // [B,H] states, element (i,j) at i * s_rs + j * s_cs, or null
+    float *s_out;                           // same addressing, or null
+    int s_rs, s_cs;
+    float *seg;                             // [B,H,nseg] states at the segments' starts (dk x dv), or null
+    float b, c;
+    int reverse;                            // walk from the last valid position to the first
+    int lead;                               // power of lam the given state has at the first position
+    int out_decay;                          // s_out takes one more factor lam
+    int q_vec, k_vec, v_vec, o_vec;         // whole 8-value pieces can be moved in one (two) 16-byte accesses
+};
+
+struct LaArgs {
+    LaWalk w[3];
+    int nwalk;
+    int B, T, H;
+    int nseg, seg_len;                      // segments of seg_len positions (whole sequences when nseg == 1)
+    const float *log_decay;
+    const int32_t *lengths;                 // or null
+    int32_t *status;
+};
+
+struct LaStepArgs {
+    const void *q, *k, *v;
+    void *o;
+    long long qs[2], ks[2], vs[2], os[2];   // strides of sequence and head
+    float *state;
+    const float *log_decay;
+    int B, H, dk, dv;
+    float scale;
+};
+
+int la_segments(int B, int T, int H, int dk, int dv, int dtype, int nwalk, int *seg_len);
+cudaError_t launch_la(const LaArgs &a, int dtype, cudaStream_t st, int *launches);
+cudaError_t launch_la_step(const LaStepArgs &a, int dtype, cudaStream_t st, int *launches);
+
+// ---- group norm ----
+
+struct NormArgs {
+    int N, S, C, G;
+    int act, wdtype;
+    float eps;
+    const void *x, *dy;
+    const void *weight, *bias;              // [C] or null
+    const int32_t *lengths;                 // [N] or null
+    void *y;                                // y, or dx in the backward
+    float *stats;                           // [N,G,2] mean and 1/std
+    float *dw, *db;                         // [C]
+    double *part;                           // scratch
+    int32_t *status;
+};
+
+size_t norm_scratch(int N, int S, int C, int G, int dtype, bool backward);
+cudaError_t launch_norm(const NormArgs &a, int dtype, bool backward, cudaStream_t st, int *launches);
+
+}  // namespace semicrf

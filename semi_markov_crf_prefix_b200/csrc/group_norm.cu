@@ -1,0 +1,596 @@
+// group_norm.cu -- group norm with an activation on channels-last rows x [N][S][C]:
+//   y = act(xh w_c + b_c),  xh = (x - mu_{n,g}) rstd_{n,g},
+// statistics over the valid positions s < L_n and the C/G channels of group g, and its
+// gradient  dz = dy act'(z),  dx = rstd (w dz - mean(w dz) - xh mean(w dz xh)),
+// dw_c = sum dz xh,  db_c = sum dz.
+#include <math.h>
+
+#include "device_util.cuh"
+#include "encoder_internal.h"
+
+namespace semicrf {
+namespace {
+
+// ---- the elementwise part ----
+
+__device__ __forceinline__ float activate(float z, int act)
+{
+    if (act == SEMICRF_ACT_SILU) return z / (1.f + expf(-z));
+    if (act == SEMICRF_ACT_GELU) return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    return z;
+}
+
+__device__ __forceinline__ float slope(float z, int act)
+{
+    if (act == SEMICRF_ACT_SILU) {
+        const float s = 1.f / (1.f + expf(-z));
+        return s * fmaf(z, 1.f - s, 1.f);
+    }
+    if (act == SEMICRF_ACT_GELU)
+        return fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), 0.5f * erfcf(-0.70710678118654752f * z));
+    return 1.f;
+}
+
+template <typename T>
+__device__ __forceinline__ float weight_at(const void *p, int wdtype, int c, float none)
+{
+    if (!p) return none;
+    return wdtype == SEMICRF_F32 ? static_cast<const float *>(p)[c] : to_f<T>(static_cast<const T *>(p)[c]);
+}
+
+__device__ __forceinline__ int norm_length(const NormArgs &a, int n)
+{
+    if (!a.lengths) return a.S;
+    const int L = a.lengths[n];
+    if (L < 0 || L > a.S) {
+        set_status(a.status, SEMICRF_ERR_INVALID_LENGTH);
+        return max(0, min(L, a.S));
+    }
+    return L;
+}
+
+// ---- rows that fit a block's registers ----
+//
+// Thread (r, col) holds U vectors of VEC channels: rows rl, rl + RL, ... of row block n.
+// NB row blocks lie side by side in a thread block, RL lanes of rows in each.  One read of
+// x (and dy), the statistics from registers in two exact passes (mean, then squares about
+// it), one write.
+struct RegShape {
+    int CV, RL, NB, W;   // vectors a row; row lanes a block; row blocks a thread block; lanes that sum one group
+};
+
+constexpr int kRegThreads = 512;
+
+template <typename V>
+__device__ __forceinline__ V warp_sum(V v, int width)
+{
+    for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Sums red[r][col] over a group's columns and its row block's lanes, for every (row block, group), into out.
+__device__ __forceinline__ void group_sums(const float *red, float *out, const RegShape &sh, int G, int CgV)
+{
+    const int per = kRegThreads / sh.W, w = threadIdx.x % sh.W, items = sh.RL * CgV;
+    for (int base = 0; base < sh.NB * G; base += per) {
+        const int o = base + threadIdx.x / sh.W;
+        float s = 0.f;
+        if (o < sh.NB * G) {
+            const int nb = o / G, g = o % G;
+            for (int i = w; i < items; i += sh.W) s += red[(nb * sh.RL + i / CgV) * sh.CV + g * CgV + i % CgV];
+        }
+        s = warp_sum(s, sh.W);
+        if (w == 0 && o < sh.NB * G) out[o] = s;
+    }
+}
+
+template <typename T, int VEC, int U, bool BWD>
+__global__ __launch_bounds__(kRegThreads) void norm_reg_kernel(const __grid_constant__ NormArgs a, const RegShape sh)
+{
+    extern __shared__ float shm[];
+    float *red = shm, *red2 = red + kRegThreads, *mean = red2 + kRegThreads, *aux = mean + sh.NB * a.G;
+    const int tid = threadIdx.x, col = tid % sh.CV, r = tid / sh.CV, nb = r / sh.RL, rl = r % sh.RL;
+    const bool mine = nb < sh.NB;
+    const int Cg = a.C / a.G, CgV = Cg / VEC, c0 = col * VEC, g = c0 / Cg;
+    float wt[VEC], bs[VEC], dw[VEC], db[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        wt[e] = mine ? weight_at<T>(a.weight, a.wdtype, c0 + e, 1.f) : 0.f;
+        bs[e] = mine ? weight_at<T>(a.bias, a.wdtype, c0 + e, 0.f) : 0.f;
+        dw[e] = db[e] = 0.f;
+    }
+    for (int n0 = blockIdx.x * sh.NB; n0 < a.N; n0 += gridDim.x * sh.NB) {
+        const int n = n0 + nb;
+        const bool on = mine && n < a.N;
+        const int L = on ? norm_length(a, n) : 0;
+        const long long base = ((long long)n * a.S) * a.C + c0;
+        Pack<T, VEC> x[U], dy[BWD ? U : 1];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = rl + u * sh.RL;
+            if (s < L) {
+                x[u] = *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(a.x) + base + (long long)s * a.C);
+                if (BWD)
+                    dy[u] = *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(a.dy) + base +
+                                                                    (long long)s * a.C);
+            }
+        }
+        const float inv = 1.f / fmaxf((float)L * Cg, 1.f);
+        float mu, rs;
+        if (!BWD) {
+            float sum = 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (rl + u * sh.RL < L)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) sum += to_f<T>(x[u].v[e]);
+            red[tid] = sum;
+            __syncthreads();
+            group_sums(red, mean, sh, a.G, CgV);
+            __syncthreads();
+            mu = mine ? mean[nb * a.G + g] * inv : 0.f;
+            sum = 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (rl + u * sh.RL < L)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float d = to_f<T>(x[u].v[e]) - mu;
+                        sum = fmaf(d, d, sum);
+                    }
+            red2[tid] = sum;
+            __syncthreads();
+            group_sums(red2, aux, sh, a.G, CgV);
+            __syncthreads();
+            rs = mine ? 1.f / sqrtf(aux[nb * a.G + g] * inv + a.eps) : 0.f;
+            if (on && a.stats && rl == 0 && c0 % Cg == 0) {
+                float *st = a.stats + 2 * ((long long)n * a.G + g);
+                st[0] = mu;
+                st[1] = rs;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int s = rl + u * sh.RL;
+                if (!on || s >= a.S) continue;
+                Pack<T, VEC> y;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    y.v[e] = from_f<T>(s < L ? activate(fmaf((to_f<T>(x[u].v[e]) - mu) * rs, wt[e], bs[e]), a.act) : 0.f);
+                *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(a.y) + base + (long long)s * a.C) = y;
+            }
+        } else {
+            const float *st = a.stats + 2 * ((long long)(on ? n : 0) * a.G + (mine ? g : 0));
+            mu = st[0];
+            rs = st[1];
+            float s1 = 0.f, s2 = 0.f;
+            float gz[U][VEC];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (rl + u * sh.RL >= L) continue;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float xh = (to_f<T>(x[u].v[e]) - mu) * rs;
+                    const float dz = to_f<T>(dy[u].v[e]) * slope(fmaf(xh, wt[e], bs[e]), a.act);
+                    gz[u][e] = dz * wt[e];
+                    s1 += gz[u][e];
+                    s2 = fmaf(gz[u][e], xh, s2);
+                    dw[e] = fmaf(dz, xh, dw[e]);
+                    db[e] += dz;
+                }
+            }
+            red[tid] = s1;
+            red2[tid] = s2;
+            __syncthreads();
+            group_sums(red, mean, sh, a.G, CgV);
+            group_sums(red2, aux, sh, a.G, CgV);
+            __syncthreads();
+            s1 = mine ? mean[nb * a.G + g] * inv : 0.f;
+            s2 = mine ? aux[nb * a.G + g] * inv : 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int s = rl + u * sh.RL;
+                if (!on || s >= a.S) continue;
+                Pack<T, VEC> y;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float xh = (to_f<T>(x[u].v[e]) - mu) * rs;
+                    y.v[e] = from_f<T>(s < L ? rs * (gz[u][e] - s1 - xh * s2) : 0.f);
+                }
+                *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(a.y) + base + (long long)s * a.C) = y;
+            }
+        }
+        __syncthreads();   // the sums' buffers serve the next row blocks
+    }
+    if (BWD) {
+        // this block's share of dw and db: part[block][2][C]
+        float *acc = shm;   // [rows][2] of one channel vector element at a time
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            __syncthreads();
+            acc[tid] = mine ? dw[e] : 0.f;
+            acc[kRegThreads + tid] = mine ? db[e] : 0.f;
+            __syncthreads();
+            if (r == 0) {
+                double sw = 0.0, sb = 0.0;
+                for (int j = col; j < sh.NB * sh.RL * sh.CV; j += sh.CV) {
+                    sw += (double)acc[j];
+                    sb += (double)acc[kRegThreads + j];
+                }
+                double *p = a.part + (long long)blockIdx.x * 2 * a.C + c0 + e;
+                p[0] = sw;
+                p[a.C] = sb;
+            }
+        }
+    }
+}
+
+// dw[c], db[c] from P rows of partial sums [P][2][C]: 32 channels and 8 strands of rows a block.
+__global__ void norm_params_kernel(const double *part, int P, int C, float *dw, float *db)
+{
+    __shared__ double sh[2][8][32];
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    double w = 0.0, b = 0.0;
+    if (c < C) {
+#pragma unroll 4
+        for (int i = threadIdx.y; i < P; i += 8) {
+            w += part[(long long)i * 2 * C + c];
+            b += part[(long long)i * 2 * C + C + c];
+        }
+    }
+    sh[0][threadIdx.y][threadIdx.x] = w;
+    sh[1][threadIdx.y][threadIdx.x] = b;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < C) {
+        for (int j = 1; j < 8; ++j) {
+            w += sh[0][j][threadIdx.x];
+            b += sh[1][j][threadIdx.x];
+        }
+        if (dw) dw[c] = (float)w;
+        if (db) db[c] = (float)b;
+    }
+}
+
+// ---- long rows: two passes over the data ----
+//
+// Pass 1: per-channel sums of a strip of positions, part[n][strip][2][C] in float64
+// (forward: x and x^2; backward: dz xh and dz).  Eight rows at a time are summed in
+// float32 about their own mean before they enter float64, so a large mean costs nothing.
+// Then the groups' statistics, then pass 2 writes y or dx, strips in the opposite
+// order: the ones that pass 1 read last are still in the L2 cache.
+constexpr int kLongThreads = 256, kBatch = 8;
+
+struct LongShape {
+    int CV, tiles, R, strips, rows;   // vectors a row, column tiles of <= 256 of them, row lanes, strips, rows a strip
+};
+
+template <typename T, int VEC, bool BWD>
+__global__ __launch_bounds__(kLongThreads) void norm_sums_kernel(const __grid_constant__ NormArgs a, const LongShape sh)
+{
+    extern __shared__ double dsm[];
+    const int cols = min(sh.CV, kLongThreads), tid = threadIdx.x, r = tid / cols;
+    const int cv = blockIdx.y * kLongThreads + tid % cols, n = blockIdx.x / sh.strips, strip = blockIdx.x % sh.strips;
+    const bool mine = r < sh.R && cv < sh.CV;
+    const int L = norm_length(a, n), s0 = strip * sh.rows, s1 = min(L, s0 + sh.rows), c0 = cv * VEC;
+    const long long base = (long long)n * a.S * a.C + c0;
+    double A[VEC], B[VEC];
+    float wt[VEC], bs[VEC], mu[VEC], rs[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        A[e] = B[e] = 0.0;
+        if (BWD && mine) {
+            wt[e] = weight_at<T>(a.weight, a.wdtype, c0 + e, 1.f);
+            bs[e] = weight_at<T>(a.bias, a.wdtype, c0 + e, 0.f);
+            const float *st = a.stats + 2 * ((long long)n * a.G + (c0 + e) / (a.C / a.G));
+            mu[e] = st[0];
+            rs[e] = st[1];
+        }
+    }
+    if (mine) {
+        for (int s = s0 + r; s < s1; s += sh.R * kBatch) {
+            Pack<T, VEC> x[kBatch], dy[BWD ? kBatch : 1];
+            int cnt = 0;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (s + u * sh.R < s1) {
+                    const long long at = base + (long long)(s + u * sh.R) * a.C;
+                    x[u] = *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(a.x) + at);
+                    if (BWD) dy[u] = *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(a.dy) + at);
+                    ++cnt;
+                }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float p = 0.f, q = 0.f;
+                if (!BWD) {
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u)
+                        if (u < cnt) p += to_f<T>(x[u].v[e]);
+                    const float m = p / cnt;
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u)
+                        if (u < cnt) {
+                            const float d = to_f<T>(x[u].v[e]) - m;
+                            q = fmaf(d, d, q);
+                        }
+                    // sum of squares about zero, exact in float64 where float32 would cancel:
+                    // sum (x - m)^2 + 2 m sum x - cnt m^2
+                    const double dm = m, dp = p;
+                    A[e] += dp;
+                    B[e] += (double)q + dm * (2.0 * dp - (double)cnt * dm);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u)
+                        if (u < cnt) {
+                            const float xh = (to_f<T>(x[u].v[e]) - mu[e]) * rs[e];
+                            const float dz = to_f<T>(dy[u].v[e]) * slope(fmaf(xh, wt[e], bs[e]), a.act);
+                            p = fmaf(dz, xh, p);
+                            q += dz;
+                        }
+                    A[e] += (double)p;
+                    B[e] += (double)q;
+                }
+            }
+        }
+    }
+    double *out = a.part + ((long long)n * sh.strips + strip) * 2 * a.C + c0;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        __syncthreads();
+        if (r < sh.R) {
+            dsm[tid] = A[e];
+            dsm[kLongThreads + tid] = B[e];
+        }
+        __syncthreads();
+        if (r == 0 && mine) {
+            double x = 0.0, y = 0.0;
+            for (int j = tid; j < sh.R * cols; j += cols) {
+                x += dsm[j];
+                y += dsm[kLongThreads + j];
+            }
+            out[e] = x;
+            out[a.C + e] = y;
+        }
+    }
+}
+
+// (n, g): mean and 1/std (forward), or the means of w dz and w dz xh (backward, to gsum [N,G,2]).
+template <typename T, bool BWD>
+__global__ void norm_group_kernel(const __grid_constant__ NormArgs a, int strips, float *gsum)
+{
+    const int n = blockIdx.x / a.G, g = blockIdx.x % a.G, Cg = a.C / a.G;
+    const double *part = a.part + (long long)n * strips * 2 * a.C + g * Cg;
+    double A = 0.0, B = 0.0;
+    for (int i = threadIdx.x; i < strips * Cg; i += blockDim.x) {
+        const double *p = part + (long long)(i / Cg) * 2 * a.C + i % Cg;
+        const double w = BWD ? (double)weight_at<T>(a.weight, a.wdtype, g * Cg + i % Cg, 1.f) : 1.0;
+        A += w * p[0];
+        B += w * p[a.C];
+    }
+    __shared__ double sa[32], sb[32];
+    A = warp_sum(A, 32);
+    B = warp_sum(B, 32);
+    if ((threadIdx.x & 31) == 0) {
+        sa[threadIdx.x >> 5] = A;
+        sb[threadIdx.x >> 5] = B;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        A = B = 0.0;
+        for (int j = 0; j < (int)(blockDim.x >> 5); ++j) {
+            A += sa[j];
+            B += sb[j];
+        }
+        const double cnt = fmax((double)norm_length(a, n) * Cg, 1.0);
+        float *o = (BWD ? gsum : a.stats) + 2 * (long long)blockIdx.x;
+        if (BWD) {
+            o[0] = (float)(B / cnt);   // mean of w dz
+            o[1] = (float)(A / cnt);   // mean of w dz xh
+        } else {
+            const double m = A / cnt;
+            o[0] = (float)m;
+            o[1] = (float)(1.0 / sqrt(fmax(B / cnt - m * m, 0.0) + (double)a.eps));
+        }
+    }
+}
+
+template <typename T, int VEC, bool BWD>
+__global__ __launch_bounds__(kLongThreads) void norm_apply_kernel(const __grid_constant__ NormArgs a, const LongShape sh,
+                                                                  const float *gsum)
+{
+    const int cols = min(sh.CV, kLongThreads), tid = threadIdx.x, r = tid / cols;
+    const int cv = blockIdx.y * kLongThreads + tid % cols;
+    const int back = gridDim.x - 1 - blockIdx.x, n = back / sh.strips, strip = back % sh.strips;
+    if (r >= sh.R || cv >= sh.CV) return;
+    const int L = norm_length(a, n), s0 = strip * sh.rows, s1 = min(a.S, s0 + sh.rows), c0 = cv * VEC;
+    const long long base = (long long)n * a.S * a.C + c0;
+    float wt[VEC], bs[VEC], mu[VEC], rs[VEC], g1[VEC], g2[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        wt[e] = weight_at<T>(a.weight, a.wdtype, c0 + e, 1.f);
+        bs[e] = weight_at<T>(a.bias, a.wdtype, c0 + e, 0.f);
+        const long long at = 2 * ((long long)n * a.G + (c0 + e) / (a.C / a.G));
+        mu[e] = a.stats[at];
+        rs[e] = a.stats[at + 1];
+        if (BWD) {
+            g1[e] = gsum[at];
+            g2[e] = gsum[at + 1];
+        }
+    }
+    constexpr int U = BWD ? 4 : 8;
+    for (int s = s0 + r; s < s1; s += sh.R * U) {
+        Pack<T, VEC> x[U], dy[BWD ? U : 1];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s + u * sh.R < min(s1, L)) {
+                const long long at = base + (long long)(s + u * sh.R) * a.C;
+                x[u] = *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(a.x) + at);
+                if (BWD) dy[u] = *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(a.dy) + at);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int p = s + u * sh.R;
+            if (p >= s1) break;
+            Pack<T, VEC> y;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float v = 0.f;
+                if (p < L) {
+                    const float xh = (to_f<T>(x[u].v[e]) - mu[e]) * rs[e], z = fmaf(xh, wt[e], bs[e]);
+                    v = BWD ? rs[e] * (to_f<T>(dy[u].v[e]) * slope(z, a.act) * wt[e] - g1[e] - xh * g2[e])
+                            : activate(z, a.act);
+                }
+                y.v[e] = from_f<T>(v);
+            }
+            *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(a.y) + base + (long long)p * a.C) = y;
+        }
+    }
+}
+
+// ---- launches ----
+
+int pow2_at_least(int v, int most)
+{
+    int p = 1;
+    while (p < v && p < most) p <<= 1;
+    return p;
+}
+
+// The widest vector that stays inside one group: a power of two that divides C/G.
+int norm_vec(int C, int G, int dtype)
+{
+    const int most = dtype == SEMICRF_F32 ? 4 : 8, Cg = C / G;
+    int v = 1;
+    while (v < most && Cg % (2 * v) == 0) v *= 2;
+    return v;
+}
+
+// Registers hold a row block where its rows take at most 32 values a thread.
+bool reg_shape(int S, int C, int G, int vec, RegShape *sh)
+{
+    sh->CV = C / vec;
+    if (sh->CV > kRegThreads) return false;
+    const int R = kRegThreads / sh->CV;
+    sh->RL = R < S ? R : S;
+    sh->NB = R / sh->RL;
+    if ((S + sh->RL - 1) / sh->RL > 32 / vec) return false;
+    sh->W = pow2_at_least(sh->RL * (C / G / vec), 32);
+    return true;
+}
+
+LongShape long_shape(int N, int S, int C, int vec)
+{
+    LongShape sh;
+    sh.CV = C / vec;
+    sh.tiles = (sh.CV + kLongThreads - 1) / kLongThreads;
+    const int cols = sh.CV < kLongThreads ? sh.CV : kLongThreads;
+    sh.R = kLongThreads / cols;
+    // strips: eight blocks an SM over everything, each at least one batch of rows deep
+    long long strips = (8LL * device_sm_count() + (long long)N * sh.tiles - 1) / ((long long)N * sh.tiles);
+    const long long most = (S + sh.R * kBatch - 1) / (sh.R * kBatch);
+    if (strips > most) strips = most;
+    if (strips < 1) strips = 1;
+    sh.rows = (int)((S + strips - 1) / strips);
+    sh.strips = (S + sh.rows - 1) / sh.rows;
+    return sh;
+}
+
+int reg_blocks(int N, const RegShape &sh)
+{
+    const int blocks = (N + sh.NB - 1) / sh.NB, most = 4 * device_sm_count();
+    return blocks < most ? blocks : most;
+}
+
+template <typename F>
+cudaError_t timed_launch(cudaStream_t st, int *n, F &&go)
+{
+    prof_before(st);
+    go();
+    prof_after(st);
+    ++*n;
+    return cudaGetLastError();
+}
+
+template <typename T, int VEC, bool BWD>
+cudaError_t norm_go(NormArgs a, cudaStream_t st, int *n)
+{
+    RegShape rsh;
+    cudaError_t e;
+    int prows;
+    if (reg_shape(a.S, a.C, a.G, VEC, &rsh)) {
+        const int blocks = reg_blocks(a.N, rsh);
+        const size_t smem = (2 * kRegThreads + 2 * (size_t)rsh.NB * a.G) * sizeof(float);
+        e = timed_launch(st, n, [&] {
+            if ((a.S + rsh.RL - 1) / rsh.RL == 1)
+                norm_reg_kernel<T, VEC, 1, BWD><<<blocks, kRegThreads, smem, st>>>(a, rsh);
+            else
+                norm_reg_kernel<T, VEC, 32 / VEC, BWD><<<blocks, kRegThreads, smem, st>>>(a, rsh);
+        });
+        if (e != cudaSuccess) return e;
+        prows = blocks;
+    } else {
+        const LongShape sh = long_shape(a.N, a.S, a.C, VEC);
+        const dim3 grid((unsigned)(a.N * sh.strips), sh.tiles);
+        float *gsum = reinterpret_cast<float *>(a.part + (size_t)a.N * sh.strips * 2 * a.C);
+        e = timed_launch(st, n, [&] {
+            norm_sums_kernel<T, VEC, BWD><<<grid, kLongThreads, 2 * kLongThreads * sizeof(double), st>>>(a, sh);
+        });
+        if (e != cudaSuccess) return e;
+        e = timed_launch(st, n, [&] { norm_group_kernel<T, BWD><<<a.N * a.G, 256, 0, st>>>(a, sh.strips, gsum); });
+        if (e != cudaSuccess) return e;
+        e = timed_launch(st, n, [&] { norm_apply_kernel<T, VEC, BWD><<<grid, kLongThreads, 0, st>>>(a, sh, gsum); });
+        if (e != cudaSuccess) return e;
+        prows = a.N * sh.strips;
+    }
+    if (!BWD || (!a.dw && !a.db)) return cudaSuccess;
+    return timed_launch(st, n, [&] {
+        norm_params_kernel<<<(a.C + 31) / 32, dim3(32, 8), 0, st>>>(a.part, prows, a.C, a.dw, a.db);
+    });
+}
+
+template <typename T, bool BWD>
+cudaError_t norm_type(const NormArgs &a, int vec, cudaStream_t st, int *n)
+{
+    if constexpr (sizeof(T) == 2)
+        if (vec == 8) return norm_go<T, 8, BWD>(a, st, n);
+    if (vec == 4) return norm_go<T, 4, BWD>(a, st, n);
+    if (vec == 2) return norm_go<T, 2, BWD>(a, st, n);
+    return norm_go<T, 1, BWD>(a, st, n);
+}
+
+}  // namespace
+
+size_t norm_scratch(int N, int S, int C, int G, int dtype, bool backward)
+{
+    // a vector width below norm_vec (misaligned tensors) may take the other path: room for either
+    size_t most = 0;
+    for (int vec = norm_vec(C, G, dtype); vec >= 1; vec /= 2) {
+        RegShape rsh;
+        size_t n;
+        if (reg_shape(S, C, G, vec, &rsh)) {
+            n = backward ? (size_t)reg_blocks(N, rsh) * 2 * C * sizeof(double) : 0;
+        } else {
+            const LongShape sh = long_shape(N, S, C, vec);
+            n = (size_t)N * sh.strips * 2 * C * sizeof(double) + (backward ? (size_t)N * G * 2 * sizeof(float) : 0);
+        }
+        if (n > most) most = n;
+    }
+    return most;
+}
+
+cudaError_t launch_norm(const NormArgs &a, int dtype, bool backward, cudaStream_t st, int *launches)
+{
+    *launches = 0;
+    int vec = norm_vec(a.C, a.G, dtype);
+    // the vector accesses need their own alignment: rows are C values apart
+    const size_t size = dtype == SEMICRF_F32 ? 4 : 2;
+    const uintptr_t all = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) |
+                          reinterpret_cast<uintptr_t>(backward ? a.dy : a.x);
+    while (vec > 1 && all % (vec * size)) vec /= 2;
+    if (dtype == SEMICRF_F32)
+        return backward ? norm_type<float, true>(a, vec, st, launches) : norm_type<float, false>(a, vec, st, launches);
+    if (dtype == SEMICRF_BF16)
+        return backward ? norm_type<__nv_bfloat16, true>(a, vec, st, launches)
+                        : norm_type<__nv_bfloat16, false>(a, vec, st, launches);
+    return backward ? norm_type<__half, true>(a, vec, st, launches) : norm_type<__half, false>(a, vec, st, launches);
+}
+
+}  // namespace semicrf

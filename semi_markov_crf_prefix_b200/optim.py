@@ -1,0 +1,141 @@
+"""AdamW over many tensors in one launch, with states in 32 or 8 bits: what turns the
+gradients of the loss (dA, dD in float64 as the library returns them, or any of the
+floating types) into new parameters.
+
+    m, v, ms, vs = sc.new_adamw_state(params, bits=8)        # ms, vs None for 32 bits
+    sc.adamw_step(params, grads, m, v, step, lr=1e-3, exp_avg_scale=ms, exp_avg_sq_scale=vs)
+
+Everything is updated in place on the current CUDA stream.  In 8 bits a moment moves
+only when an update passes half of its code's spacing (1/16 of its value at most), so
+beta2 near 1 makes the second moment follow slowly growing or shrinking gradients in
+steps; 32 bits are the exact form.
+"""
+from __future__ import annotations
+
+import array
+import ctypes
+
+import torch
+
+from . import _lib
+from .encoder import _call
+
+BLOCK = 256   # values that share a scale
+_TYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16, torch.float64: _lib.F64}
+
+
+def new_adamw_state(params, bits=32):
+    """(exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale): zero states for `params`; the
+    scales are None for 32 bits."""
+    if bits == 32:
+        return ([torch.zeros(p.shape, dtype=torch.float32, device=p.device) for p in params],
+                [torch.zeros(p.shape, dtype=torch.float32, device=p.device) for p in params], None, None)
+    if bits != 8:
+        raise ValueError(f"bits must be 32 or 8, got {bits}")
+    code = lambda p: torch.zeros(p.shape, dtype=torch.uint8, device=p.device)  # noqa: E731
+    scale = lambda p: torch.zeros(-(-p.numel() // BLOCK), dtype=torch.float32, device=p.device)  # noqa: E731
+    return [code(p) for p in params], [code(p) for p in params], [scale(p) for p in params], [scale(p) for p in params]
+
+
+def _same_length(lists):
+    n = len(lists[0][1])
+    for name, ts in lists:
+        if ts is not None and len(ts) != n:
+            raise ValueError(f"{n} params, but {len(ts)} of {name}")
+
+
+def _check(ts, name, like, dtypes, device, scales=False):
+    for t, p in zip(ts, like):
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} has type {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+        if t.numel() != (-(-p.numel() // BLOCK) if scales else p.numel()):
+            raise ValueError(f"{name} of a tensor of shape {tuple(p.shape)} has shape {tuple(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _table(params, grads, m, v, ms, vs):
+    """The library's array of semicrf_adamw_tensor, one of eight 64-bit words each."""
+    words = array.array("q")
+    for i, p in enumerate(params):
+        g = grads[i] if grads is not None else None
+        words.extend((p.data_ptr(), g.data_ptr() if g is not None else 0, m[i].data_ptr() if m else 0,
+                      v[i].data_ptr() if v else 0, ms[i].data_ptr() if ms else 0, vs[i].data_ptr() if vs else 0,
+                      p.numel(), _TYPES[p.dtype] | (_TYPES[g.dtype] << 32 if g is not None else 0)))
+    return words
+
+
+def _scalar(x, name, dtype, device):
+    if x.dtype != dtype or x.numel() != 1 or x.device != device:
+        raise TypeError(f"{name} must be a number or one {dtype} value on {device}")
+    return x.data_ptr()
+
+
+@torch.no_grad()
+def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+               grad_scale=1.0, exp_avg_scale=None, exp_avg_sq_scale=None):
+    """One step over lists of tensors, in place; `step` counts from 1.
+
+    params: float32, bfloat16 or float16; grads: those or float64, of the params' shapes;
+    exp_avg, exp_avg_sq: float32, or uint8 with the lists exp_avg_scale and
+    exp_avg_sq_scale (new_adamw_state).  step and lr may be CUDA scalars (int64 and
+    float32), which the kernel reads: a captured step then follows them.
+    """
+    eight = exp_avg_scale is not None
+    if eight != (exp_avg_sq_scale is not None):
+        raise ValueError("exp_avg_scale and exp_avg_sq_scale come together")
+    _same_length([("params", params), ("grads", grads), ("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq),
+                  ("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)])
+    if not params:
+        return
+    device = params[0].device
+    if not params[0].is_cuda:
+        raise TypeError("params must be CUDA tensors")
+    kind = (torch.uint8,) if eight else (torch.float32,)
+    _check(params, "params", params, (torch.float32, torch.bfloat16, torch.float16), device)
+    _check(grads, "grads", params, tuple(_TYPES), device)
+    for p, g in zip(params, grads):
+        if g.shape != p.shape:
+            raise ValueError(f"a gradient of shape {tuple(g.shape)} for a tensor of shape {tuple(p.shape)}")
+    _check(exp_avg, "exp_avg", params, kind, device)
+    _check(exp_avg_sq, "exp_avg_sq", params, kind, device)
+    if eight:
+        _check(exp_avg_scale, "exp_avg_scale", params, (torch.float32,), device, scales=True)
+        _check(exp_avg_sq_scale, "exp_avg_sq_scale", params, (torch.float32,), device, scales=True)
+    c = _lib.AdamWConfig(0.0, betas[0], betas[1], eps, weight_decay, grad_scale, 0)
+    if isinstance(step, torch.Tensor):
+        c.step_ptr = _scalar(step, "step", torch.int64, device)
+    else:
+        c.step = step
+    if isinstance(lr, torch.Tensor):
+        c.lr_ptr = _scalar(lr, "lr", torch.float32, device)
+    else:
+        c.lr = lr
+    words = _table(params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale)
+    full = [p for p, n in zip(words[0::8], words[6::8]) if n]
+    if len(set(full)) != len(full):
+        raise ValueError("the same tensor is given twice")
+    _call("adamw", device, words.buffer_info()[0], len(params), ctypes.byref(c))
+
+
+@torch.no_grad()
+def adamw_state_values(codes, scales, which):
+    """The float32 values that 8-bit states stand for; which: "exp_avg" or "exp_avg_sq"."""
+    if which not in ("exp_avg", "exp_avg_sq"):
+        raise ValueError(f"which must be exp_avg or exp_avg_sq, got {which!r}")
+    _same_length([("codes", codes), ("scales", scales)])
+    if not codes:
+        return []
+    device = codes[0].device
+    if not codes[0].is_cuda:
+        raise TypeError("codes must be CUDA tensors")
+    _check(codes, "codes", codes, (torch.uint8,), device)
+    _check(scales, "scales", codes, (torch.float32,), device, scales=True)
+    out = [torch.empty(c.shape, dtype=torch.float32, device=device) for c in codes]
+    second = which == "exp_avg_sq"
+    words = _table(out, None, None if second else codes, codes if second else None, None if second else scales,
+                   scales if second else None)
+    _call("adamw_state_values", device, words.buffer_info()[0], len(out), int(second))
+    return out
