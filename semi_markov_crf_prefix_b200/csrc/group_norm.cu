@@ -13,22 +13,62 @@ namespace {
 
 // ---- the elementwise part ----
 
-__device__ __forceinline__ float activate(float z, int act)
+// Phi(z), the normal distribution function, and phi(z) from one exponential:
+// Abramowitz and Stegun 7.1.26, erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2) with
+// t = 1 / (1 + p x) and an error below 1.5e-7, at x = |z| / sqrt 2.  The library's
+// erfcf kept the two-pass kernel at a fifth of the memory's rate.
+__device__ __forceinline__ float normal_cdf(float z, float &density)
 {
-    if (act == SEMICRF_ACT_SILU) return z / (1.f + expf(-z));
-    if (act == SEMICRF_ACT_GELU) return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    const float x = fabsf(z) * 0.70710678118654752f, e = __expf(-x * x);
+    const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+    const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                                0.254829592f);
+    density = 0.39894228040143268f * e;
+    const float tail = 0.5f * poly * e;
+    return z < 0.f ? tail : 1.f - tail;
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z)
+{
+    float density;
+    if constexpr (ACT == SEMICRF_ACT_SILU) return z * sigmoid(z);
+    if constexpr (ACT == SEMICRF_ACT_GELU) return z * normal_cdf(z, density);
     return z;
 }
 
-__device__ __forceinline__ float slope(float z, int act)
+template <int ACT>
+__device__ __forceinline__ float slope(float z)
 {
-    if (act == SEMICRF_ACT_SILU) {
-        const float s = 1.f / (1.f + expf(-z));
+    if constexpr (ACT == SEMICRF_ACT_SILU) {
+        const float s = sigmoid(z);
         return s * fmaf(z, 1.f - s, 1.f);
     }
-    if (act == SEMICRF_ACT_GELU)
-        return fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), 0.5f * erfcf(-0.70710678118654752f * z));
+    if constexpr (ACT == SEMICRF_ACT_GELU) {
+        float density;
+        const float cdf = normal_cdf(z, density);
+        return fmaf(z, density, cdf);
+    }
     return 1.f;
+}
+
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
+// The loop body for the call's activation: chosen once for many values.
+template <typename F>
+__device__ __forceinline__ void by_activation(int act, F &&body)
+{
+    if (act == SEMICRF_ACT_SILU)
+        body(Int<SEMICRF_ACT_SILU>());
+    else if (act == SEMICRF_ACT_GELU)
+        body(Int<SEMICRF_ACT_GELU>());
+    else
+        body(Int<SEMICRF_ACT_NONE>());
 }
 
 template <typename T>
@@ -57,6 +97,7 @@ __device__ __forceinline__ int norm_length(const NormArgs &a, int n)
 // it), one write.
 struct RegShape {
     int CV, RL, NB, W;   // vectors a row; row lanes a block; row blocks a thread block; lanes that sum one group
+    int lanes;           // a group's vectors of one row lie in this many neighbouring lanes of a warp (0: they do not)
 };
 
 constexpr int kRegThreads = 512;
@@ -85,7 +126,7 @@ __device__ __forceinline__ void group_sums(const float *red, float *out, const R
 }
 
 template <typename T, int VEC, int U, bool BWD>
-__global__ __launch_bounds__(kRegThreads) void norm_reg_kernel(const __grid_constant__ NormArgs a, const RegShape sh)
+__global__ __launch_bounds__(kRegThreads, U == 1 ? (BWD ? 2 : 3) : 1) void norm_reg_kernel(const __grid_constant__ NormArgs a, const RegShape sh)
 {
     extern __shared__ float shm[];
     float *red = shm, *red2 = red + kRegThreads, *mean = red2 + kRegThreads, *aux = mean + sh.NB * a.G;
@@ -99,6 +140,15 @@ __global__ __launch_bounds__(kRegThreads) void norm_reg_kernel(const __grid_cons
         bs[e] = mine ? weight_at<T>(a.bias, a.wdtype, c0 + e, 0.f) : 0.f;
         dw[e] = db[e] = 0.f;
     }
+    // a thread's share to its group's sum over the row block
+    auto total = [&](float share, float *red, float *out) {
+        if (sh.lanes) return warp_sum(share, sh.lanes);
+        red[tid] = share;
+        __syncthreads();
+        group_sums(red, out, sh, a.G, CgV);
+        __syncthreads();
+        return mine ? out[nb * a.G + g] : 0.f;
+    };
     for (int n0 = blockIdx.x * sh.NB; n0 < a.N; n0 += gridDim.x * sh.NB) {
         const int n = n0 + nb;
         const bool on = mine && n < a.N;
@@ -124,11 +174,7 @@ __global__ __launch_bounds__(kRegThreads) void norm_reg_kernel(const __grid_cons
                 if (rl + u * sh.RL < L)
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) sum += to_f<T>(x[u].v[e]);
-            red[tid] = sum;
-            __syncthreads();
-            group_sums(red, mean, sh, a.G, CgV);
-            __syncthreads();
-            mu = mine ? mean[nb * a.G + g] * inv : 0.f;
+            mu = inv * total(sum, red, mean);
             sum = 0.f;
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -138,54 +184,49 @@ __global__ __launch_bounds__(kRegThreads) void norm_reg_kernel(const __grid_cons
                         const float d = to_f<T>(x[u].v[e]) - mu;
                         sum = fmaf(d, d, sum);
                     }
-            red2[tid] = sum;
-            __syncthreads();
-            group_sums(red2, aux, sh, a.G, CgV);
-            __syncthreads();
-            rs = mine ? 1.f / sqrtf(aux[nb * a.G + g] * inv + a.eps) : 0.f;
+            rs = 1.f / sqrtf(fmaf(total(sum, red2, aux), inv, a.eps));
             if (on && a.stats && rl == 0 && c0 % Cg == 0) {
                 float *st = a.stats + 2 * ((long long)n * a.G + g);
                 st[0] = mu;
                 st[1] = rs;
             }
+            by_activation(a.act, [&](auto act) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int s = rl + u * sh.RL;
-                if (!on || s >= a.S) continue;
-                Pack<T, VEC> y;
+                for (int u = 0; u < U; ++u) {
+                    const int s = rl + u * sh.RL;
+                    if (!on || s >= a.S) continue;
+                    Pack<T, VEC> y;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    y.v[e] = from_f<T>(s < L ? activate(fmaf((to_f<T>(x[u].v[e]) - mu) * rs, wt[e], bs[e]), a.act) : 0.f);
-                *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(a.y) + base + (long long)s * a.C) = y;
-            }
+                    for (int e = 0; e < VEC; ++e)
+                        y.v[e] = from_f<T>(
+                            s < L ? activate<act.value>(fmaf((to_f<T>(x[u].v[e]) - mu) * rs, wt[e], bs[e])) : 0.f);
+                    *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(a.y) + base + (long long)s * a.C) = y;
+                }
+            });
         } else {
             const float *st = a.stats + 2 * ((long long)(on ? n : 0) * a.G + (mine ? g : 0));
             mu = st[0];
             rs = st[1];
             float s1 = 0.f, s2 = 0.f;
             float gz[U][VEC];
+            by_activation(a.act, [&](auto act) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (rl + u * sh.RL >= L) continue;
+                for (int u = 0; u < U; ++u) {
+                    if (rl + u * sh.RL >= L) continue;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float xh = (to_f<T>(x[u].v[e]) - mu) * rs;
-                    const float dz = to_f<T>(dy[u].v[e]) * slope(fmaf(xh, wt[e], bs[e]), a.act);
-                    gz[u][e] = dz * wt[e];
-                    s1 += gz[u][e];
-                    s2 = fmaf(gz[u][e], xh, s2);
-                    dw[e] = fmaf(dz, xh, dw[e]);
-                    db[e] += dz;
+                    for (int e = 0; e < VEC; ++e) {
+                        const float xh = (to_f<T>(x[u].v[e]) - mu) * rs;
+                        const float dz = to_f<T>(dy[u].v[e]) * slope<act.value>(fmaf(xh, wt[e], bs[e]));
+                        gz[u][e] = dz * wt[e];
+                        s1 += gz[u][e];
+                        s2 = fmaf(gz[u][e], xh, s2);
+                        dw[e] = fmaf(dz, xh, dw[e]);
+                        db[e] += dz;
+                    }
                 }
-            }
-            red[tid] = s1;
-            red2[tid] = s2;
-            __syncthreads();
-            group_sums(red, mean, sh, a.G, CgV);
-            group_sums(red2, aux, sh, a.G, CgV);
-            __syncthreads();
-            s1 = mine ? mean[nb * a.G + g] * inv : 0.f;
-            s2 = mine ? aux[nb * a.G + g] * inv : 0.f;
+            });
+            s1 = inv * total(s1, red, mean);
+            s2 = inv * total(s2, red2, aux);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int s = rl + u * sh.RL;
@@ -199,7 +240,7 @@ __global__ __launch_bounds__(kRegThreads) void norm_reg_kernel(const __grid_cons
                 *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(a.y) + base + (long long)s * a.C) = y;
             }
         }
-        __syncthreads();   // the sums' buffers serve the next row blocks
+        if (!sh.lanes) __syncthreads();   // the sums' buffers serve the next row blocks
     }
     if (BWD) {
         // this block's share of dw and db: part[block][2][C]
@@ -224,40 +265,43 @@ __global__ __launch_bounds__(kRegThreads) void norm_reg_kernel(const __grid_cons
     }
 }
 
-// dw[c], db[c] from P rows of partial sums [P][2][C]: 32 channels and 8 strands of rows a block.
-__global__ void norm_params_kernel(const double *part, int P, int C, float *dw, float *db)
+// dw[c], db[c] from P rows of partial sums [P][2][C]: 8 channels and 64 strands of rows a block.
+__global__ __launch_bounds__(512) void norm_params_kernel(const double *part, int P, int C, float *dw, float *db)
 {
-    __shared__ double sh[2][8][32];
-    const int c = blockIdx.x * 32 + threadIdx.x;
+    __shared__ double sh[2][64][8];
+    const int c = blockIdx.x * 8 + threadIdx.x, j = threadIdx.y;
     double w = 0.0, b = 0.0;
     if (c < C) {
 #pragma unroll 4
-        for (int i = threadIdx.y; i < P; i += 8) {
+        for (int i = j; i < P; i += 64) {
             w += part[(long long)i * 2 * C + c];
             b += part[(long long)i * 2 * C + C + c];
         }
     }
-    sh[0][threadIdx.y][threadIdx.x] = w;
-    sh[1][threadIdx.y][threadIdx.x] = b;
-    __syncthreads();
-    if (threadIdx.y == 0 && c < C) {
-        for (int j = 1; j < 8; ++j) {
-            w += sh[0][j][threadIdx.x];
-            b += sh[1][j][threadIdx.x];
+    sh[0][j][threadIdx.x] = w;
+    sh[1][j][threadIdx.x] = b;
+    for (int half = 32; half > 0; half >>= 1) {
+        __syncthreads();
+        if (j < half) {
+            sh[0][j][threadIdx.x] += sh[0][j + half][threadIdx.x];
+            sh[1][j][threadIdx.x] += sh[1][j + half][threadIdx.x];
         }
-        if (dw) dw[c] = (float)w;
-        if (db) db[c] = (float)b;
+    }
+    if (j == 0 && c < C) {
+        if (dw) dw[c] = (float)sh[0][0][threadIdx.x];
+        if (db) db[c] = (float)sh[1][0][threadIdx.x];
     }
 }
 
 // ---- long rows: two passes over the data ----
 //
 // Pass 1: per-channel sums of a strip of positions, part[n][strip][2][C] in float64
-// (forward: x and x^2; backward: dz xh and dz).  Eight rows at a time are summed in
-// float32 about their own mean before they enter float64, so a large mean costs nothing.
-// Then the groups' statistics, then pass 2 writes y or dx, strips in the opposite
-// order: the ones that pass 1 read last are still in the L2 cache.
-constexpr int kLongThreads = 256, kBatch = 8;
+// (forward: x and x^2; backward: dz xh and dz).  A thread sums up to kRun of a
+// channel's values in float32 about the first of them, which no mean can spoil, and
+// takes the two sums about zero to float64.  Then the groups' statistics, then pass 2
+// writes y or dx, strips in the opposite order: the ones that pass 1 read last are
+// still in the L2 cache.
+constexpr int kLongThreads = 256, kRun = 64;
 
 struct LongShape {
     int CV, tiles, R, strips, rows;   // vectors a row, column tiles of <= 256 of them, row lanes, strips, rows a strip
@@ -273,62 +317,98 @@ __global__ __launch_bounds__(kLongThreads) void norm_sums_kernel(const __grid_co
     const int L = norm_length(a, n), s0 = strip * sh.rows, s1 = min(L, s0 + sh.rows), c0 = cv * VEC;
     const long long base = (long long)n * a.S * a.C + c0;
     double A[VEC], B[VEC];
-    float wt[VEC], bs[VEC], mu[VEC], rs[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        A[e] = B[e] = 0.0;
-        if (BWD && mine) {
-            wt[e] = weight_at<T>(a.weight, a.wdtype, c0 + e, 1.f);
-            bs[e] = weight_at<T>(a.bias, a.wdtype, c0 + e, 0.f);
-            const float *st = a.stats + 2 * ((long long)n * a.G + (c0 + e) / (a.C / a.G));
-            mu[e] = st[0];
-            rs[e] = st[1];
-        }
-    }
+    for (int e = 0; e < VEC; ++e) A[e] = B[e] = 0.0;
     if (mine) {
-        for (int s = s0 + r; s < s1; s += sh.R * kBatch) {
-            Pack<T, VEC> x[kBatch], dy[BWD ? kBatch : 1];
-            int cnt = 0;
+        const T *px = static_cast<const T *>(a.x) + base, *pd = static_cast<const T *>(a.dy) + base;
+        if constexpr (!BWD) {
+            for (int from = s0 + r; from < s1; from += sh.R * kRun) {
+                const int to = min(s1, from + sh.R * kRun);
+                float about[VEC], p[VEC], q[VEC];
+                const Pack<T, VEC> first = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)from * a.C);
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (s + u * sh.R < s1) {
-                    const long long at = base + (long long)(s + u * sh.R) * a.C;
-                    x[u] = *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(a.x) + at);
-                    if (BWD) dy[u] = *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(a.dy) + at);
-                    ++cnt;
+                for (int e = 0; e < VEC; ++e) {
+                    about[e] = to_f<T>(first.v[e]);
+                    p[e] = q[e] = 0.f;
+                }
+                int s = from + sh.R, cnt = 1;
+                constexpr int U = 8;
+                for (; s + (U - 1) * sh.R < to; s += U * sh.R, cnt += U) {
+                    Pack<T, VEC> x[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        x[u] = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s + u * sh.R) * a.C);
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) {
+                            const float d = to_f<T>(x[u].v[e]) - about[e];
+                            p[e] += d;
+                            q[e] = fmaf(d, d, q[e]);
+                        }
+                }
+                for (; s < to; s += sh.R, ++cnt) {
+                    const Pack<T, VEC> x = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)s * a.C);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float d = to_f<T>(x.v[e]) - about[e];
+                        p[e] += d;
+                        q[e] = fmaf(d, d, q[e]);
+                    }
                 }
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float p = 0.f, q = 0.f;
-                if (!BWD) {
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u)
-                        if (u < cnt) p += to_f<T>(x[u].v[e]);
-                    const float m = p / cnt;
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u)
-                        if (u < cnt) {
-                            const float d = to_f<T>(x[u].v[e]) - m;
-                            q = fmaf(d, d, q);
-                        }
-                    // sum of squares about zero, exact in float64 where float32 would cancel:
-                    // sum (x - m)^2 + 2 m sum x - cnt m^2
-                    const double dm = m, dp = p;
-                    A[e] += dp;
-                    B[e] += (double)q + dm * (2.0 * dp - (double)cnt * dm);
-                } else {
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u)
-                        if (u < cnt) {
-                            const float xh = (to_f<T>(x[u].v[e]) - mu[e]) * rs[e];
-                            const float dz = to_f<T>(dy[u].v[e]) * slope(fmaf(xh, wt[e], bs[e]), a.act);
-                            p = fmaf(dz, xh, p);
-                            q += dz;
-                        }
-                    A[e] += (double)p;
-                    B[e] += (double)q;
+                for (int e = 0; e < VEC; ++e) {
+                    const double m = about[e], dp = p[e];
+                    A[e] += dp + cnt * m;
+                    B[e] += (double)q[e] + m * (2.0 * dp + cnt * m);
                 }
             }
+        } else {
+            float wt[VEC], bs[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                wt[e] = weight_at<T>(a.weight, a.wdtype, c0 + e, 1.f);
+                bs[e] = weight_at<T>(a.bias, a.wdtype, c0 + e, 0.f);
+            }
+            const float *st = a.stats + 2 * ((long long)n * a.G + c0 / (a.C / a.G));   // a vector lies inside one group
+            const float mu = st[0], rs = st[1];
+            by_activation(a.act, [&](auto act) {
+                for (int from = s0 + r; from < s1; from += sh.R * kRun) {
+                    const int to = min(s1, from + sh.R * kRun);
+                    float p[VEC], q[VEC];
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) p[e] = q[e] = 0.f;
+                    auto add = [&](const Pack<T, VEC> &x, const Pack<T, VEC> &dy) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) {
+                            const float xh = (to_f<T>(x.v[e]) - mu) * rs;
+                            const float dz = to_f<T>(dy.v[e]) * slope<act.value>(fmaf(xh, wt[e], bs[e]));
+                            p[e] = fmaf(dz, xh, p[e]);
+                            q[e] += dz;
+                        }
+                    };
+                    int s = from;
+                    constexpr int U = 4;
+                    for (; s + (U - 1) * sh.R < to; s += U * sh.R) {
+                        Pack<T, VEC> x[U], dy[U];
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            x[u] = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s + u * sh.R) * a.C);
+                            dy[u] = *reinterpret_cast<const Pack<T, VEC> *>(pd + (long long)(s + u * sh.R) * a.C);
+                        }
+#pragma unroll
+                        for (int u = 0; u < U; ++u) add(x[u], dy[u]);
+                    }
+                    for (; s < to; s += sh.R)
+                        add(*reinterpret_cast<const Pack<T, VEC> *>(px + (long long)s * a.C),
+                            *reinterpret_cast<const Pack<T, VEC> *>(pd + (long long)s * a.C));
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        A[e] += (double)p[e];
+                        B[e] += (double)q[e];
+                    }
+                }
+            });
         }
     }
     double *out = a.part + ((long long)n * sh.strips + strip) * 2 * a.C + c0;
@@ -393,8 +473,8 @@ __global__ void norm_group_kernel(const __grid_constant__ NormArgs a, int strips
 }
 
 template <typename T, int VEC, bool BWD>
-__global__ __launch_bounds__(kLongThreads) void norm_apply_kernel(const __grid_constant__ NormArgs a, const LongShape sh,
-                                                                  const float *gsum)
+__global__ __launch_bounds__(kLongThreads, BWD ? 3 : 4) void norm_apply_kernel(const __grid_constant__ NormArgs a,
+                                                                               const LongShape sh, const float *gsum)
 {
     const int cols = min(sh.CV, kLongThreads), tid = threadIdx.x, r = tid / cols;
     const int cv = blockIdx.y * kLongThreads + tid % cols;
@@ -402,47 +482,54 @@ __global__ __launch_bounds__(kLongThreads) void norm_apply_kernel(const __grid_c
     if (r >= sh.R || cv >= sh.CV) return;
     const int L = norm_length(a, n), s0 = strip * sh.rows, s1 = min(a.S, s0 + sh.rows), c0 = cv * VEC;
     const long long base = (long long)n * a.S * a.C + c0;
-    float wt[VEC], bs[VEC], mu[VEC], rs[VEC], g1[VEC], g2[VEC];
+    float wt[VEC], bs[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
         wt[e] = weight_at<T>(a.weight, a.wdtype, c0 + e, 1.f);
         bs[e] = weight_at<T>(a.bias, a.wdtype, c0 + e, 0.f);
-        const long long at = 2 * ((long long)n * a.G + (c0 + e) / (a.C / a.G));
-        mu[e] = a.stats[at];
-        rs[e] = a.stats[at + 1];
-        if (BWD) {
-            g1[e] = gsum[at];
-            g2[e] = gsum[at + 1];
-        }
     }
-    constexpr int U = BWD ? 4 : 8;
-    for (int s = s0 + r; s < s1; s += sh.R * U) {
-        Pack<T, VEC> x[U], dy[BWD ? U : 1];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (s + u * sh.R < min(s1, L)) {
-                const long long at = base + (long long)(s + u * sh.R) * a.C;
-                x[u] = *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(a.x) + at);
-                if (BWD) dy[u] = *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(a.dy) + at);
-            }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int p = s + u * sh.R;
-            if (p >= s1) break;
+    const long long at = 2 * ((long long)n * a.G + c0 / (a.C / a.G));   // a vector lies inside one group
+    const float mu = a.stats[at], rs = a.stats[at + 1], g1 = BWD ? gsum[at] : 0.f, g2 = BWD ? gsum[at + 1] : 0.f;
+    const T *px = static_cast<const T *>(a.x) + base, *pd = static_cast<const T *>(a.dy) + base;
+    T *py = static_cast<T *>(a.y) + base;
+    const int in = min(s1, L);
+    by_activation(a.act, [&](auto act) {
+        auto value = [&](const Pack<T, VEC> &x, const Pack<T, VEC> &dy) {
             Pack<T, VEC> y;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                float v = 0.f;
-                if (p < L) {
-                    const float xh = (to_f<T>(x[u].v[e]) - mu[e]) * rs[e], z = fmaf(xh, wt[e], bs[e]);
-                    v = BWD ? rs[e] * (to_f<T>(dy[u].v[e]) * slope(z, a.act) * wt[e] - g1[e] - xh * g2[e])
-                            : activate(z, a.act);
-                }
-                y.v[e] = from_f<T>(v);
+                const float xh = (to_f<T>(x.v[e]) - mu) * rs, z = fmaf(xh, wt[e], bs[e]);
+                y.v[e] = from_f<T>(BWD ? rs * (to_f<T>(dy.v[e]) * slope<act.value>(z) * wt[e] - g1 - xh * g2)
+                                       : activate<act.value>(z));
             }
-            *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(a.y) + base + (long long)p * a.C) = y;
+            return y;
+        };
+        constexpr int U = 4;
+        int s = s0 + r;
+        for (; s + (U - 1) * sh.R < in; s += sh.R * U) {
+            Pack<T, VEC> x[U], dy[BWD ? U : 1];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                x[u] = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s + u * sh.R) * a.C);
+                if (BWD) dy[BWD ? u : 0] = *reinterpret_cast<const Pack<T, VEC> *>(pd + (long long)(s + u * sh.R) * a.C);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                *reinterpret_cast<Pack<T, VEC> *>(py + (long long)(s + u * sh.R) * a.C) = value(x[u], dy[BWD ? u : 0]);
         }
-    }
+        for (; s < in; s += sh.R) {
+            const Pack<T, VEC> x = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)s * a.C);
+            *reinterpret_cast<Pack<T, VEC> *>(py + (long long)s * a.C) =
+                value(x, BWD ? *reinterpret_cast<const Pack<T, VEC> *>(pd + (long long)s * a.C) : x);
+        }
+        // behind the row block's end: zeros
+        for (; s < s1; s += sh.R) {
+            Pack<T, VEC> y;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) y.v[e] = from_f<T>(0.f);
+            *reinterpret_cast<Pack<T, VEC> *>(py + (long long)s * a.C) = y;
+        }
+    });
 }
 
 // ---- launches ----
@@ -454,14 +541,16 @@ int pow2_at_least(int v, int most)
     return p;
 }
 
-// The widest vector that stays inside one group: a power of two that divides C/G.
+// The widest vector that stays inside one group: 16 bytes, 4 bytes or one value.
 int norm_vec(int C, int G, int dtype)
 {
     const int most = dtype == SEMICRF_F32 ? 4 : 8, Cg = C / G;
-    int v = 1;
-    while (v < most && Cg % (2 * v) == 0) v *= 2;
-    return v;
+    if (Cg % most == 0) return most;
+    return dtype != SEMICRF_F32 && Cg % 2 == 0 ? 2 : 1;
 }
+
+// The next narrower vector (0 behind the narrowest).
+int narrower(int vec, int dtype) { return vec == 1 ? 0 : vec > 2 && dtype != SEMICRF_F32 ? 2 : 1; }
 
 // Registers hold a row block where its rows take at most 32 values a thread.
 bool reg_shape(int S, int C, int G, int vec, RegShape *sh)
@@ -472,7 +561,9 @@ bool reg_shape(int S, int C, int G, int vec, RegShape *sh)
     sh->RL = R < S ? R : S;
     sh->NB = R / sh->RL;
     if ((S + sh->RL - 1) / sh->RL > 32 / vec) return false;
-    sh->W = pow2_at_least(sh->RL * (C / G / vec), 32);
+    const int CgV = C / G / vec;
+    sh->W = pow2_at_least(sh->RL * CgV, 32);
+    sh->lanes = sh->RL == 1 && CgV <= 32 && (CgV & (CgV - 1)) == 0 ? CgV : 0;
     return true;
 }
 
@@ -485,7 +576,7 @@ LongShape long_shape(int N, int S, int C, int vec)
     sh.R = kLongThreads / cols;
     // strips: eight blocks an SM over everything, each at least one batch of rows deep
     long long strips = (8LL * device_sm_count() + (long long)N * sh.tiles - 1) / ((long long)N * sh.tiles);
-    const long long most = (S + sh.R * kBatch - 1) / (sh.R * kBatch);
+    const long long most = (S + sh.R * 8 - 1) / (sh.R * 8);
     if (strips > most) strips = most;
     if (strips < 1) strips = 1;
     sh.rows = (int)((S + strips - 1) / strips);
@@ -495,7 +586,7 @@ LongShape long_shape(int N, int S, int C, int vec)
 
 int reg_blocks(int N, const RegShape &sh)
 {
-    const int blocks = (N + sh.NB - 1) / sh.NB, most = 4 * device_sm_count();
+    const int blocks = (N + sh.NB - 1) / sh.NB, most = 6 * device_sm_count();
     return blocks < most ? blocks : most;
 }
 
@@ -542,7 +633,7 @@ cudaError_t norm_go(NormArgs a, cudaStream_t st, int *n)
     }
     if (!BWD || (!a.dw && !a.db)) return cudaSuccess;
     return timed_launch(st, n, [&] {
-        norm_params_kernel<<<(a.C + 31) / 32, dim3(32, 8), 0, st>>>(a.part, prows, a.C, a.dw, a.db);
+        norm_params_kernel<<<(a.C + 7) / 8, dim3(8, 64), 0, st>>>(a.part, prows, a.C, a.dw, a.db);
     });
 }
 
@@ -551,8 +642,10 @@ cudaError_t norm_type(const NormArgs &a, int vec, cudaStream_t st, int *n)
 {
     if constexpr (sizeof(T) == 2)
         if (vec == 8) return norm_go<T, 8, BWD>(a, st, n);
-    if (vec == 4) return norm_go<T, 4, BWD>(a, st, n);
-    if (vec == 2) return norm_go<T, 2, BWD>(a, st, n);
+    if constexpr (sizeof(T) == 4)
+        if (vec == 4) return norm_go<T, 4, BWD>(a, st, n);
+    if constexpr (sizeof(T) == 2)
+        if (vec == 2) return norm_go<T, 2, BWD>(a, st, n);
     return norm_go<T, 1, BWD>(a, st, n);
 }
 
@@ -562,7 +655,7 @@ size_t norm_scratch(int N, int S, int C, int G, int dtype, bool backward)
 {
     // a vector width below norm_vec (misaligned tensors) may take the other path: room for either
     size_t most = 0;
-    for (int vec = norm_vec(C, G, dtype); vec >= 1; vec /= 2) {
+    for (int vec = norm_vec(C, G, dtype); vec >= 1; vec = narrower(vec, dtype)) {
         RegShape rsh;
         size_t n;
         if (reg_shape(S, C, G, vec, &rsh)) {
@@ -584,7 +677,7 @@ cudaError_t launch_norm(const NormArgs &a, int dtype, bool backward, cudaStream_
     const size_t size = dtype == SEMICRF_F32 ? 4 : 2;
     const uintptr_t all = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) |
                           reinterpret_cast<uintptr_t>(backward ? a.dy : a.x);
-    while (vec > 1 && all % (vec * size)) vec /= 2;
+    while (vec > 1 && all % (vec * size)) vec = narrower(vec, dtype);
     if (dtype == SEMICRF_F32)
         return backward ? norm_type<float, true>(a, vec, st, launches) : norm_type<float, false>(a, vec, st, launches);
     if (dtype == SEMICRF_BF16)

@@ -19,6 +19,22 @@ constexpr int kTerms = sizeof(T) == 4 ? 3 : 1;
 template <>
 constexpr int kTerms<__half> = 2;   // 11 bits: two bf16 terms hold them exactly
 
+// One operand as a block walks it: element d of position p lies at at + p * step + d.
+struct Track {
+    unsigned char *at;
+    long long step;
+    int d, vec;
+};
+
+// What a block's loop needs of the arguments, in shared memory: the loop has no
+// registers to spare for it, and a spilled register comes back from L2 (400 cycles:
+// the tiles leave next to nothing of the L1 cache).
+struct LaHot {
+    Track q, k, v, o;
+    float b, c;
+    int lead, pe;
+};
+
 // Shapes of the chunked walk for padded width D.  Operands enter the matrix unit as
 // sums of bf16 terms: NI for the inputs (exact), NM for the products P and for the
 // state as an operand of q S (2: 2^-17 relative, far inside the rounding of a 16-bit
@@ -27,86 +43,52 @@ constexpr int kTerms<__half> = 2;   // 11 bits: two bf16 terms hold them exactly
 template <typename T, int D>
 struct LaCfg {
     static constexpr int NI = kTerms<T>, NM = NI == 3 ? 3 : 2, NK = 3;
-    static constexpr bool kStateTmem = D == 128;   // the state itself: float32 in tensor memory, or
-    static constexpr int NS = kStateTmem ? NM : 3; // three bf16 terms (24 bits) in shared memory
-    static constexpr int kTile = tile_bytes(kChunk, D), kSTile = tile_bytes(D, D);
+    static constexpr bool kStateTmem = D == 128;   // the float32 state: tensor memory, or 16 registers a thread
+    static constexpr int kCol = tile_col(kChunk), kSCol = D * 16;   // (threads write S along columns)
+    static constexpr int kTile = D / 8 * kCol, kSTile = D / 8 * kSCol;
     static constexpr int kQ = 0, kK = kQ + NI * kTile, kV = kK + NK * kTile, kS = kV + NI * kTile;
-    static constexpr int kDec = kS + NS * kSTile, kMisc = kDec + (kChunk + 4) * 4;
-    static constexpr int kSmem = kMisc + 32;
+    // decays lam^0 .. lam^128, and P's factors by (row - column) + 127, zero above the diagonal
+    static constexpr int kDec = kS + NM * kSTile, kPf = kDec + (kChunk + 4) * 4, kMisc = kPf + 2 * kChunk * 4;
+    static constexpr int kSmem = kMisc + 32 + (int)sizeof(LaHot);
     // tensor memory columns: scores (P replaces them where two terms fit the same columns), o, k v^T, state
     static constexpr int kP = NM == 3 ? 128 : 0, kO = NM == 3 ? 320 : 128, kKV = kO + D, kState = kKV + D;
     static constexpr int kCols = kState + (kStateTmem ? D : 0) <= 256 ? 256 : 512;
-    static constexpr int kBlocks = kCols == 256 && kSmem <= 114 * 1024 ? 2 : 1;
+    static constexpr int kBlocks = kCols == 256 && kSmem <= 113 * 1024 ? 2 : 1;
+    // where q S waits for the scores' part of o: scaled in its accumulator, or (float32,
+    // where that costs 1e-6 to the accumulator's rounding) in registers
+    static constexpr bool kKeep = NI == 3;
     static constexpr int NP = kChunk * (D / 8) / 256;   // 8-value pieces of a tile for each of 256 threads
+    static constexpr int kRows = 256 / (D / 8);         // tile rows between a thread's pieces
     static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert((NK - (NI == 3 ? 0 : NI)) * kTile >= kChunk * D * (int)sizeof(T), "room for a chunk's outputs");
 };
 
 template <typename T>
 struct Piece {
-    Pack<T, 16 / sizeof(T)> h[sizeof(T) / 2];   // 8 values
-    __device__ __forceinline__ float get(int i) const
-    {
-        constexpr int n = 16 / sizeof(T);
-        return to_f<T>(h[i / n].v[i % n]);
-    }
+    static constexpr int n = 16 / sizeof(T);
+    Pack<T, n> h[8 / n];   // 8 values
+    __device__ __forceinline__ float get(int i) const { return to_f<T>(h[i / n].v[i % n]); }
 };
 
-// 8 values of row p (of the walk) from column d8 * 8 on; zeros outside the sequence and the width.
-template <typename T>
-__device__ __forceinline__ Piece<T> load_piece(const T *base, long long st, long long t, int d0, int d, bool in, int vec)
+// The piece in NT bf16 terms to its place of NT tiles, times w if WEIGHTED.
+template <typename T, int NT, bool WEIGHTED>
+__device__ __forceinline__ void store_terms(unsigned char *at, int tile_stride, const Piece<T> &p, float w)
 {
-    constexpr int n = 16 / sizeof(T);
-    Piece<T> r;
-    if (vec) {
-        if (in && d0 < d) {
-            const Pack<T, n> *src = reinterpret_cast<const Pack<T, n> *>(base + t * st + d0);
+    if constexpr (kTerms<T> == 1 && NT == 1 && !WEIGHTED) {
+        *reinterpret_cast<uint4 *>(at) = *reinterpret_cast<const uint4 *>(&p);
+        return;
+    }
+    uint32_t o[NT][4];
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.h[i] = src[i];
-            return r;
-        }
+    for (int i = 0; i < 4; ++i) {
+        uint32_t t[NT];
+        split2<NT>(WEIGHTED ? p.get(2 * i) * w : p.get(2 * i), WEIGHTED ? p.get(2 * i + 1) * w : p.get(2 * i + 1), t);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) o[j][i] = t[j];
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        r.h[i / n].v[i % n] = !vec && in && d0 + i < d ? base[t * st + d0 + i] : from_f<T>(0.f);
-    return r;
-}
-
-union U16 {
-    __nv_bfloat16 b[8];
-    uint4 u;
-};
-
-// The piece in NT bf16 terms to its places of NT tiles.
-template <typename T, int NT>
-__device__ __forceinline__ void store_terms(unsigned char *tile, int tile_stride, int at, const Piece<T> &p, float w)
-{
-    U16 o[NT];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        __nv_bfloat16 t[NT];
-        bf16_terms<NT>(w == 1.f ? p.get(i) : p.get(i) * w, t);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) o[j].b[i] = t[j];
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) *reinterpret_cast<uint4 *>(tile + j * tile_stride + at) = o[j].u;
-}
-
-template <int N>
-__device__ __forceinline__ float term_sum(const uint4 (&u)[N], int i)
-{
-    float s = 0.f;
-#pragma unroll
-    for (int j = N - 1; j >= 0; --j) {
-        const uint32_t w = reinterpret_cast<const uint32_t *>(&u[j])[i >> 1];
-        s += __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
-    }
-    return s;
-}
-
-__device__ __forceinline__ uint32_t pack2(__nv_bfloat16 lo, __nv_bfloat16 hi)
-{
-    return (uint32_t)__bfloat16_as_ushort(lo) | (uint32_t)__bfloat16_as_ushort(hi) << 16;
+    for (int j = 0; j < NT; ++j)
+        *reinterpret_cast<uint4 *>(at + j * tile_stride) = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
 }
 
 // lam^n from the float32 log_decay, exact to float32's rounding at any n (exponents in float64).
@@ -181,11 +163,93 @@ __device__ __forceinline__ StateAt state_from(const LaWalk &w, const LaArgs &a, 
     return {w.s_in ? w.s_in + bh * sz : nullptr, w.s_rs, w.s_cs};
 }
 
+template <typename T>
+__device__ __forceinline__ Track track_of(const void *base, const long long (&st)[3], int d, int vec, const LaSpan &s,
+                                          int reverse)
+{
+    const T *p = static_cast<const T *>(base) + s.b * st[0] + s.h * st[2] + (reverse ? (s.L - 1) * st[1] : 0);
+    return {reinterpret_cast<unsigned char *>(const_cast<T *>(p)), reverse ? -st[1] : st[1], d, vec};
+}
+
+// This thread's pieces of an operand: 8 values at column d0 of positions p, p + ROWS, ...
+// of which those below `end` lie inside the sequence.  Whole pieces: loads under a
+// predicate, none waits for another.
+template <typename T, int NP, int ROWS>
+__device__ __forceinline__ void load_pieces(const Track &g, Piece<T> (&o)[NP], int p, int end, int d0)
+{
+    constexpr int n = Piece<T>::n;
+    const long long step = g.step;
+    const int d = g.d;
+    const T *src = reinterpret_cast<const T *>(g.at) + p * step + d0;
+    if (g.vec) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+#pragma unroll
+            for (int i = 0; i < 8 / n; ++i) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (p + j * ROWS < end && d0 < d) v = reinterpret_cast<const uint4 *>(src + j * ROWS * step)[i];
+                *reinterpret_cast<uint4 *>(&o[j].h[i]) = v;
+            }
+    } else {
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                T v = from_f<T>(0.f);
+                if (p + j * ROWS < end && d0 + i < d) v = src[j * ROWS * step + i];
+                o[j].h[i / n].v[i % n] = v;
+            }
+    }
+}
+
+// bf16 operands need no conversion: whole pieces go from global to shared memory on
+// their own (to be waited for with cp_async_wait), others by way of registers.
+template <typename T, int NP, int ROWS>
+__device__ __forceinline__ void bring_pieces(const Track &g, unsigned char *to, int p, int end, int d0)
+{
+    if (g.vec) {
+        const long long step = g.step;
+        const T *src = reinterpret_cast<const T *>(g.at) + p * step + d0;
+        const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            const bool in = p + j * ROWS < end && d0 < g.d;
+            const void *from = in ? static_cast<const void *>(src + j * ROWS * step) : g.at;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + j * ROWS * 16), "l"(from),
+                         "r"(in ? 16 : 0)
+                         : "memory");
+        }
+    } else {
+#pragma unroll 1
+        for (int j = 0; j < NP; ++j) {
+            Piece<T> o[1];
+            load_pieces<T, 1, ROWS>(g, o, p + j * ROWS, end, d0);
+            *reinterpret_cast<uint4 *>(to + j * ROWS * 16) = *reinterpret_cast<const uint4 *>(&o[0]);
+        }
+    }
+}
+
+// Products of operands in NA and NB terms: go(x, y, accumulate) for the pairs of terms
+// with x + y < N, the smallest first.
+template <int NA, int NB, int N, typename F>
+__device__ __forceinline__ void mma_terms(F &&go)
+{
+    bool acc = false;
+#pragma unroll
+    for (int sum = N - 1; sum >= 0; --sum)
+#pragma unroll
+        for (int x = 0; x <= sum; ++x)
+            if (x < NA && sum - x < NB) {
+                go(x, sum - x, acc);
+                acc = true;
+            }
+}
+
 // The chunked walk: 128 positions at a time,
-//   scores = Q K^T and Q S                           (tensor memory)
-//   P = b c lam^{i-j} scores (j <= i), K~ = c lam^{end-j} K   (threads; P to tensor memory, K~ to shared)
-//   o = P V + b lam^{i+1} (Q S),  KV = K~^T V        (tensor memory, read back by rows)
-//   S = lam^n S + KV                                 (threads, float32)
+//   scores = Q K^T and Q S                              (tensor memory)
+//   K~ = c lam^{end-j} K,  P = b c lam^{i-j} scores     (threads; P to tensor memory, K~ over K)
+//   KV = K~^T V (while P is formed),  o = b lam^{i+1} (Q S) + P V
+//   S = lam^n S + KV                                    (threads, float32)
 // The matrix unit's accumulators round towards zero (measured: -1.4e-7 relative for
 // each 8 steps of 16), which a state carried in them over thousands of chunks would
 // show; so they hold one chunk's sums only, small terms first, and the state is
@@ -194,11 +258,15 @@ template <typename T, int D, bool STATE_ONLY>
 __global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(const __grid_constant__ LaArgs args)
 {
     using G = LaCfg<T, D>;
-    constexpr int NI = G::NI, NM = G::NM, NK = G::NK, NS = G::NS, NP = G::NP;
+    constexpr int NI = G::NI, NM = G::NM, NK = G::NK, NP = G::NP;
+    // steps of 16 values of a contraction, and of one tile, in a descriptor's units
+    constexpr uint64_t kCol2 = 2 * G::kCol >> 4, kRow2 = 2 * 128 >> 4, 
+                       kTileD = G::kTile >> 4, kSTileD = G::kSTile >> 4;
     extern __shared__ __align__(128) unsigned char sm[];
     const LaWalk &w = args.w[blockIdx.y];
     const LaSpan s = la_span(args, blockIdx.x);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3, half = warp >> 2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int quad = warp & 3, half = warp >> 2;
     if (STATE_ONLY && s.seg == args.nseg - 1) return;
     if (!STATE_ONLY) {
         zero_rows<T>(w, s, 0, w.dv);
@@ -206,277 +274,381 @@ __global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(c
     }
     if (s.pe == s.p0) return;
 
-    float *dec = reinterpret_cast<float *>(sm + G::kDec);
+    float *dec = reinterpret_cast<float *>(sm + G::kDec), *pf = reinterpret_cast<float *>(sm + G::kPf);
+    float *full = reinterpret_cast<float *>(sm + G::kMisc + 24);   // lam^128 in two floats
+    LaHot &hot = *reinterpret_cast<LaHot *>(sm + G::kMisc + 32);
     uint32_t *slot = reinterpret_cast<uint32_t *>(sm + G::kMisc + 16);
     const uint32_t smem = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
     const uint32_t bar1 = smem + G::kMisc, bar2 = bar1 + 8;
-    const float ld = args.log_decay[s.h], pa = w.b * w.c;
+    const float ld = args.log_decay[s.h];
     if (warp == 0) tmem_alloc(static_cast<uint32_t>(__cvta_generic_to_shared(slot)), G::kCols);
     if (tid == 0) {
         mbar_init(bar1, 1);
         mbar_init(bar2, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (tid <= kChunk) dec[tid] = (float)decay_pow(ld, tid);
-
-    const T *qb = static_cast<const T *>(w.q) + s.b * w.qs[0] + s.h * w.qs[2];
-    const T *kb = static_cast<const T *>(w.k) + s.b * w.ks[0] + s.h * w.ks[2];
-    const T *vb = static_cast<const T *>(w.v) + s.b * w.vs[0] + s.h * w.vs[2];
-    Piece<T> rq[NP], rk[NP], rv[NP];
-    auto fetch = [&](int pc) {
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int idx = tid + i * 256, d0 = idx % (D / 8) * 8, p = pc + idx / (D / 8);
-            const bool in = p < s.pe;
-            const long long t = w.reverse ? s.L - 1 - p : p;
-            if (!STATE_ONLY) rq[i] = load_piece<T>(qb, w.qs[1], t, d0, w.dk, in, w.q_vec);
-            rk[i] = load_piece<T>(kb, w.ks[1], t, d0, w.dk, in, w.k_vec);
-            rv[i] = load_piece<T>(vb, w.vs[1], t, d0, w.dv, in, w.v_vec);
+    if (tid <= kChunk) {
+        const double v = decay_pow(ld, tid);
+        dec[tid] = (float)v;
+        if (tid < kChunk) {
+            pf[kChunk - 1 + tid] = (float)(v * (double)(w.b * w.c));
+        } else {
+            full[0] = (float)v;
+            full[1] = (float)(v - (double)full[0]);
         }
+    } else {
+        pf[tid - kChunk - 1] = 0.f;   // 127 entries
+    }
+
+    const int r0 = tid / (D / 8), d8 = tid % (D / 8), at0 = d8 * G::kCol + r0 * 16;
+    if (tid == 0) {
+        hot.q = track_of<T>(w.q, w.qs, w.dk, w.q_vec, s, w.reverse);
+        hot.k = track_of<T>(w.k, w.ks, w.dk, w.k_vec, s, w.reverse);
+        hot.v = track_of<T>(w.v, w.vs, w.dv, w.v_vec, s, w.reverse);
+        hot.o = track_of<T>(w.o, w.os, w.dv, w.o_vec, s, w.reverse);
+        hot.b = w.b;
+        hot.c = w.c;
+        hot.lead = w.lead;
+        hot.pe = s.pe;
+    }
+    __syncthreads();
+    const int pe = s.pe;
+    // float32 and float16 are prefetched in registers and split on their way to shared
+    // memory; the state-only walk weights its keys there
+    constexpr bool kDirect = NI == 1 && !STATE_ONLY;
+    Piece<T> rk[kDirect ? 1 : NP], rv[kDirect ? 1 : NP];
+    auto fetch = [&](const Track &g, Piece<T> (&to)[NP], int pc) {
+        load_pieces<T, NP, G::kRows>(g, to, pc + r0, hot.pe, d8 * 8);
     };
-    fetch(s.p0);
+    auto bring = [&](const Track &g, int tile, int pc) {
+        bring_pieces<T, NP, G::kRows>(g, sm + tile + at0, pc + r0, hot.pe, d8 * 8);
+    };
 
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
-    const uint32_t tm = *slot, tlane = tm + ((uint32_t)(quad * 32) << 16);
+    const uint32_t tm = __shfl_sync(0xffffffffu, *slot, 0), tlane = tm + ((uint32_t)(quad * 32) << 16);
+    const int nv = (w.dv + 15) / 16 * 16, kd = (w.dk + 15) / 16, c0 = half * (D / 2);
 
-    // this thread's row of the state (64 rows lie in the first 16 lanes of each quadrant)
-    // and its half of the columns
-    const int srow = D == 64 ? quad * 16 + (lane & 15) : quad * 32 + lane;
-    const bool has_row = D == 128 || lane < 16;
-    const int nv = (w.dv + 15) / 16 * 16, kd = (w.dk + 15) / 16;
-    {
-        const StateAt from = STATE_ONLY ? StateAt{nullptr, 0, 0} : state_from(w, args, s);
+    // The state.  D = 64: rows quad * 16 + lane / 4 (+ 8), column pairs c0 + 8 j + 2 (lane % 4)
+    // in registers; D = 128: row quad * 32 + lane, columns c0 .. c0 + 63 in tensor memory.
+    float S[G::kStateTmem ? 1 : 16];
+    const StateAt from = STATE_ONLY ? StateAt{nullptr, 0, 0} : state_from(w, args, s);
+    auto given = [&](int row, int col) {
+        return from.p && row < w.dk && col < w.dv ? from.p[(long long)row * from.rs + (long long)col * from.cs] : 0.f;
+    };
+    auto put_pairs = [&] {   // D = 64: the terms of S to shared memory
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                uint32_t t[NM];
+                split2<NM>(S[4 * j + 2 * a], S[4 * j + 2 * a + 1], t);
+                unsigned char *to = sm + G::kS + (half * 4 + j) * G::kSCol + (quad * 16 + (lane >> 2) + 8 * a) * 16 + 4 * (lane & 3);
+#pragma unroll
+                for (int x = 0; x < NM; ++x) *reinterpret_cast<uint32_t *>(to + x * G::kSTile) = t[x];
+            }
+    };
+    auto put_row = [&](int c, const uint32_t (&r)[16]) {   // D = 128: 16 columns of this thread's row
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            uint32_t o[NM][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t t[NM];
+                split2<NM>(__uint_as_float(r[8 * g + 2 * e]), __uint_as_float(r[8 * g + 2 * e + 1]), t);
+#pragma unroll
+                for (int x = 0; x < NM; ++x) o[x][e] = t[x];
+            }
+#pragma unroll
+            for (int x = 0; x < NM; ++x)
+                *reinterpret_cast<uint4 *>(sm + G::kS + x * G::kSTile + (c / 8 + g) * G::kSCol + (quad * 32 + lane) * 16) =
+                    make_uint4(o[x][0], o[x][1], o[x][2], o[x][3]);
+        }
+    };
+    if constexpr (G::kStateTmem) {
 #pragma unroll 1
-        for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+        for (int c = c0; c < c0 + D / 2; c += 16) {
             uint32_t r[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const bool in = from.p && has_row && srow < w.dk && c + e < w.dv;
-                r[e] = __float_as_uint(in ? from.p[(long long)srow * from.rs + (long long)(c + e) * from.cs] : 0.f);
-            }
-            if (G::kStateTmem) tmem_st16(tlane + G::kState + c, r);
-            if (has_row) {
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    U16 o[NS];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        __nv_bfloat16 t[NS];
-                        bf16_terms<NS>(__uint_as_float(r[g * 8 + e]), t);
-#pragma unroll
-                        for (int j = 0; j < NS; ++j) o[j].b[e] = t[j];
-                    }
-#pragma unroll
-                    for (int j = 0; j < NS; ++j)
-                        *reinterpret_cast<uint4 *>(sm + G::kS + j * G::kSTile + tile_at(D, srow, c / 8 + g)) = o[j].u;
-                }
-            }
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(given(quad * 32 + lane, c + e));
+            tmem_st16(tlane + G::kState + c, r);
+            put_row(c, r);
         }
-        if (G::kStateTmem) tmem_wait_st();
+        tmem_wait_st();
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            S[i] = given(quad * 16 + (lane >> 2) + (i & 2) * 4, c0 + (i >> 2) * 8 + (lane & 3) * 2 + (i & 1));
+        put_pairs();
+    }
+
+    if constexpr (kDirect) {
+        bring(hot.q, G::kQ, s.p0);
+        bring(hot.k, G::kK, s.p0);
+        bring(hot.v, G::kV, s.p0);
+    } else {
+        if (!STATE_ONLY) {
+            Piece<T> rq[NP];
+            fetch(hot.q, rq, s.p0);
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                store_terms<T, NI, false>(sm + G::kQ + at0 + i * G::kRows * 16, G::kTile, rq[i], 1.f);
+        }
+        fetch(hot.k, rk, s.p0);
+        fetch(hot.v, rv, s.p0);
     }
 
     bool alive = true;
     uint32_t parity = 0;
-    for (int pc = s.p0; pc < s.pe; pc += kChunk, parity ^= 1) {
-        const int cnt = min(kChunk, s.pe - pc);
-        const int lead = pc == 0 ? w.lead : 1;
-        // operands to shared memory; the state-only walk needs K~ alone
+    for (int pc = s.p0; pc < pe; pc += kChunk, parity ^= 1) {
+        const int cnt = min(kChunk, pe - pc);
+        const int lead = pc == 0 ? hot.lead : 1;
+        const bool more = pc + kChunk < pe;
+        if constexpr (kDirect) {
+            cp_async_commit();
+            cp_async_wait<0>();
+        } else {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int idx = tid + i * 256, r = idx / (D / 8), at = tile_at(kChunk, r, idx % (D / 8));
-            if (STATE_ONLY) {
-                store_terms<T, NK>(sm + G::kK, G::kTile, at, rk[i], r < cnt ? w.c * dec[cnt - 1 - r] : 0.f);
-            } else {
-                store_terms<T, NI>(sm + G::kQ, G::kTile, at, rq[i], 1.f);
-                store_terms<T, NI>(sm + G::kK, G::kTile, at, rk[i], 1.f);
+            for (int i = 0; i < NP; ++i) {
+                const int r = r0 + i * G::kRows, at = at0 + i * G::kRows * 16;
+                if (STATE_ONLY)
+                    store_terms<T, NK, true>(sm + G::kK + at, G::kTile, rk[i], r < cnt ? hot.c * dec[cnt - 1 - r] : 0.f);
+                else
+                    store_terms<T, NI, false>(sm + G::kK + at, G::kTile, rk[i], 1.f);
+                store_terms<T, NI, false>(sm + G::kV + at, G::kTile, rv[i], 1.f);
             }
-            store_terms<T, NI>(sm + G::kV, G::kTile, at, rv[i], 1.f);
         }
         smem_to_mma();
         tc_before_sync();
         if (__syncthreads_or(!alive)) break;
 
-        if (!STATE_ONLY && tid == 0) {
-            tc_after_sync();
-            const uint32_t i1 = mma_idesc(128, 128, false, false), i2 = mma_idesc(128, nv, false, true);
-            bool acc = false;
-            for (int sum = NI - 1; sum >= 0; --sum)
-                for (int x = 0; x <= sum; ++x)
-                    for (int k = 0; k < kd; ++k) {
-                        mma_ss(tm, desc_k(smem + G::kQ + x * G::kTile, kChunk, k),
-                               desc_k(smem + G::kK + (sum - x) * G::kTile, kChunk, k), i1, acc);
-                        acc = true;
-                    }
-            acc = false;
-            for (int sum = NM - 1; sum >= 0; --sum)
-                for (int x = 0; x <= sum && x < NI; ++x)
-                    for (int k = 0; k < kd; ++k) {
-                        mma_ss(tm + G::kO, desc_k(smem + G::kQ + x * G::kTile, kChunk, k),
-                               desc_mn(smem + G::kS + (sum - x) * G::kSTile, D, k), i2, acc);
-                        acc = true;
-                    }
-            mma_commit(bar1);
-        }
-
-        float qs[D / 2];
         if (!STATE_ONLY) {
+            if (warp == 0) {
+                tc_after_sync();
+                const uint32_t lead1 = elect_lane();
+                const uint32_t i1 = mma_idesc(128, 128, false, false), i2 = mma_idesc(128, nv, false, true);
+                const uint64_t dq = desc_k(smem + G::kQ, G::kCol), dk = desc_k(smem + G::kK, G::kCol);
+                const uint64_t ds = desc_mn(smem + G::kS, G::kSCol);
+                mma_terms<NI, NI, NI>([&](int x, int y, bool acc) {
+#pragma unroll 1
+                    for (int k = 0; k < kd; ++k, acc = true)
+                        mma_ss(lead1, tm, dq + x * kTileD + k * kCol2, dk + y * kTileD + k * kCol2, i1, acc);
+                });
+                mma_terms<NI, NM, NM>([&](int x, int y, bool acc) {
+#pragma unroll 1
+                    for (int k = 0; k < kd; ++k, acc = true)
+                        mma_ss(lead1, tm + G::kO, dq + x * kTileD + k * kCol2, ds + y * kSTileD + k * kRow2, i2, acc);
+                });
+                mma_commit(lead1, bar1);
+            }
+            // the next queries travel while the scores are formed; then their tile is free
+            Piece<T> rq[kDirect ? 1 : NP];
+            if constexpr (!kDirect)
+                if (more) fetch(hot.q, rq, pc + kChunk);
             alive = mbar_wait_bounded(bar1, parity) && alive;
             __syncwarp();
             tc_after_sync();
+            if (more) {
+                if constexpr (kDirect) {
+                    bring(hot.q, G::kQ, pc + kChunk);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+                        store_terms<T, NI, false>(sm + G::kQ + at0 + i * G::kRows * 16, G::kTile, rq[i], 1.f);
+                }
+            }
             // K -> K~ in place
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                const int idx = tid + i * 256, r = idx / (D / 8), at = tile_at(kChunk, r, idx % (D / 8));
+                const int r = r0 + i * G::kRows;
+                unsigned char *at = sm + G::kK + at0 + i * G::kRows * 16;
+                const float wk = r < cnt ? hot.c * dec[cnt - 1 - r] : 0.f;
                 uint4 u[NI];
 #pragma unroll
-                for (int j = 0; j < NI; ++j) u[j] = *reinterpret_cast<const uint4 *>(sm + G::kK + j * G::kTile + at);
-                const float wk = r < cnt ? w.c * dec[cnt - 1 - r] : 0.f;
-                U16 o[NK];
+                for (int j = 0; j < NI; ++j) u[j] = *reinterpret_cast<const uint4 *>(at + j * G::kTile);
+                uint32_t o[NK][4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    __nv_bfloat16 t[NK];
-                    bf16_terms<NK>(term_sum(u, e) * wk, t);
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t t[NI], n[NK];
 #pragma unroll
-                    for (int j = 0; j < NK; ++j) o[j].b[e] = t[j];
+                    for (int j = 0; j < NI; ++j) t[j] = reinterpret_cast<const uint32_t *>(&u[j])[e];
+                    float x, y;
+                    join2<NI>(t, x, y);
+                    split2<NK>(x * wk, y * wk, n);
+#pragma unroll
+                    for (int j = 0; j < NK; ++j) o[j][e] = n[j];
                 }
 #pragma unroll
-                for (int j = 0; j < NK; ++j) *reinterpret_cast<uint4 *>(sm + G::kK + j * G::kTile + at) = o[j].u;
+                for (int j = 0; j < NK; ++j)
+                    *reinterpret_cast<uint4 *>(at + j * G::kTile) = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
             }
-            // scores -> P: sixteen scores at a time become 8 columns of each term
+            smem_to_mma();
+            __syncthreads();
+        }
+        if (warp == 0) {
+            tc_after_sync();
+            const uint32_t lead1 = elect_lane();
+            const uint32_t i4 = mma_idesc(D, nv, true, true);
+            const uint64_t dk = desc_mn(smem + G::kK, G::kCol), dv = desc_mn(smem + G::kV, G::kCol);
+            mma_terms<NK, NI, NK>([&](int x, int y, bool acc) {
+#pragma unroll 1
+                for (int k = 0; k < kChunk / 16; ++k, acc = true)
+                    mma_ss(lead1, tm + G::kKV, dk + x * kTileD + k * kRow2, dv + y * kTileD + k * kRow2, i4, acc);
+            });
+            if (STATE_ONLY) mma_commit(lead1, bar2);
+        }
+        float qs[!STATE_ONLY && G::kKeep ? D / 2 : 1];
+        if (!STATE_ONLY) {
+            // scores -> P: 32 scores at a time become 16 columns of each term
             const int row = quad * 32 + lane;
 #pragma unroll 1
-            for (int c = half * 64; c < half * 64 + 64; c += 16) {
-                uint32_t r[16], o[NM][8];
-                tmem_ld16(tlane + c, r);
-                tmem_wait_ld();
+            for (int c = half * 64; c < half * 64 + 64; c += 32) {
+                uint32_t r[32];
+                if (c <= quad * 32 + 31) {   // some row of this warp reaches these keys
+                    tmem_ld32(tlane + c, r);
+                    tmem_wait_ld();
+                    const float *f = pf + (kChunk - 1) + row - c;
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    __nv_bfloat16 t0[NM], t1[NM];
-                    const int far = row - c - e;
-                    bf16_terms<NM>(far >= 0 ? __uint_as_float(r[e]) * (pa * dec[far]) : 0.f, t0);
-                    bf16_terms<NM>(far >= 1 ? __uint_as_float(r[e + 1]) * (pa * dec[far - 1]) : 0.f, t1);
+                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f[-e]);
+                } else {
 #pragma unroll
-                    for (int j = 0; j < NM; ++j) o[j][e / 2] = pack2(t0[j], t1[j]);
+                    for (int e = 0; e < 32; ++e) r[e] = 0;
                 }
 #pragma unroll
-                for (int j = 0; j < NM; ++j) tmem_st8(tlane + G::kP + c / 16 * (8 * NM) + j * 8, o[j]);
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t o[NM][8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t t[NM];
+                        split2<NM>(__uint_as_float(r[16 * g + 2 * e]), __uint_as_float(r[16 * g + 2 * e + 1]), t);
+#pragma unroll
+                        for (int j = 0; j < NM; ++j) o[j][e] = t[j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < NM; ++j) tmem_st8(tlane + G::kP + (c / 16 + g) * (8 * NM) + j * 8, o[j]);
+                }
             }
-            // q S, kept until the scores' part of o is there
+            // o starts as b lam^{i+1} q S
+            const float f = hot.b * dec[row + lead];
 #pragma unroll
             for (int c = 0; c < D / 2; c += 16) {
                 uint32_t r[16];
-                tmem_ld16(tlane + G::kO + half * (D / 2) + c, r);
+                tmem_ld16(tlane + G::kO + c0 + c, r);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) qs[c + e] = __uint_as_float(r[e]);
+                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                if constexpr (G::kKeep) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) qs[c + e] = __uint_as_float(r[e]);
+                } else {
+                    tmem_st16(tlane + G::kO + c0 + c, r);
+                }
             }
             tmem_wait_st();
-            smem_to_mma();
             tc_before_sync();
             __syncthreads();
-        }
-        if (tid == 0) {
-            tc_after_sync();
-            const uint32_t i3 = mma_idesc(128, nv, false, true), i4 = mma_idesc(D, nv, true, true);
-            bool acc = false;
-            if (!STATE_ONLY) {
-                for (int sum = NM - 1; sum >= 0; --sum)
-                    for (int x = 0; x <= sum; ++x) {
-                        if (sum - x >= NI) continue;
-                        for (int k = 0; k < kChunk / 16; ++k) {
-                            mma_ts(tm + G::kO, tm + G::kP + k * (8 * NM) + x * 8,
-                                   desc_mn(smem + G::kV + (sum - x) * G::kTile, kChunk, k), i3, acc);
-                            acc = true;
-                        }
-                    }
-                acc = false;
+            if (warp == 0) {
+                tc_after_sync();
+                const uint32_t lead1 = elect_lane();
+                const uint32_t i3 = mma_idesc(128, nv, false, true);
+                const uint64_t dv = desc_mn(smem + G::kV, G::kCol);
+                mma_terms<NM, NI, NM>([&](int x, int y, bool acc) {
+                    acc |= !G::kKeep;
+#pragma unroll 1
+                    for (int k = 0; k < kChunk / 16; ++k, acc = true)
+                        mma_ts(lead1, tm + G::kO, tm + G::kP + k * (8 * NM) + x * 8, dv + y * kTileD + k * kRow2, i3, acc);
+                });
+                mma_commit(lead1, bar2);
             }
-            for (int sum = NK - 1; sum >= 0; --sum)
-                for (int x = 0; x <= sum; ++x) {
-                    if (sum - x >= NI) continue;
-                    for (int k = 0; k < kChunk / 16; ++k) {
-                        mma_ss(tm + G::kKV, desc_mn(smem + G::kK + x * G::kTile, kChunk, k),
-                               desc_mn(smem + G::kV + (sum - x) * G::kTile, kChunk, k), i4, acc);
-                        acc = true;
-                    }
-                }
-            mma_commit(bar2);
         }
-        if (pc + kChunk < s.pe) fetch(pc + kChunk);
+        if constexpr (!kDirect)
+            if (more) {
+                fetch(hot.k, rk, pc + kChunk);
+                fetch(hot.v, rv, pc + kChunk);
+            }
         alive = mbar_wait_bounded(bar2, parity) && alive;
         __syncwarp();
         tc_after_sync();
+        if constexpr (kDirect)
+            if (more) {   // (the outputs below use the parts of K~ behind the keys' own tile)
+                bring(hot.k, G::kK, pc + kChunk);
+                bring(hot.v, G::kV, pc + kChunk);
+            }
 
         if (!STATE_ONLY) {
-            const int row = quad * 32 + lane, p = pc + row;
-            const float f = w.b * dec[min(row + lead, kChunk)];
-            T *ob = static_cast<T *>(w.o) + s.b * w.os[0] + s.h * w.os[2] +
-                    (w.reverse ? s.L - 1 - p : p) * w.os[1];
+            // rows to shared memory (the part of K~'s tiles that the next keys leave
+            // alone), then whole rows to global memory; 16-byte pieces of a row are
+            // exchanged by the row's number so that neither side meets bank conflicts
+            constexpr int n = 16 / sizeof(T), W = D / n;   // values of a piece, pieces of a row
+            unsigned char *ob = sm + G::kK + (NI == 3 ? 0 : NI * G::kTile);
+            const int row = quad * 32 + lane;
 #pragma unroll
             for (int c = 0; c < D / 2; c += 16) {
                 uint32_t r[16];
-                tmem_ld16(tlane + G::kO + half * (D / 2) + c, r);
+                tmem_ld16(tlane + G::kO + c0 + c, r);
                 tmem_wait_ld();
-                const int col = half * (D / 2) + c;
-                if (p < s.pe) {
-                    constexpr int n = 16 / sizeof(T);
 #pragma unroll
-                    for (int g = 0; g < 16 / n; ++g) {
-                        Pack<T, n> o;
+                for (int g = 0; g < 16 / n; ++g) {
+                    Pack<T, n> o;
 #pragma unroll
-                        for (int e = 0; e < n; ++e)
-                            o.v[e] = from_f<T>(fmaf(f, qs[c + g * n + e], __uint_as_float(r[g * n + e])));
-                        const int c0 = col + g * n;
-                        if (w.o_vec) {
-                            if (c0 < w.dv) *reinterpret_cast<Pack<T, n> *>(ob + c0) = o;
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < n; ++e)
-                                if (c0 + e < w.dv) ob[c0 + e] = o.v[e];
-                        }
-                    }
+                    for (int e = 0; e < n; ++e)
+                        o.v[e] = from_f<T>(__uint_as_float(r[g * n + e]) + (G::kKeep ? qs[G::kKeep ? c + g * n + e : 0] : 0.f));
+                    *reinterpret_cast<Pack<T, n> *>(ob + (row * W + (((c0 + c) / n + g) ^ (row & 7))) * 16) = o;
                 }
             }
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");   // the two halves of these 32 rows
+            const Track to = hot.o;
+            T *og = reinterpret_cast<T *>(to.at) + pc * to.step;
+#pragma unroll
+            for (int j = 0; j < W / 2; ++j) {
+                const int i = j * 64 + half * 32 + lane, rr = quad * 32 + i / W, piece = i % W, col = piece * n;
+                if (pc + rr >= hot.pe || col >= to.d) continue;
+                const Pack<T, n> o = *reinterpret_cast<const Pack<T, n> *>(ob + (rr * W + (piece ^ (rr & 7))) * 16);
+                T *at = og + rr * to.step + col;
+                if (to.vec) {
+                    *reinterpret_cast<Pack<T, n> *>(at) = o;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < n; ++e)
+                        if (col + e < to.d) at[e] = o.v[e];
+                }
+            }
+            if (NI == 3) __syncthreads();   // the next keys go where these rows were
         }
         // S = lam^n S + KV, and its terms for the next chunk.  The float32 rounding of
         // lam^n alone would bias a state that lives for many chunks: two parts.
-        const double step = decay_pow(ld, cnt - 1 + lead);
-        const float hi = (float)step, lo = (float)(step - (double)hi);
-#pragma unroll 1
-        for (int c = half * (D / 2); c < min((half + 1) * (D / 2), nv); c += 16) {
-            uint32_t r[16], old[16];
-            tmem_ld16(tlane + G::kKV + c, r);
-            if (G::kStateTmem) tmem_ld16(tlane + G::kState + c, old);
-            tmem_wait_ld();
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint4 u[NS];
-                U16 o[NS];
-                const int at = tile_at(D, srow, c / 8 + g);
-                if (!G::kStateTmem) {
-#pragma unroll
-                    for (int j = 0; j < NS; ++j) u[j] = *reinterpret_cast<const uint4 *>(sm + G::kS + j * G::kSTile + at);
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float prev = G::kStateTmem ? __uint_as_float(old[g * 8 + e]) : term_sum(u, e);
-                    const float next = fmaf(prev, hi, fmaf(prev, lo, __uint_as_float(r[g * 8 + e])));
-                    old[g * 8 + e] = __float_as_uint(next);
-                    __nv_bfloat16 t[NS];
-                    bf16_terms<NS>(next, t);
-#pragma unroll
-                    for (int j = 0; j < NS; ++j) o[j].b[e] = t[j];
-                }
-                if (has_row) {
-#pragma unroll
-                    for (int j = 0; j < NS; ++j) *reinterpret_cast<uint4 *>(sm + G::kS + j * G::kSTile + at) = o[j].u;
-                }
-            }
-            if (G::kStateTmem) tmem_st16(tlane + G::kState + c, old);
+        float hi = full[0], lo = full[1];
+        if (cnt - 1 + lead != kChunk) {
+            const double step = decay_pow(ld, cnt - 1 + lead);
+            hi = (float)step;
+            lo = (float)(step - (double)hi);
         }
-        if (G::kStateTmem) tmem_wait_st();
+        if constexpr (G::kStateTmem) {
+#pragma unroll 1
+            for (int c = c0; c < min(c0 + D / 2, nv); c += 16) {
+                uint32_t r[16], old[16];
+                tmem_ld16(tlane + G::kKV + c, r);
+                tmem_ld16(tlane + G::kState + c, old);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float prev = __uint_as_float(old[e]);
+                    old[e] = __float_as_uint(fmaf(prev, hi, fmaf(prev, lo, __uint_as_float(r[e]))));
+                }
+                tmem_st16(tlane + G::kState + c, old);
+                if (!STATE_ONLY) put_row(c, old);
+            }
+            tmem_wait_st();
+        } else {
+            uint32_t r[16];
+            tmem_ld16x256(tlane + G::kKV + c0, r);
+            tmem_wait_ld();
+            // (columns from nv on are not computed: their values stay out of every result)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[i] = fmaf(S[i], hi, fmaf(S[i], lo, __uint_as_float(r[i])));
+            if (!STATE_ONLY) put_pairs();
+        }
     }
     if (!alive && tid == 0) set_status(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
 
@@ -486,28 +658,22 @@ __global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(c
     if (to) {
         const int rs = STATE_ONLY ? w.dv : w.s_rs, cs = STATE_ONLY ? 1 : w.s_cs;
         const float f = !STATE_ONLY && w.out_decay ? dec[1] : 1.f;
+        auto keep = [&](int row, int col, float v) {
+            if (row < w.dk && col < w.dv) to[(long long)row * rs + (long long)col * cs] = f * v;
+        };
+        if constexpr (G::kStateTmem) {
 #pragma unroll 1
-        for (int c = half * (D / 2); c < min((half + 1) * (D / 2), nv); c += 16) {
-            uint32_t r[16];
-            if (G::kStateTmem) {
+            for (int c = c0; c < min(c0 + D / 2, nv); c += 16) {
+                uint32_t r[16];
                 tmem_ld16(tlane + G::kState + c, r);
                 tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) keep(quad * 32 + lane, c + e, __uint_as_float(r[e]));
             }
+        } else {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint4 u[NS];
-                if (!G::kStateTmem) {
-#pragma unroll
-                    for (int j = 0; j < NS; ++j)
-                        u[j] = *reinterpret_cast<const uint4 *>(sm + G::kS + j * G::kSTile + tile_at(D, srow, c / 8 + g));
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int col = c + g * 8 + e;
-                    const float v = G::kStateTmem ? __uint_as_float(r[g * 8 + e]) : term_sum(u, e);
-                    if (has_row && srow < w.dk && col < w.dv) to[(long long)srow * rs + (long long)col * cs] = f * v;
-                }
-            }
+            for (int i = 0; i < 16; ++i)
+                keep(quad * 16 + (lane >> 2) + (i & 2) * 4, c0 + (i >> 2) * 8 + (lane & 3) * 2 + (i & 1), S[i]);
         }
     }
     tc_before_sync();
@@ -519,20 +685,29 @@ __global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(c
 __global__ void la_join_kernel(const __grid_constant__ LaArgs args)
 {
     const LaWalk &w = args.w[blockIdx.z];
-    const int sz = w.dk * w.dv, i = blockIdx.y * blockDim.x + threadIdx.x;
-    const LaSpan s = la_span(args, blockIdx.x * args.nseg);
+    const int sz = w.dk * w.dv, i = blockIdx.y * blockDim.x + threadIdx.x, nseg = args.nseg;
+    const LaSpan s = la_span(args, blockIdx.x * nseg);
+    __shared__ double power[2];   // of a whole segment: the first one, the others
+    if (threadIdx.x < 2)
+        power[threadIdx.x] = decay_pow(args.log_decay[s.h], args.seg_len - 1 + (threadIdx.x ? 1 : w.lead));
+    __syncthreads();
     if (i >= sz) return;
     const long long bh = blockIdx.x;
-    float *seg = w.seg + bh * args.nseg * sz + i;
-    const float ld = args.log_decay[s.h];
+    float *seg = w.seg + bh * nseg * sz + i;
+    // segments before the last one that are whole: their sums exist
+    const int whole = min(nseg - 1, s.L / args.seg_len);
     float carry = w.s_in ? w.s_in[bh * sz + (long long)(i / w.dv) * w.s_rs + (long long)(i % w.dv) * w.s_cs] : 0.f;
-    for (int j = 0; j < args.nseg; ++j) {
-        const long long left = (long long)s.L - (long long)j * args.seg_len;
-        const int len = (int)max(0LL, min(left, (long long)args.seg_len));
-        const bool more = j + 1 < args.nseg && len == args.seg_len;
-        const float add = more ? seg[(long long)j * sz] : 0.f;
-        seg[(long long)j * sz] = carry;
-        if (more) carry = (float)(decay_pow(ld, len - 1 + (j == 0 ? w.lead : 1)) * (double)carry + (double)add);
+    constexpr int U = 8;   // loads in flight
+    for (int j0 = 0; j0 <= whole; j0 += U) {
+        float add[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) add[u] = j0 + u < whole ? seg[(long long)(j0 + u) * sz] : 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (j0 + u > whole) break;
+            seg[(long long)(j0 + u) * sz] = carry;
+            carry = (float)(power[j0 + u > 0] * (double)carry + (double)add[u]);
+        }
     }
 }
 

@@ -8,16 +8,15 @@
 namespace semicrf {
 
 // A tile X[R][D] of 16-bit values lies in shared memory as 8 x 8 blocks: 8 rows of
-// 16 bytes, 128 bytes in all.  Block (r/8, d/8) starts at (d/8) * col + (r/8) * 128,
-// where col = tile_col(R) pads each column of blocks by 16 bytes: eight lanes that
-// write one row's pieces then fall into eight different bank groups.  The same image
-// serves both ways a product can read it:
+// 16 bytes, 128 bytes in all, the blocks of one column of 8 values one after the
+// other: row r, column d at (d/8) * col + r * 16 + (d%8) * 2.  col is 16 R, or
+// tile_col(R) = 16 R + 16 where threads write along rows: eight lanes with one row's
+// pieces then fall into eight different bank groups.  The same image serves both
+// ways a product can read it:
 //   contraction over d (K-major):   row groups 128 apart, k groups col apart
 //   contraction over r (MN-major):  d groups col apart, k groups 128 apart
 // so no tile is ever transposed or kept twice.
 __host__ __device__ constexpr int tile_col(int R) { return R * 16 + 16; }
-__host__ __device__ constexpr int tile_bytes(int R, int D) { return D / 8 * tile_col(R); }
-__device__ __forceinline__ int tile_at(int R, int r, int d8) { return d8 * tile_col(R) + (r >> 3) * 128 + (r & 7) * 16; }
 
 // Descriptor of an unswizzled operand: start address, leading and stride byte
 // offsets in 16-byte units, and the constant 1 in bits 46..48.
@@ -27,17 +26,8 @@ __device__ __forceinline__ uint64_t mma_desc(uint32_t saddr, uint32_t lbo, uint3
            (uint64_t)1 << 46;
 }
 
-// K-major operand: step k (16 values of the contraction) of a tile with R rows.
-__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int R, int k)
-{
-    return mma_desc(tile + 2 * k * tile_col(R), tile_col(R), 128);
-}
-
-// MN-major operand (contraction over the tile's rows): step k (16 rows).
-__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int R, int k)
-{
-    return mma_desc(tile + 2 * k * 128, 128, tile_col(R));
-}
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int col) { return mma_desc(tile, col, 128); }    // K-major
+__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int col) { return mma_desc(tile, 128, col); }   // MN-major
 
 // Instruction descriptor: bf16 x bf16 -> fp32, M x N, operands K-major unless flagged.
 __host__ __device__ constexpr uint32_t mma_idesc(int M, int N, bool a_mn, bool b_mn)
@@ -46,26 +36,40 @@ __host__ __device__ constexpr uint32_t mma_idesc(int M, int N, bool a_mn, bool b
            (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+// The instructions below are issued by one lane (`lead`, from elect_lane) of a warp
+// that runs the code around them as a whole: addresses and descriptors then stay in
+// uniform registers.  Inside a branch of one thread each instruction took 60 to 100
+// cycles to issue, more than it runs.
+__device__ __forceinline__ uint32_t elect_lane()
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
                  : "memory");
 }
 
 // A in tensor memory: row i in lane i, two 16-bit values of the contraction in each column.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
                  : "memory");
 }
 
-__device__ __forceinline__ void mma_commit(uint32_t mbar)
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t mbar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar) : "memory");
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(mbar),
+                 "r"(lead)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols)
@@ -105,6 +109,30 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+                   "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+                   "=r"(r[30]), "=r"(r[31])
+                 : "r"(addr));
+}
+
+// 16 lanes and 32 columns spread over all 32 threads: r[4j + 2a + b] is lane
+// (thread / 4) + 8 a, column 8 j + 2 (thread % 4) + b.
+__device__ __forceinline__ void tmem_ld16x256(uint32_t addr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr));
+}
+
 __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]),
@@ -134,15 +162,33 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t mbar, uint32_t parity
     }
 }
 
-// v = t[0] + t[1] + ... in bf16 terms: each takes the nearest value of what is left,
-// so n terms carry 8 n bits of the float.
+// Two floats as sums of NT bf16 terms, packed (a low, b high).  Each term but the last
+// is the upper half of what is left (8 bits, cut off: no conversion), the last one
+// rounds to nearest.  Three terms hold a float exactly; two leave 2^-17 of it.
 template <int NT>
-__device__ __forceinline__ void bf16_terms(float v, __nv_bfloat16 (&t)[NT])
+__device__ __forceinline__ void split2(float a, float b, uint32_t (&t)[NT])
 {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        t[i] = __float2bfloat16_rn(v);
-        if (i + 1 < NT) v -= __bfloat162float(t[i]);
+    for (int i = 0; i + 1 < NT; ++i) {
+        const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+        t[i] = __byte_perm(ua, ub, 0x7632);
+        a -= __uint_as_float(ua & 0xffff0000u);
+        b -= __uint_as_float(ub & 0xffff0000u);
+    }
+    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+    t[NT - 1] = *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// The floats that NT packed terms stand for.
+template <int NT>
+__device__ __forceinline__ void join2(const uint32_t (&t)[NT], float &a, float &b)
+{
+    a = __uint_as_float(t[NT - 1] << 16);
+    b = __uint_as_float(t[NT - 1] & 0xffff0000u);
+#pragma unroll
+    for (int i = NT - 2; i >= 0; --i) {
+        a += __uint_as_float(t[i] << 16);
+        b += __uint_as_float(t[i] & 0xffff0000u);
     }
 }
 
