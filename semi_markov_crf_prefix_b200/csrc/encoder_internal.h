@@ -86,6 +86,7 @@ struct LaStepArgs {
 
 int la_segments(int B, int T, int H, int dk, int dv, int dtype, int nwalk, int *seg_len);
 cudaError_t launch_la(const LaArgs &a, int dtype, cudaStream_t st, int *launches);
+bool la_tma_walk(const LaArgs &a, int width, bool state_only, cudaStream_t st, int *launches, cudaError_t *e);
 cudaError_t launch_la_step(const LaStepArgs &a, int dtype, cudaStream_t st, int *launches);
 
 // ---- group norm ----

@@ -3,16 +3,11 @@
 // over whole sequences (la_chunk_kernel, la_token_kernel) and for single tokens
 // (la_step_kernel).  The backward runs the same walks with exchanged operands:
 //   dq = walk(dO, V, K)   dv = walk back in time(K, Q, dO)   dk = walk back in time(V, dO, Q).
-#include <math.h>
-
-#include "device_util.cuh"
-#include "encoder_internal.h"
+#include "la_common.cuh"
 #include "tensor_core.cuh"
 
 namespace semicrf {
 namespace {
-
-constexpr int kChunk = 128;     // positions of one step of the chunked walk
 
 template <typename T>
 constexpr int kTerms = sizeof(T) == 4 ? 3 : 1;
@@ -91,78 +86,6 @@ __device__ __forceinline__ void store_terms(unsigned char *at, int tile_stride, 
         *reinterpret_cast<uint4 *>(at + j * tile_stride) = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
 }
 
-// lam^n from the float32 log_decay, exact to float32's rounding at any n (exponents in float64).
-__device__ __forceinline__ double decay_pow(float log_decay, long long n)
-{
-    return n == 0 ? 1.0 : exp((double)log_decay * (double)n);
-}
-
-// One block of the walk: (sequence b, head h, segment seg).
-struct LaSpan {
-    int b, h, seg, L, p0, pe, p1;
-    bool last;
-};
-
-__device__ __forceinline__ LaSpan la_span(const LaArgs &a, int idx)
-{
-    LaSpan s;
-    s.seg = idx % a.nseg;
-    const int bh = idx / a.nseg;
-    s.h = bh % a.H;
-    s.b = bh / a.H;
-    int L = a.T;
-    if (a.lengths) {
-        L = a.lengths[s.b];
-        if (L < 0 || L > a.T) {
-            if (threadIdx.x == 0) set_status(a.status, SEMICRF_ERR_INVALID_LENGTH);
-            L = max(0, min(L, a.T));
-        }
-    }
-    s.L = L;
-    const long long q0 = (long long)s.seg * a.seg_len;
-    s.p0 = (int)min(q0, (long long)a.T);
-    s.p1 = (int)min(q0 + a.seg_len, (long long)a.T);
-    s.pe = max(s.p0, min(s.p1, L));
-    s.last = L == 0 ? s.seg == 0 : (L - 1) / a.seg_len == s.seg;
-    return s;
-}
-
-// Positions behind the sequence's end: zeros.
-template <typename T>
-__device__ __forceinline__ void zero_rows(const LaWalk &w, const LaSpan &s, int d_begin, int d_end)
-{
-    T *o = static_cast<T *>(w.o) + s.b * w.os[0] + s.h * w.os[2];
-    const int n = d_end - d_begin;
-    const int from = max(s.p0, s.L);
-    for (long long i = threadIdx.x; i < (long long)(s.p1 - from) * n; i += blockDim.x)
-        o[(from + i / n) * w.os[1] + d_begin + i % n] = from_f<T>(0.f);
-}
-
-// A sequence without positions hands its state on.
-__device__ __forceinline__ void copy_state(const LaWalk &w, const LaArgs &a, const LaSpan &s, int j0, int j1)
-{
-    if (!w.s_out) return;
-    const long long base = ((long long)s.b * a.H + s.h) * w.dk * w.dv;
-    const int n = j1 - j0;
-    for (int i = threadIdx.x; i < w.dk * n; i += blockDim.x) {
-        const long long at = base + (long long)(i / n) * w.s_rs + (long long)(j0 + i % n) * w.s_cs;
-        w.s_out[at] = w.s_in ? w.s_in[at] : 0.f;
-    }
-}
-
-// Where the walk of this segment takes its state from, element (i, j) at i * rs + j * cs.
-struct StateAt {
-    const float *p;
-    int rs, cs;
-};
-
-__device__ __forceinline__ StateAt state_from(const LaWalk &w, const LaArgs &a, const LaSpan &s)
-{
-    const long long bh = (long long)s.b * a.H + s.h, sz = (long long)w.dk * w.dv;
-    if (w.seg) return {w.seg + (bh * a.nseg + s.seg) * sz, w.dv, 1};
-    return {w.s_in ? w.s_in + bh * sz : nullptr, w.s_rs, w.s_cs};
-}
-
 template <typename T>
 __device__ __forceinline__ Track track_of(const void *base, const long long (&st)[3], int d, int vec, const LaSpan &s,
                                           int reverse)
@@ -227,22 +150,6 @@ __device__ __forceinline__ void bring_pieces(const Track &g, unsigned char *to, 
             *reinterpret_cast<uint4 *>(to + j * ROWS * 16) = *reinterpret_cast<const uint4 *>(&o[0]);
         }
     }
-}
-
-// Products of operands in NA and NB terms: go(x, y, accumulate) for the pairs of terms
-// with x + y < N, the smallest first.
-template <int NA, int NB, int N, typename F>
-__device__ __forceinline__ void mma_terms(F &&go)
-{
-    bool acc = false;
-#pragma unroll
-    for (int sum = N - 1; sum >= 0; --sum)
-#pragma unroll
-        for (int x = 0; x <= sum; ++x)
-            if (x < NA && sum - x < NB) {
-                go(x, sum - x, acc);
-                acc = true;
-            }
 }
 
 // The chunked walk: 128 positions at a time,
@@ -424,23 +331,22 @@ __global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(c
         if (__syncthreads_or(!alive)) break;
 
         if (!STATE_ONLY) {
-            if (warp == 0) {
+            if (warp == 0 && elect_lane()) {
                 tc_after_sync();
-                const uint32_t lead1 = elect_lane();
                 const uint32_t i1 = mma_idesc(128, 128, false, false), i2 = mma_idesc(128, nv, false, true);
                 const uint64_t dq = desc_k(smem + G::kQ, G::kCol), dk = desc_k(smem + G::kK, G::kCol);
                 const uint64_t ds = desc_mn(smem + G::kS, G::kSCol);
                 mma_terms<NI, NI, NI>([&](int x, int y, bool acc) {
 #pragma unroll 1
                     for (int k = 0; k < kd; ++k, acc = true)
-                        mma_ss(lead1, tm, dq + x * kTileD + k * kCol2, dk + y * kTileD + k * kCol2, i1, acc);
+                        mma_ss(tm, dq + x * kTileD + k * kCol2, dk + y * kTileD + k * kCol2, i1, acc);
                 });
                 mma_terms<NI, NM, NM>([&](int x, int y, bool acc) {
 #pragma unroll 1
                     for (int k = 0; k < kd; ++k, acc = true)
-                        mma_ss(lead1, tm + G::kO, dq + x * kTileD + k * kCol2, ds + y * kSTileD + k * kRow2, i2, acc);
+                        mma_ss(tm + G::kO, dq + x * kTileD + k * kCol2, ds + y * kSTileD + k * kRow2, i2, acc);
                 });
-                mma_commit(lead1, bar1);
+                mma_commit(bar1);
             }
             // the next queries travel while the scores are formed; then their tile is free
             Piece<T> rq[kDirect ? 1 : NP];
@@ -486,17 +392,16 @@ __global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(c
             smem_to_mma();
             __syncthreads();
         }
-        if (warp == 0) {
+        if (warp == 0 && elect_lane()) {
             tc_after_sync();
-            const uint32_t lead1 = elect_lane();
             const uint32_t i4 = mma_idesc(D, nv, true, true);
             const uint64_t dk = desc_mn(smem + G::kK, G::kCol), dv = desc_mn(smem + G::kV, G::kCol);
             mma_terms<NK, NI, NK>([&](int x, int y, bool acc) {
 #pragma unroll 1
                 for (int k = 0; k < kChunk / 16; ++k, acc = true)
-                    mma_ss(lead1, tm + G::kKV, dk + x * kTileD + k * kRow2, dv + y * kTileD + k * kRow2, i4, acc);
+                    mma_ss(tm + G::kKV, dk + x * kTileD + k * kRow2, dv + y * kTileD + k * kRow2, i4, acc);
             });
-            if (STATE_ONLY) mma_commit(lead1, bar2);
+            if (STATE_ONLY) mma_commit(bar2);
         }
         float qs[!STATE_ONLY && G::kKeep ? D / 2 : 1];
         if (!STATE_ONLY) {
@@ -548,18 +453,17 @@ __global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(c
             tmem_wait_st();
             tc_before_sync();
             __syncthreads();
-            if (warp == 0) {
+            if (warp == 0 && elect_lane()) {
                 tc_after_sync();
-                const uint32_t lead1 = elect_lane();
                 const uint32_t i3 = mma_idesc(128, nv, false, true);
                 const uint64_t dv = desc_mn(smem + G::kV, G::kCol);
                 mma_terms<NM, NI, NM>([&](int x, int y, bool acc) {
                     acc |= !G::kKeep;
 #pragma unroll 1
                     for (int k = 0; k < kChunk / 16; ++k, acc = true)
-                        mma_ts(lead1, tm + G::kO, tm + G::kP + k * (8 * NM) + x * 8, dv + y * kTileD + k * kRow2, i3, acc);
+                        mma_ts(tm + G::kO, tm + G::kP + k * (8 * NM) + x * 8, dv + y * kTileD + k * kRow2, i3, acc);
                 });
-                mma_commit(lead1, bar2);
+                mma_commit(bar2);
             }
         }
         if constexpr (!kDirect)
@@ -873,16 +777,6 @@ __global__ __launch_bounds__(256) void la_step_kernel(const __grid_constant__ La
     }
 }
 
-template <typename F>
-cudaError_t timed_launch(cudaStream_t st, int *n, F &&go)
-{
-    prof_before(st);
-    go();
-    prof_after(st);
-    ++*n;
-    return cudaGetLastError();
-}
-
 // Which walk serves these widths: the padded width of the chunked walk (64 or 128), or 0
 // for the token walk.  Chunk tiles hold kTerms terms of q, k, v: 128 columns fit an SM's
 // shared memory in one term (bf16) only.
@@ -919,6 +813,10 @@ cudaError_t go_token(const LaArgs &a, cudaStream_t st, int *n)
 template <typename T, bool STATE_ONLY>
 cudaError_t go_walk(const LaArgs &a, int width, cudaStream_t st, int *n)
 {
+    if constexpr (sizeof(T) == 2 && kTerms<T> == 1) {
+        cudaError_t e;
+        if (width && la_tma_walk(a, width, STATE_ONLY, st, n, &e)) return e;
+    }
     if (width == 64) return go_chunk<T, 64, STATE_ONLY>(a, st, n);
     if constexpr (sizeof(T) == 2 && kTerms<T> == 1)
         if (width == 128) return go_chunk<T, 128, STATE_ONLY>(a, st, n);

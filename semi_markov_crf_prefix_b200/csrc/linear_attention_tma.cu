@@ -1,0 +1,606 @@
+// linear_attention_tma.cu -- the chunked walk of linear attention for bf16 operands that
+// the copy engine can address (16-byte aligned rows and strides).
+//
+// Eight warps compute, a ninth issues: it alone starts copies and matrix instructions,
+// so that neither a full queue of the matrix unit nor a full queue of loads holds up a
+// warp that has arithmetic to do.  A chunk of 128 positions:
+//
+//   copies   Q, K, V tiles, each fetched again as soon as its last reader is done
+//   matrix   o = Q S  |  KV = K~^T V                 |  o += P V            next scores = Q K^T
+//   warps    K~       |  P from the scores, o scaled |  S = lam^128 S + KV, o out  |
+//
+// with K~ = c lam^{end-i} K and P = b c lam^{i-j} scores; between the bars all warps meet.
+// Two blocks share an SM at width 64 (112 KB of tiles, 256 columns of tensor memory
+// each), one computing while the other waits.  Accumulators hold one chunk's sums only:
+// they round towards zero, which the state, float32 in registers (tensor memory at
+// width 128), must not.
+//
+// A walk against time takes a chunk's rows in memory order too: row r is position
+// 127 - r of the chunk, and the tables of decays are mirrored.
+#include <cuda.h>
+
+#include "la_common.cuh"
+#include "tensor_core.cuh"
+
+namespace semicrf {
+namespace {
+
+constexpr int kWorkers = 256, kThreads = kWorkers + 32;
+
+struct LaMaps {
+    struct {
+        CUtensorMap q, k, v, o;
+    } w[3];
+};
+
+struct LaTables {
+    float diag[64];   // b c lam^d by 31 + (row - column) inside a 32 x 32 block, 0 where the column lies ahead
+    float side[32];   // by column: the rest of lam^d in the blocks beside the diagonal
+    float block[4];   // lam^{32 m}
+    float full[2];    // lam^128 in two floats
+};
+
+template <int D>
+struct TmaCfg {
+    static constexpr int NM = 2, NK = 3;            // terms of P and S, and of K~ (see the register form)
+    static constexpr int kTile = D / 64 * 16384;    // 128 rows
+    static constexpr int kSTile = D * D * 2;
+    static constexpr bool kApart = D == 64;         // K has a tile of its own beside K~, or becomes K~'s first term
+    static constexpr bool kStateTmem = D == 128;
+    static constexpr int kQ = 0, kK = kQ + kTile, kKt = kApart ? kK + kTile : kK, kV = kKt + NK * kTile,
+                         kS = kV + kTile, kTab = kS + NM * kSTile, kBars = kTab + (int)sizeof(LaTables),
+                         kSmem = kBars + 64;
+    static constexpr int kO = 128, kKV = kO + D, kCols = D == 64 ? 256 : 512;
+    static constexpr int kState = kKV + (kStateTmem ? D : 0);
+    static constexpr int kOut = kKt + 2 * kTile;    // outputs on their way: K~'s third term
+    static constexpr int NP = kChunk * (D / 8) / kWorkers, kRows = kWorkers / (D / 8);
+    static constexpr int kBlocks = D == 64 ? 2 : 1;
+    static_assert(kSmem <= (kBlocks == 2 ? 113 : 227) * 1024, "shared memory");
+};
+
+template <int D, bool STATE_ONLY>
+__global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(const __grid_constant__ LaArgs args,
+                                                                             const __grid_constant__ LaMaps maps)
+{
+    using G = TmaCfg<D>;
+    using T = __nv_bfloat16;
+    constexpr int NM = G::NM, NK = G::NK, NP = G::NP;
+    constexpr uint64_t kTileD = G::kTile >> 4, kSTileD = G::kSTile >> 4, kRow16 = 2048 >> 4;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const LaWalk &w = args.w[blockIdx.y];
+    const LaSpan s = la_span(args, blockIdx.x);
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    if (STATE_ONLY && s.seg == args.nseg - 1) return;
+    if (!STATE_ONLY) {
+        zero_rows<T>(w, s, 0, w.dv);
+        if (s.L == 0 && s.last) copy_state(w, args, s, 0, w.dv);
+    }
+    if (s.pe == s.p0) return;
+
+    LaTables &tab = *reinterpret_cast<LaTables *>(sm + G::kTab);
+    uint32_t *slot = reinterpret_cast<uint32_t *>(sm + G::kBars + 56);
+    const uint32_t smem = static_cast<uint32_t>(__cvta_generic_to_shared(sm)), bars = smem + G::kBars;
+    const uint32_t full_q = bars, full_k = bars + 8, full_v = bars + 16;
+    const uint32_t done_qk = bars + 24, done_qs = bars + 32, done_kv = bars + 40, done_pv = bars + 48;
+    const float ld = args.log_decay[s.h], pa = w.b * w.c;
+    const int rev = w.reverse;
+    if (warp == 8) {
+        tmem_alloc(static_cast<uint32_t>(__cvta_generic_to_shared(slot)), G::kCols);
+        if (lane == 0) {
+            for (int i = 0; i < 7; ++i) mbar_init(bars + 8 * i, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+    } else if (tid < 64) {
+        const int d = rev ? 31 - tid : tid - 31;
+        tab.diag[tid] = d >= 0 && tid < 63 ? (float)(decay_pow(ld, d) * (double)pa) : 0.f;
+    } else if (tid < 96) {
+        tab.side[tid - 64] = (float)decay_pow(ld, rev ? tid - 64 : 95 - tid);
+    } else if (tid < 100) {
+        tab.block[tid - 96] = (float)decay_pow(ld, 32 * (tid - 96));
+    } else if (tid == 100) {
+        const double v = decay_pow(ld, kChunk);
+        tab.full[0] = (float)v;
+        tab.full[1] = (float)(v - (double)tab.full[0]);
+    }
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tm = __shfl_sync(0xffffffffu, *slot, 0);
+    const int nv = (w.dv + 15) / 16 * 16, kd = (w.dk + 15) / 16;
+    const int chunks = (s.pe - s.p0 + kChunk - 1) / kChunk, whole = (s.pe - s.p0) / kChunk;
+    // first row in memory of chunk n
+    auto row_of = [&](int n) { return rev ? s.L - s.p0 - (n + 1) * kChunk : s.p0 + n * kChunk; };
+    bool alive = true;
+
+    if (warp == 8) {
+        const bool lead = elect_lane();
+        const auto &map = maps.w[blockIdx.y];
+        // (all of these in a branch of the leading lane)
+        auto await = [&](uint32_t bar, uint32_t parity) { alive = mbar_wait_bounded(bar, parity) && alive; };
+        auto fetch = [&](const CUtensorMap &m, int tile, uint32_t bar, int n) {
+            mbar_expect(bar, G::kTile);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+                tma_load(smem + tile + c * 16384, &m, c * 64, s.h, row_of(n), s.b, bar);
+        };
+        auto scores = [&](int n) {   // Q K^T of chunk n
+            if (n < whole) {
+                await(full_q, n & 1);
+                await(full_k, n & 1);
+            }
+            tc_after_sync();
+            const uint64_t dq = desc_swz(smem + G::kQ, 16), dk = desc_swz(smem + G::kK, 16);
+#pragma unroll 1
+            for (int k = 0; k < kd; ++k) {
+                const uint64_t at = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                mma_ss(tm, dq + at, dk + at, mma_idesc(128, 128, false, false), k > 0);
+            }
+            mma_commit(done_qk);
+        };
+        // the warp whole again, then all warps: false once a wait has run out
+        auto meet = [&] {
+            __syncwarp();
+            return !__syncthreads_or(!alive);
+        };
+        if (lead && whole > 0) {
+            if (!STATE_ONLY) fetch(map.q, G::kQ, full_q, 0);
+            fetch(map.k, G::kK, full_k, 0);
+            fetch(map.v, G::kV, full_v, 0);
+            if (!STATE_ONLY && G::kApart) scores(0);
+        }
+        if (!STATE_ONLY) meet();   // the state's terms are there
+        for (int n = 0; n < chunks; ++n) {
+            const uint32_t parity = n & 1;
+            const bool next = n + 1 < whole;
+            if (!STATE_ONLY) {
+                if (n >= whole && !meet()) break;   // the shorter chunk's tiles are there
+                if (lead) {
+                    if (n >= whole || !G::kApart) scores(n);
+                    tc_after_sync();
+                    const uint32_t i2 = mma_idesc(128, nv, false, true);
+                    const uint64_t dq = desc_swz(smem + G::kQ, 16), ds = desc_swz(smem + G::kS, 16384);
+#pragma unroll 1
+                    for (int i = 0; i < 2 * kd; ++i) {   // the state's second term first
+                        const int k = i < kd ? i : i - kd;
+                        const uint64_t at = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                        mma_ss(tm + G::kO, dq + at, ds + (i < kd ? kSTileD : 0) + k * kRow16, i2, i > 0);
+                    }
+                    mma_commit(done_qs);
+                    tma_store_read();   // K~'s third term is free again
+                }
+                if (!meet()) break;
+                if (lead && next) {
+                    await(done_qs, parity);
+                    fetch(map.q, G::kQ, full_q, n + 1);
+                }
+            }
+            if (!meet()) break;   // K~ is there
+            if (lead) {
+                if (G::kApart && next) fetch(map.k, G::kK, full_k, n + 1);
+                if (n < whole) await(full_v, parity);
+                tc_after_sync();
+                const uint32_t i4 = mma_idesc(D, nv, true, true);
+                const uint64_t dk = desc_swz(smem + G::kKt, 16384), dv = desc_swz(smem + G::kV, 16384);
+#pragma unroll
+                for (int x = NK - 1; x >= 0; --x)
+#pragma unroll 1
+                    for (int k = 0; k < kChunk / 16; ++k)
+                        mma_ss(tm + G::kKV, dk + x * kTileD + k * kRow16, dv + k * kRow16, i4, x < NK - 1 || k > 0);
+                mma_commit(done_kv);
+                if (STATE_ONLY && next) {
+                    await(done_kv, parity);
+                    if (!G::kApart) fetch(map.k, G::kK, full_k, n + 1);
+                    fetch(map.v, G::kV, full_v, n + 1);
+                }
+            }
+            if (STATE_ONLY) continue;
+            if (!meet()) break;   // P is there, o scaled
+            if (lead) {
+                tc_after_sync();
+                const uint32_t i3 = mma_idesc(128, nv, false, true);
+                const uint64_t dv = desc_swz(smem + G::kV, 16384);
+#pragma unroll
+                for (int x = NM - 1; x >= 0; --x)
+#pragma unroll 1
+                    for (int k = 0; k < kChunk / 16; ++k)
+                        mma_ts(tm + G::kO, tm + k * (8 * NM) + x * 8, dv + k * kRow16, i3, true);
+                mma_commit(done_pv);
+                if (next) {
+                    if (!G::kApart) {
+                        await(done_kv, parity);
+                        fetch(map.k, G::kK, full_k, n + 1);
+                    }
+                    await(done_pv, parity);   // P is read: its columns take the next scores
+                    fetch(map.v, G::kV, full_v, n + 1);
+                    if (G::kApart) scores(n + 1);
+                }
+            }
+            if (!meet()) break;   // this chunk's outputs lie in shared memory, the next state's terms too
+            if (lead && n < whole) {
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    tma_store(smem + G::kOut + c * 16384, &map.o, c * 64, s.h, row_of(n), s.b);
+                tma_store_commit();
+            }
+        }
+        if (lead) {
+            tma_store_done();
+            if (!alive) set_status(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
+        }
+        __syncwarp();
+    } else {
+        auto await = [&](uint32_t bar, uint32_t parity) {
+            alive = mbar_wait_bounded(bar, parity) && alive;
+            __syncwarp();
+        };
+        const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane, c0 = half * (D / 2);
+        const uint32_t tlane = tm + ((uint32_t)(quad * 32) << 16);
+        // pieces of K this thread turns into K~: column piece j8 of rows r0, r0 + kRows, ...
+        const int r0 = tid / (D / 8), j8 = tid % (D / 8);
+        const int at0 = (j8 >> 3) * 16384 + swz(r0, j8 & 7);   // (kRows is a multiple of 8)
+        float wk[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int far = rev ? r0 + i * G::kRows : kChunk - 1 - r0 - i * G::kRows;   // positions to the chunk's end
+            const int low = far & 31;
+            wk[i] = w.c * tab.side[rev ? low : 31 - low] * tab.block[far >> 5];
+        }
+        const float beside = pa * (float)decay_pow(ld, rev ? 32 - lane : lane + 1);
+        const float ofull = w.b * (float)decay_pow(ld, (rev ? kChunk - 1 - row : row) + 1);
+
+        float S[G::kStateTmem ? 1 : 16];
+        auto put_pairs = [&] {   // D = 64: rows quad * 16 + lane / 4 (+ 8), column pairs c0 + 8 j + 2 (lane % 4)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    uint32_t t[NM];
+                    split2<NM>(S[4 * j + 2 * a], S[4 * j + 2 * a + 1], t);
+                    unsigned char *to = sm + G::kS + swz(quad * 16 + (lane >> 2) + 8 * a, half * 4 + j) + 4 * (lane & 3);
+#pragma unroll
+                    for (int x = 0; x < NM; ++x) *reinterpret_cast<uint32_t *>(to + x * G::kSTile) = t[x];
+                }
+        };
+        auto put_row = [&](int c, const uint32_t (&r)[16]) {   // D = 128: columns c .. c + 15 of row `row`
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                uint32_t o[NM][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t t[NM];
+                    split2<NM>(__uint_as_float(r[8 * g + 2 * e]), __uint_as_float(r[8 * g + 2 * e + 1]), t);
+#pragma unroll
+                    for (int x = 0; x < NM; ++x) o[x][e] = t[x];
+                }
+                const int p = c / 8 + g;
+#pragma unroll
+                for (int x = 0; x < NM; ++x)
+                    *reinterpret_cast<uint4 *>(sm + G::kS + x * G::kSTile + (p >> 3) * 16384 + swz(row, p & 7)) =
+                        make_uint4(o[x][0], o[x][1], o[x][2], o[x][3]);
+            }
+        };
+        {
+            const StateAt from = STATE_ONLY ? StateAt{nullptr, 0, 0} : state_from(w, args, s);
+            auto given = [&](int i, int j) {
+                return from.p && i < w.dk && j < w.dv ? from.p[(long long)i * from.rs + (long long)j * from.cs] : 0.f;
+            };
+            if constexpr (G::kStateTmem) {
+#pragma unroll 1
+                for (int c = c0; c < c0 + D / 2; c += 16) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(given(row, c + e));
+                    tmem_st16(tlane + G::kState + c, r);
+                    if (!STATE_ONLY) put_row(c, r);
+                }
+                tmem_wait_st();
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    S[i] = given(quad * 16 + (lane >> 2) + (i & 2) * 4, c0 + (i >> 2) * 8 + (lane & 3) * 2 + (i & 1));
+                if (!STATE_ONLY) put_pairs();
+            }
+        }
+
+        if (!STATE_ONLY) {
+            smem_to_mma();
+            __syncthreads_or(!alive);
+        }
+        for (int n = 0; n < chunks; ++n) {
+            const uint32_t parity = n & 1;
+            const int cnt = min(kChunk, s.pe - s.p0 - n * kChunk);
+            const bool is_whole = n < whole;
+            if (!is_whole) {
+                // the last, shorter chunk: rows outside the sequence have to be zeros
+                auto bring = [&](const void *base, const long long (&st)[3], int d, int tile) {
+                    const T *p = static_cast<const T *>(base) + s.b * st[0] + s.h * st[2] + (long long)j8 * 8;
+#pragma unroll 1
+                    for (int i = 0; i < NP; ++i) {
+                        const int r = r0 + i * G::kRows, pos = rev ? kChunk - 1 - r : r;
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (pos < cnt && j8 * 8 < d) v = *reinterpret_cast<const uint4 *>(p + (row_of(n) + r) * st[1]);
+                        *reinterpret_cast<uint4 *>(sm + tile + at0 + i * G::kRows * 128) = v;
+                    }
+                };
+                if (!STATE_ONLY) bring(w.q, w.qs, w.dk, G::kQ);
+                bring(w.k, w.ks, w.dk, G::kK);
+                bring(w.v, w.vs, w.dv, G::kV);
+            }
+            if (!STATE_ONLY && !is_whole) {
+                smem_to_mma();
+                if (__syncthreads_or(!alive)) break;
+            }
+            const int lead = s.p0 + n == 0 ? w.lead : 1;
+            if (is_whole) await(full_k, parity);
+            if (!G::kApart && !STATE_ONLY) await(done_qk, parity);   // K~ replaces K
+            uint4 third[NP];   // K~'s third term, whose tile the last outputs may still be leaving
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const unsigned char *at = sm + G::kK + at0 + i * G::kRows * 128;
+                const uint4 u = *reinterpret_cast<const uint4 *>(at);
+                float f = wk[i];
+                if (!is_whole) {
+                    const int r = r0 + i * G::kRows, pos = rev ? kChunk - 1 - r : r;
+                    f = pos < cnt ? w.c * (float)decay_pow(ld, cnt - 1 - pos) : 0.f;
+                }
+                uint32_t o[NK][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t v = reinterpret_cast<const uint32_t *>(&u)[e];
+                    uint32_t t[NK];
+                    split2<NK>(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f, t);
+#pragma unroll
+                    for (int x = 0; x < NK; ++x) o[x][e] = t[x];
+                }
+#pragma unroll
+                for (int x = 0; x < NK; ++x) {
+                    const uint4 v = make_uint4(o[x][0], o[x][1], o[x][2], o[x][3]);
+                    if (x == 2 && !STATE_ONLY)
+                        third[i] = v;
+                    else
+                        *reinterpret_cast<uint4 *>(sm + G::kKt + x * G::kTile + at0 + i * G::kRows * 128) = v;
+                }
+            }
+            if (!STATE_ONLY) {
+                if (__syncthreads_or(!alive)) break;
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+                    *reinterpret_cast<uint4 *>(sm + G::kKt + 2 * G::kTile + at0 + i * G::kRows * 128) = third[i];
+            }
+            smem_to_mma();
+            if (__syncthreads_or(!alive)) break;
+
+            if (!STATE_ONLY) {
+                if (G::kApart) await(done_qk, parity);
+                tc_after_sync();
+                // scores -> P: 32 columns at a time, 16 scores becoming 8 columns of each term
+#pragma unroll 1
+                for (int c = half * 64; c < half * 64 + 64; c += 32) {
+                    const int away = rev ? c / 32 - quad : quad - c / 32;
+                    uint32_t r[32];
+                    if (away >= 0) {
+                        tmem_ld32(tlane + c, r);
+                        tmem_wait_ld();
+                    }
+                    if (away > 0) {
+                        const float g = beside * tab.block[away - 1];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * (g * tab.side[e]));
+                    } else if (away == 0) {
+                        const float *f = tab.diag + 31 + lane;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f[-e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) r[e] = 0;
+                    }
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        uint32_t o[NM][8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            uint32_t t[NM];
+                            split2<NM>(__uint_as_float(r[16 * g + 2 * e]), __uint_as_float(r[16 * g + 2 * e + 1]), t);
+#pragma unroll
+                            for (int x = 0; x < NM; ++x) o[x][e] = t[x];
+                        }
+#pragma unroll
+                        for (int x = 0; x < NM; ++x) tmem_st8(tlane + (c / 16 + g) * (8 * NM) + x * 8, o[x]);
+                    }
+                }
+                // o starts as b lam^{i+1} q S
+                await(done_qs, parity);
+                tc_after_sync();
+                const float f = lead ? ofull : w.b * (float)decay_pow(ld, rev ? kChunk - 1 - row : row);
+#pragma unroll 1
+                for (int c = 0; c < D / 2; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(tlane + G::kO + c0 + c, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                    tmem_st16(tlane + G::kO + c0 + c, r);
+                }
+                tmem_wait_st();
+                tc_before_sync();
+                if (__syncthreads_or(!alive)) break;
+            }
+            await(done_kv, parity);
+            tc_after_sync();
+            // S = lam^n S + KV; the float32 rounding of lam^n alone would bias a state that
+            // lives for many chunks: two parts
+            float hi = tab.full[0], lo = tab.full[1];
+            if (cnt - 1 + lead != kChunk) {
+                const double step = decay_pow(ld, cnt - 1 + lead);
+                hi = (float)step;
+                lo = (float)(step - (double)hi);
+            }
+            if constexpr (G::kStateTmem) {
+#pragma unroll 1
+                for (int c = c0; c < min(c0 + D / 2, nv); c += 16) {
+                    uint32_t r[16], old[16];
+                    tmem_ld16(tlane + G::kKV + c, r);
+                    tmem_ld16(tlane + G::kState + c, old);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float prev = __uint_as_float(old[e]);
+                        old[e] = __float_as_uint(fmaf(prev, hi, fmaf(prev, lo, __uint_as_float(r[e]))));
+                    }
+                    tmem_st16(tlane + G::kState + c, old);
+                    if (!STATE_ONLY) put_row(c, old);
+                }
+                tmem_wait_st();
+                tc_before_sync();
+            } else {
+                uint32_t r[16];
+                tmem_ld16x256(tlane + G::kKV + c0, r);
+                tmem_wait_ld();
+                tc_before_sync();
+                // (columns from nv on are not computed: their values stay out of every result)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[i] = fmaf(S[i], hi, fmaf(S[i], lo, __uint_as_float(r[i])));
+                if (!STATE_ONLY) put_pairs();
+            }
+            if (!STATE_ONLY) {
+                await(done_pv, parity);
+                tc_after_sync();
+#pragma unroll 1
+                for (int c = 0; c < D / 2; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(tlane + G::kO + c0 + c, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[8 * g + 2 * e]),
+                                                                          __uint_as_float(r[8 * g + 2 * e + 1]));
+                            o[e] = *reinterpret_cast<const uint32_t *>(&v);
+                        }
+                        const int p = (c0 + c) / 8 + g;
+                        *reinterpret_cast<uint4 *>(sm + G::kOut + (p >> 3) * 16384 + swz(row, p & 7)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                smem_to_mma();
+                tc_before_sync();
+                if (__syncthreads_or(!alive)) break;
+                if (!is_whole && j8 * 8 < w.dv) {
+                    T *o = static_cast<T *>(w.o) + s.b * w.os[0] + s.h * w.os[2] + (long long)j8 * 8;
+#pragma unroll 1
+                    for (int i = 0; i < NP; ++i) {
+                        const int r = r0 + i * G::kRows, pos = rev ? kChunk - 1 - r : r;
+                        if (pos < cnt)
+                            *reinterpret_cast<uint4 *>(o + (row_of(n) + r) * w.os[1]) =
+                                *reinterpret_cast<const uint4 *>(sm + G::kOut + at0 + i * G::kRows * 128);
+                    }
+                }
+            }
+        }
+
+        // the state behind the last position (or behind this segment)
+        const long long bh = (long long)s.b * args.H + s.h, sz = (long long)w.dk * w.dv;
+        float *to = STATE_ONLY ? w.seg + (bh * args.nseg + s.seg) * sz : s.last && w.s_out ? w.s_out + bh * sz : nullptr;
+        if (to) {
+            const int rs = STATE_ONLY ? w.dv : w.s_rs, cs = STATE_ONLY ? 1 : w.s_cs;
+            const float f = !STATE_ONLY && w.out_decay ? (float)decay_pow(ld, 1) : 1.f;
+            auto keep = [&](int i, int j, float v) {
+                if (i < w.dk && j < w.dv) to[(long long)i * rs + (long long)j * cs] = f * v;
+            };
+            if constexpr (G::kStateTmem) {
+#pragma unroll 1
+                for (int c = c0; c < min(c0 + D / 2, nv); c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(tlane + G::kState + c, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) keep(row, c + e, __uint_as_float(r[e]));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    keep(quad * 16 + (lane >> 2) + (i & 2) * 4, c0 + (i >> 2) * 8 + (lane & 3) * 2 + (i & 1), S[i]);
+            }
+        }
+        if (!alive && tid == 0) set_status(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
+    }
+    tc_before_sync();
+    __syncthreads();
+    if (warp == 8) tmem_free(tm, G::kCols);
+}
+
+using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                            const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+Encode encoder()
+{
+    static const Encode fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<Encode>(p);
+    }();
+    return fn;
+}
+
+// The map of a [B][T][H][d] operand: boxes of 64 columns and 128 positions of one head.
+bool make_map(CUtensorMap *m, const void *p, const long long (&st)[3], int d, const LaArgs &a)
+{
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)a.H, (cuuint64_t)a.T, (cuuint64_t)a.B};
+    const cuuint64_t strides[3] = {(cuuint64_t)st[2] * 2, (cuuint64_t)st[1] * 2, (cuuint64_t)st[0] * 2};
+    const cuuint32_t box[4] = {64, 1, kChunk, 1}, step[4] = {1, 1, 1, 1};
+    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, step,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool STATE_ONLY>
+cudaError_t go(const LaArgs &a, const LaMaps &maps, cudaStream_t st, int *n)
+{
+    using G = TmaCfg<D>;
+    return timed_launch(st, n, [&] {
+        la_tma_kernel<D, STATE_ONLY><<<dim3(a.B * a.H * a.nseg, a.nwalk), kThreads, G::kSmem, st>>>(a, maps);
+    });
+}
+
+template <int D, bool STATE_ONLY>
+cudaError_t allow_smem()
+{
+    return cudaFuncSetAttribute(la_tma_kernel<D, STATE_ONLY>, cudaFuncAttributeMaxDynamicSharedMemorySize, TmaCfg<D>::kSmem);
+}
+
+}  // namespace
+
+// False where the copy engine cannot address an operand (nothing is launched then).
+bool la_tma_walk(const LaArgs &a, int width, bool state_only, cudaStream_t st, int *n, cudaError_t *e)
+{
+    if (!encoder()) return false;
+    // (also binds the device's context to a thread that makes its first call, which the
+    // driver's encoder wants: the backward pass runs in a thread of its own)
+    *e = width == 64 ? (state_only ? allow_smem<64, true>() : allow_smem<64, false>())
+                     : (state_only ? allow_smem<128, true>() : allow_smem<128, false>());
+    if (*e != cudaSuccess) return true;
+    LaMaps maps;
+    for (int i = 0; i < a.nwalk; ++i) {
+        const LaWalk &w = a.w[i];
+        if (!w.q_vec || !w.k_vec || !w.v_vec || !w.o_vec) return false;
+        auto &m = maps.w[i];
+        if (!make_map(&m.q, w.q, w.qs, w.dk, a) || !make_map(&m.k, w.k, w.ks, w.dk, a) ||
+            !make_map(&m.v, w.v, w.vs, w.dv, a) || !make_map(&m.o, w.o, w.os, w.dv, a))
+            return false;
+    }
+    if (width == 64)
+        *e = state_only ? go<64, true>(a, maps, st, n) : go<64, false>(a, maps, st, n);
+    else
+        *e = state_only ? go<128, true>(a, maps, st, n) : go<128, false>(a, maps, st, n);
+    return true;
+}
+
+}  // namespace semicrf

@@ -29,6 +29,16 @@ __device__ __forceinline__ uint64_t mma_desc(uint32_t saddr, uint32_t lbo, uint3
 __device__ __forceinline__ uint64_t desc_k(uint32_t tile, int col) { return mma_desc(tile, col, 128); }    // K-major
 __device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int col) { return mma_desc(tile, 128, col); }   // MN-major
 
+// Tiles that the copy engine writes: 64 columns (128 bytes) a row, the 16-byte pieces
+// of row r exchanged by r % 8 (128-byte swizzle), 8 rows to 1024 bytes; wider tiles are
+// several of them.  Both readings again, steps along k within a tile: K-major 32 bytes
+// for 16 columns, MN-major 2048 bytes for 16 rows (the next 64 columns `wide` apart).
+__device__ __forceinline__ int swz(int r, int piece) { return r * 128 + ((piece ^ (r & 7)) << 4); }
+__device__ __forceinline__ uint64_t desc_swz(uint32_t tile, int wide)
+{
+    return mma_desc(tile, wide, 1024) | (uint64_t)2 << 61;
+}
+
 // Instruction descriptor: bf16 x bf16 -> fp32, M x N, operands K-major unless flagged.
 __host__ __device__ constexpr uint32_t mma_idesc(int M, int N, bool a_mn, bool b_mn)
 {
@@ -36,40 +46,37 @@ __host__ __device__ constexpr uint32_t mma_idesc(int M, int N, bool a_mn, bool b
            (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
 }
 
-// The instructions below are issued by one lane (`lead`, from elect_lane) of a warp
-// that runs the code around them as a whole: addresses and descriptors then stay in
-// uniform registers.  Inside a branch of one thread each instruction took 60 to 100
-// cycles to issue, more than it runs.
-__device__ __forceinline__ uint32_t elect_lane()
+// The instructions below belong to one thread: they stand in a branch of the lane that
+// elect_lane names, with the warp whole before and behind it.  (Under a predicate of
+// the whole warp instead, a commit after a loop that one lane had left late signalled
+// its barrier twice.)
+__device__ __forceinline__ bool elect_lane()
 {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r;
+    return r != 0;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
 {
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
                  : "memory");
 }
 
 // A in tensor memory: row i in lane i, two 16-bit values of the contraction in each column.
-__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
 {
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
                  : "memory");
 }
 
-__device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t mbar)
+__device__ __forceinline__ void mma_commit(uint32_t mbar)
 {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(mbar),
-                 "r"(lead)
-                 : "memory");
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar) : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols)
@@ -144,6 +151,32 @@ __device__ __forceinline__ void mbar_init(uint32_t mbar, uint32_t count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(mbar), "r"(count) : "memory");
 }
+
+__device__ __forceinline__ void mbar_expect(uint32_t mbar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mbar), "r"(bytes) : "memory");
+}
+
+// One box of a tensor [b][t][h][column] to shared memory, and back.
+__device__ __forceinline__ void tma_load(uint32_t dst, const void *map, int col, int h, int t, int b, uint32_t mbar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+                 "l"(map), "r"(col), "r"(h), "r"(t), "r"(b), "r"(mbar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_store(uint32_t src, const void *map, int col, int h, int t, int b)
+{
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(map),
+                 "r"(src), "r"(col), "r"(h), "r"(t), "r"(b)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// the shared memory of every committed store may be written again / the stores are done
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Waits for the phase of `parity`; false once 2^31 cycles (about a second) have passed.
 __device__ __forceinline__ bool mbar_wait_bounded(uint32_t mbar, uint32_t parity)
