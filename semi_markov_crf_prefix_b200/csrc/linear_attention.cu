@@ -850,17 +850,21 @@ cudaError_t go_step(const LaStepArgs &a, cudaStream_t st, int *n)
 
 }  // namespace
 
-// Segments of each sequence: one where the sequences and heads alone fill the GPU,
-// else enough for two blocks an SM, of 512 positions or more.  A split walk reads K and
-// V twice (once for each segment's own state).
+// Segments of each sequence, which walk side by side: a split walk first forms what each
+// segment adds to the state (K and V read twice), so it pays where the sequences and
+// heads leave most of the GPU idle.  Blocks that share an SM (two at width 64 in bf16)
+// take 4.6 us a chunk and 1.8 us for the state alone, one by itself 3.2 us: three
+// segments are the fewest that gain (100 000 positions of 8 heads: 151 us in 36 segments,
+// 209 us in 18; 4000 positions of 128 heads: 115 us in two, 102 us in one).  One block an
+// SM elsewhere (4.6 and 3.0 us a chunk at width 128): two gain.
 int la_segments(int B, int T, int H, int dk, int dv, int dtype, int nwalk, int *seg_len)
 {
     const int width = la_width(dk, dv, dtype);
-    const long long per = width ? 1 : (dv + 31) / 32;
-    const long long rows = (long long)B * H * nwalk * per, slots = 2LL * device_sm_count();
-    long long n = slots / rows;
+    const bool shared = width == 0 || (width == 64 && dtype == SEMICRF_BF16);
+    const long long rows = (long long)B * H * nwalk * (width ? 1 : (dv + 31) / 32);
+    long long n = (shared ? 2LL : 1LL) * device_sm_count() / rows;
     if (n > T / 512) n = T / 512;
-    if (n < 2) {
+    if (n < (shared ? 3 : 2)) {
         *seg_len = (T + kChunk - 1) / kChunk * kChunk;
         return 1;
     }

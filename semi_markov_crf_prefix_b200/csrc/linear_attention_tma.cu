@@ -42,29 +42,33 @@ struct LaTables {
 
 template <int D>
 struct TmaCfg {
-    static constexpr int NM = 2, NK = 3;            // terms of P and S, and of K~ (see the register form)
+    static constexpr int NM = 2;                    // terms of P and S (see the register form)
     static constexpr int kTile = D / 64 * 16384;    // 128 rows
     static constexpr int kSTile = D * D * 2;
     static constexpr bool kApart = D == 64;         // K has a tile of its own beside K~, or becomes K~'s first term
     static constexpr bool kStateTmem = D == 128;
-    static constexpr int kQ = 0, kK = kQ + kTile, kKt = kApart ? kK + kTile : kK, kV = kKt + NK * kTile,
+    static constexpr int kQ = 0, kK = kQ + kTile, kKt = kApart ? kK + kTile : kK, kV = kKt + 3 * kTile,
                          kS = kV + kTile, kTab = kS + NM * kSTile, kBars = kTab + (int)sizeof(LaTables),
                          kSmem = kBars + 64;
     static constexpr int kO = 128, kKV = kO + D, kCols = D == 64 ? 256 : 512;
     static constexpr int kState = kKV + (kStateTmem ? D : 0);
-    static constexpr int kOut = kKt + 2 * kTile;    // outputs on their way: K~'s third term
+    static constexpr int kOut = kKt + 2 * kTile;    // outputs on their way, where K~'s third term is if there is one
     static constexpr int NP = kChunk * (D / 8) / kWorkers, kRows = kWorkers / (D / 8);
     static constexpr int kBlocks = D == 64 ? 2 : 1;
     static_assert(kSmem <= (kBlocks == 2 ? 113 : 227) * 1024, "shared memory");
 };
 
-template <int D, bool STATE_ONLY>
+// NK: terms of K~.  Three (24 bits) where a float32 state leaves the call; two leave 2^-17,
+// which 16-bit outputs do not show, and cost a third less of the shared memory's traffic,
+// the first bound of this kernel (2.9 of 4.2 thousand cycles a chunk at width 64).
+template <int D, bool STATE_ONLY, int NK>
 __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(const __grid_constant__ LaArgs args,
-                                                                             const __grid_constant__ LaMaps maps)
+                                                                                const __grid_constant__ LaMaps maps)
 {
     using G = TmaCfg<D>;
     using T = __nv_bfloat16;
-    constexpr int NM = G::NM, NK = G::NK, NP = G::NP;
+    constexpr int NM = G::NM, NP = G::NP;
+    constexpr int kUnroll = D == 128 ? 8 : 1;   // of the matrix instructions: no registers for it at width 64
     constexpr uint64_t kTileD = G::kTile >> 4, kSTileD = G::kSTile >> 4, kRow16 = 2048 >> 4;
     extern __shared__ __align__(1024) unsigned char sm[];
     const LaWalk &w = args.w[blockIdx.y];
@@ -113,9 +117,9 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
     bool alive = true;
 
     if (warp == 8) {
-        const bool lead = elect_lane();
         const auto &map = maps.w[blockIdx.y];
-        // (all of these in a branch of the leading lane)
+        // all of these in a branch of one lane, which is elected anew each time: a flag of the
+        // election kept in a variable made each instruction 60 to 180 cycles long
         auto await = [&](uint32_t bar, uint32_t parity) { alive = mbar_wait_bounded(bar, parity) && alive; };
         auto fetch = [&](const CUtensorMap &m, int tile, uint32_t bar, int n) {
             mbar_expect(bar, G::kTile);
@@ -130,7 +134,7 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
             }
             tc_after_sync();
             const uint64_t dq = desc_swz(smem + G::kQ, 16), dk = desc_swz(smem + G::kK, 16);
-#pragma unroll 1
+#pragma unroll(kUnroll)
             for (int k = 0; k < kd; ++k) {
                 const uint64_t at = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
                 mma_ss(tm, dq + at, dk + at, mma_idesc(128, 128, false, false), k > 0);
@@ -142,7 +146,7 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
             __syncwarp();
             return !__syncthreads_or(!alive);
         };
-        if (lead && whole > 0) {
+        if (whole > 0 && elect_lane()) {
             if (!STATE_ONLY) fetch(map.q, G::kQ, full_q, 0);
             fetch(map.k, G::kK, full_k, 0);
             fetch(map.v, G::kV, full_v, 0);
@@ -154,28 +158,34 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
             const bool next = n + 1 < whole;
             if (!STATE_ONLY) {
                 if (n >= whole && !meet()) break;   // the shorter chunk's tiles are there
-                if (lead) {
+                if (elect_lane()) {
                     if (n >= whole || !G::kApart) scores(n);
                     tc_after_sync();
                     const uint32_t i2 = mma_idesc(128, nv, false, true);
                     const uint64_t dq = desc_swz(smem + G::kQ, 16), ds = desc_swz(smem + G::kS, 16384);
-#pragma unroll 1
+#pragma unroll(kUnroll)
                     for (int i = 0; i < 2 * kd; ++i) {   // the state's second term first
                         const int k = i < kd ? i : i - kd;
                         const uint64_t at = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
                         mma_ss(tm + G::kO, dq + at, ds + (i < kd ? kSTileD : 0) + k * kRow16, i2, i > 0);
                     }
                     mma_commit(done_qs);
-                    tma_store_read();   // K~'s third term is free again
+                    tma_store_read();   // the last outputs have left
+                    if (NK == 2 && next) {
+                        await(done_qs, parity);
+                        fetch(map.q, G::kQ, full_q, n + 1);
+                    }
                 }
-                if (!meet()) break;
-                if (lead && next) {
-                    await(done_qs, parity);
-                    fetch(map.q, G::kQ, full_q, n + 1);
+                if (NK == 3) {
+                    if (!meet()) break;   // K~'s third term may be written
+                    if (next && elect_lane()) {
+                        await(done_qs, parity);
+                        fetch(map.q, G::kQ, full_q, n + 1);
+                    }
                 }
             }
             if (!meet()) break;   // K~ is there
-            if (lead) {
+            if (elect_lane()) {
                 if (G::kApart && next) fetch(map.k, G::kK, full_k, n + 1);
                 if (n < whole) await(full_v, parity);
                 tc_after_sync();
@@ -183,7 +193,7 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
                 const uint64_t dk = desc_swz(smem + G::kKt, 16384), dv = desc_swz(smem + G::kV, 16384);
 #pragma unroll
                 for (int x = NK - 1; x >= 0; --x)
-#pragma unroll 1
+#pragma unroll(kUnroll)
                     for (int k = 0; k < kChunk / 16; ++k)
                         mma_ss(tm + G::kKV, dk + x * kTileD + k * kRow16, dv + k * kRow16, i4, x < NK - 1 || k > 0);
                 mma_commit(done_kv);
@@ -195,13 +205,13 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
             }
             if (STATE_ONLY) continue;
             if (!meet()) break;   // P is there, o scaled
-            if (lead) {
+            if (elect_lane()) {
                 tc_after_sync();
                 const uint32_t i3 = mma_idesc(128, nv, false, true);
                 const uint64_t dv = desc_swz(smem + G::kV, 16384);
 #pragma unroll
                 for (int x = NM - 1; x >= 0; --x)
-#pragma unroll 1
+#pragma unroll(kUnroll)
                     for (int k = 0; k < kChunk / 16; ++k)
                         mma_ts(tm + G::kO, tm + k * (8 * NM) + x * 8, dv + k * kRow16, i3, true);
                 mma_commit(done_pv);
@@ -216,14 +226,14 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
                 }
             }
             if (!meet()) break;   // this chunk's outputs lie in shared memory, the next state's terms too
-            if (lead && n < whole) {
+            if (n < whole && elect_lane()) {
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
                     tma_store(smem + G::kOut + c * 16384, &map.o, c * 64, s.h, row_of(n), s.b);
                 tma_store_commit();
             }
         }
-        if (lead) {
+        if (elect_lane()) {
             tma_store_done();
             if (!alive) set_status(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
         }
@@ -333,7 +343,7 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
             const int lead = s.p0 + n == 0 ? w.lead : 1;
             if (is_whole) await(full_k, parity);
             if (!G::kApart && !STATE_ONLY) await(done_qk, parity);   // K~ replaces K
-            uint4 third[NP];   // K~'s third term, whose tile the last outputs may still be leaving
+            uint4 third[NK == 3 ? NP : 1];   // K~'s third term, whose tile the last outputs may still be leaving
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 const unsigned char *at = sm + G::kK + at0 + i * G::kRows * 128;
@@ -356,16 +366,16 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
                 for (int x = 0; x < NK; ++x) {
                     const uint4 v = make_uint4(o[x][0], o[x][1], o[x][2], o[x][3]);
                     if (x == 2 && !STATE_ONLY)
-                        third[i] = v;
+                        third[NK == 3 ? i : 0] = v;
                     else
                         *reinterpret_cast<uint4 *>(sm + G::kKt + x * G::kTile + at0 + i * G::kRows * 128) = v;
                 }
             }
-            if (!STATE_ONLY) {
+            if (NK == 3 && !STATE_ONLY) {
                 if (__syncthreads_or(!alive)) break;
 #pragma unroll
                 for (int i = 0; i < NP; ++i)
-                    *reinterpret_cast<uint4 *>(sm + G::kKt + 2 * G::kTile + at0 + i * G::kRows * 128) = third[i];
+                    *reinterpret_cast<uint4 *>(sm + G::kKt + 2 * G::kTile + at0 + i * G::kRows * 128) = third[NK == 3 ? i : 0];
             }
             smem_to_mma();
             if (__syncthreads_or(!alive)) break;
@@ -561,20 +571,27 @@ bool make_map(CUtensorMap *m, const void *p, const long long (&st)[3], int d, co
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool STATE_ONLY>
-cudaError_t go(const LaArgs &a, const LaMaps &maps, cudaStream_t st, int *n)
-{
-    using G = TmaCfg<D>;
-    return timed_launch(st, n, [&] {
-        la_tma_kernel<D, STATE_ONLY><<<dim3(a.B * a.H * a.nseg, a.nwalk), kThreads, G::kSmem, st>>>(a, maps);
-    });
-}
-
-template <int D, bool STATE_ONLY>
+template <int D, bool STATE_ONLY, int NK>
 cudaError_t allow_smem()
 {
-    return cudaFuncSetAttribute(la_tma_kernel<D, STATE_ONLY>, cudaFuncAttributeMaxDynamicSharedMemorySize, TmaCfg<D>::kSmem);
+    return cudaFuncSetAttribute(la_tma_kernel<D, STATE_ONLY, NK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                TmaCfg<D>::kSmem);
 }
+
+template <int D, bool STATE_ONLY, int NK>
+void go(const LaArgs &a, const LaMaps &maps, cudaStream_t st)
+{
+    using G = TmaCfg<D>;
+    la_tma_kernel<D, STATE_ONLY, NK><<<dim3(a.B * a.H * a.nseg, a.nwalk), kThreads, G::kSmem, st>>>(a, maps);
+}
+
+struct Kernel {
+    cudaError_t (*allow)();
+    void (*go)(const LaArgs &, const LaMaps &, cudaStream_t);
+};
+
+template <int D, bool STATE_ONLY, int NK>
+constexpr Kernel kernel_of{allow_smem<D, STATE_ONLY, NK>, go<D, STATE_ONLY, NK>};
 
 }  // namespace
 
@@ -582,10 +599,15 @@ cudaError_t allow_smem()
 bool la_tma_walk(const LaArgs &a, int width, bool state_only, cudaStream_t st, int *n, cudaError_t *e)
 {
     if (!encoder()) return false;
+    bool keeps = false;   // some walk's state leaves the call
+    for (int i = 0; i < a.nwalk; ++i) keeps |= a.w[i].s_out != nullptr;
+    const Kernel k = width == 64 ? (state_only ? (keeps ? kernel_of<64, true, 3> : kernel_of<64, true, 2>)
+                                               : (keeps ? kernel_of<64, false, 3> : kernel_of<64, false, 2>))
+                                 : (state_only ? (keeps ? kernel_of<128, true, 3> : kernel_of<128, true, 2>)
+                                               : (keeps ? kernel_of<128, false, 3> : kernel_of<128, false, 2>));
     // (also binds the device's context to a thread that makes its first call, which the
     // driver's encoder wants: the backward pass runs in a thread of its own)
-    *e = width == 64 ? (state_only ? allow_smem<64, true>() : allow_smem<64, false>())
-                     : (state_only ? allow_smem<128, true>() : allow_smem<128, false>());
+    *e = k.allow();
     if (*e != cudaSuccess) return true;
     LaMaps maps;
     for (int i = 0; i < a.nwalk; ++i) {
@@ -596,10 +618,7 @@ bool la_tma_walk(const LaArgs &a, int width, bool state_only, cudaStream_t st, i
             !make_map(&m.v, w.v, w.vs, w.dv, a) || !make_map(&m.o, w.o, w.os, w.dv, a))
             return false;
     }
-    if (width == 64)
-        *e = state_only ? go<64, true>(a, maps, st, n) : go<64, false>(a, maps, st, n);
-    else
-        *e = state_only ? go<128, true>(a, maps, st, n) : go<128, false>(a, maps, st, n);
+    *e = timed_launch(st, n, [&] { k.go(a, maps, st); });
     return true;
 }
 
