@@ -352,7 +352,7 @@ semicrf_status semicrf_linear_attention_step(const semicrf_attention_dims *dims,
  *   weight, bias  [C] in float32 or in x's dtype (both the same), or NULL (1 and 0)
  *   lengths   int32 [N] in [0, S], or NULL (all S); y = 0 at s >= L_n, where nothing
  *             is read
- *   stats     float32 [N, G, 2]: mean and rstd, kept for the backward
+ *   stats     float32 [N, G, 2], 8-byte aligned: mean and rstd, kept for the backward
  */
 typedef struct {
     int32_t N, S, C, G;

@@ -6,6 +6,7 @@ path.  Build it with ``python -m semi_markov_crf_prefix_b200.build``.
 from __future__ import annotations
 
 import ctypes
+import struct
 from pathlib import Path
 
 LIB_PATH = Path(__file__).resolve().parent / "libsemicrf.so"
@@ -37,17 +38,10 @@ F32, BF16, F16, F64 = 0, 1, 2, 3
 MAX_HEAD = 256
 
 
-class AttentionDims(ctypes.Structure):
-    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("dk", ctypes.c_int32),
-                ("dv", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reverse", ctypes.c_int32),
-                ("scale", ctypes.c_float), ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3),
-                ("v_stride", ctypes.c_int64 * 3), ("o_stride", ctypes.c_int64 * 3)]
-
-
-class NormDims(ctypes.Structure):
-    _fields_ = [("N", ctypes.c_int32), ("S", ctypes.c_int32), ("C", ctypes.c_int32), ("G", ctypes.c_int32),
-                ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
-                ("eps", ctypes.c_float)]
+# semicrf_attention_dims and semicrf_norm_dims as packed bytes (a call's arguments are
+# marshalled once for each call, where a Structure costs several times as much)
+ATTENTION_DIMS = struct.Struct("7if12q")
+NORM_DIMS = struct.Struct("7if")
 
 
 class AdamWConfig(ctypes.Structure):
@@ -68,8 +62,6 @@ _lib = None
 _P = ctypes.c_void_p
 _S = ctypes.c_size_t
 _DP = ctypes.POINTER(Dims)
-_AP = ctypes.POINTER(AttentionDims)
-_NP = ctypes.POINTER(NormDims)
 SIGNATURES = {
     "semicrf_workspace_bytes": (ctypes.c_size_t, [_DP, ctypes.c_int32]),
     "semicrf_check_dims": (ctypes.c_int, [_DP]),
@@ -86,14 +78,14 @@ SIGNATURES = {
     "semicrf_gold_backward": (ctypes.c_int, [_DP, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
     "semicrf_nll": (ctypes.c_int, [_DP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
     "semicrf_nll_backward": (ctypes.c_int, [_DP, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P, _P, _P, _P]),
-    "semicrf_linear_attention_workspace_bytes": (ctypes.c_size_t, [_AP, ctypes.c_int32]),
-    "semicrf_linear_attention": (ctypes.c_int, [_AP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
-    "semicrf_linear_attention_backward": (ctypes.c_int, [_AP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S,
+    "semicrf_linear_attention_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32]),
+    "semicrf_linear_attention": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
+    "semicrf_linear_attention_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S,
                                                          _P]),
-    "semicrf_linear_attention_step": (ctypes.c_int, [_AP, _P, _P, _P, _P, _P, _P, _P]),
-    "semicrf_group_norm_workspace_bytes": (ctypes.c_size_t, [_NP, ctypes.c_int32]),
-    "semicrf_group_norm": (ctypes.c_int, [_NP, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
-    "semicrf_group_norm_backward": (ctypes.c_int, [_NP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
+    "semicrf_linear_attention_step": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P]),
+    "semicrf_group_norm_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32]),
+    "semicrf_group_norm": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
+    "semicrf_group_norm_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
     "semicrf_adamw": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.POINTER(AdamWConfig), _P]),
     "semicrf_adamw_state_values": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32, _P]),
     "semicrf_clear_device_status": (ctypes.c_int, [_P, _P]),

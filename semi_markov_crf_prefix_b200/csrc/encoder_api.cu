@@ -303,7 +303,7 @@ semicrf_status semicrf_group_norm(const semicrf_norm_dims *dims, const void *x, 
     prof_reset();
     semicrf_status s = norm_ok(dims);
     if (s != SEMICRF_OK) return s;
-    if (!x || !y || !stats) return SEMICRF_ERR_INVALID_ARG;
+    if (!x || !y || !stats || reinterpret_cast<uintptr_t>(stats) % 8) return SEMICRF_ERR_INVALID_ARG;
     s = ws_ok(ws, ws_bytes, semicrf_group_norm_workspace_bytes(dims, 0));
     if (s != SEMICRF_OK) return s;
     NormArgs a = norm_args(*dims, weight, bias, lengths, ws);
@@ -323,7 +323,7 @@ semicrf_status semicrf_group_norm_backward(const semicrf_norm_dims *dims, const 
     prof_reset();
     semicrf_status s = norm_ok(dims);
     if (s != SEMICRF_OK) return s;
-    if (!dy || !x || !stats || !dx) return SEMICRF_ERR_INVALID_ARG;
+    if (!dy || !x || !stats || !dx || reinterpret_cast<uintptr_t>(stats) % 8) return SEMICRF_ERR_INVALID_ARG;
     s = ws_ok(ws, ws_bytes, semicrf_group_norm_workspace_bytes(dims, 1));
     if (s != SEMICRF_OK) return s;
     NormArgs a = norm_args(*dims, weight, bias, lengths, ws);

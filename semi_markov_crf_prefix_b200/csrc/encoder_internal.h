@@ -44,6 +44,52 @@ struct alignas(sizeof(T) * N) Pack {
     T v[N];
 };
 
+// The values of a pack as floats, and back: two 16-bit values of a word at a time.
+template <typename T, int N>
+__device__ __forceinline__ void unpack(const Pack<T, N> &p, float (&o)[N])
+{
+    if constexpr (sizeof(T) == 2 && N % 2 == 0) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(&p);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            if constexpr (__is_same(T, __half)) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                o[2 * i] = f.x;
+                o[2 * i + 1] = f.y;
+            } else {
+                o[2 * i] = __uint_as_float(w[i] << 16);
+                o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = to_f<T>(p.v[i]);
+    }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> pack(const float (&f)[N])
+{
+    Pack<T, N> p;
+    if constexpr (sizeof(T) == 2 && N % 2 == 0) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(&p);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            if constexpr (__is_same(T, __half)) {
+                const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) p.v[i] = from_f<T>(f[i]);
+    }
+    return p;
+}
+
 // ---- linear attention ----
 
 // One walk over all sequences and heads: S_p = lam S_{p-1} + c k_p v_p^T, o_p = b q_p S_p.  The forward is

@@ -13,29 +13,41 @@ namespace {
 
 // ---- the elementwise part ----
 
-// Phi(z), the normal distribution function, and phi(z) from one exponential:
-// Abramowitz and Stegun 7.1.26, erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2) with
-// t = 1 / (1 + p x) and an error below 1.5e-7, at x = |z| / sqrt 2.  The library's
-// erfcf kept the two-pass kernel at a fifth of the memory's rate.
-__device__ __forceinline__ float normal_cdf(float z, float &density)
+__device__ __forceinline__ float exp2_approx(float x)
 {
-    const float x = fabsf(z) * 0.70710678118654752f, e = __expf(-x * x);
-    const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-    const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
-                                0.254829592f);
-    density = 0.39894228040143268f * e;
-    const float tail = 0.5f * poly * e;
-    return z < 0.f ? tail : 1.f - tail;
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The upper tail 1 - Phi(|z|) of the normal distribution, and exp(-z^2 / 2): Abramowitz
+// and Stegun 7.1.26, erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2) with t = 1 / (1 + p x) and an
+// error below 1.5e-7, at x = |z| / sqrt 2 with the half and the root in the constants.
+// Eleven operations of which two are transcendental; with the library's erfcf the
+// two-pass kernel ran at a fifth of the memory's rate.
+__device__ __forceinline__ float normal_tail(float z, float &e)
+{
+    e = exp2_approx(z * z * -0.72134752044448170f);
+    const float t = rcp_approx(fmaf(0.23164189f, fabsf(z), 1.f));
+    return t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5307027145f, -0.7265760135f), 0.7107068705f), -0.142248368f),
+                    0.127414796f) * e;
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.f + exp2_approx(z * -1.4426950408889634f)); }
 
 template <int ACT>
 __device__ __forceinline__ float activate(float z)
 {
-    float density;
+    float e;
     if constexpr (ACT == SEMICRF_ACT_SILU) return z * sigmoid(z);
-    if constexpr (ACT == SEMICRF_ACT_GELU) return z * normal_cdf(z, density);
+    if constexpr (ACT == SEMICRF_ACT_GELU) return fmaf(-fabsf(z), normal_tail(z, e), fmaxf(z, 0.f));
     return z;
 }
 
@@ -47,9 +59,9 @@ __device__ __forceinline__ float slope(float z)
         return s * fmaf(z, 1.f - s, 1.f);
     }
     if constexpr (ACT == SEMICRF_ACT_GELU) {
-        float density;
-        const float cdf = normal_cdf(z, density);
-        return fmaf(z, density, cdf);
+        float e;
+        const float tail = normal_tail(z, e);
+        return fmaf(z * 0.39894228040143268f, e, z < 0.f ? tail : 1.f - tail);
     }
     return 1.f;
 }
@@ -97,7 +109,6 @@ __device__ __forceinline__ int norm_length(const NormArgs &a, int n)
 // it), one write.
 struct RegShape {
     int CV, RL, NB, W;   // vectors a row; row lanes a block; row blocks a thread block; lanes that sum one group
-    int lanes;           // a group's vectors of one row lie in this many neighbouring lanes of a warp (0: they do not)
 };
 
 constexpr int kRegThreads = 512;
@@ -142,49 +153,55 @@ __global__ __launch_bounds__(kRegThreads, U == 1 ? (BWD ? 2 : 3) : 1) void norm_
     }
     // a thread's share to its group's sum over the row block
     auto total = [&](float share, float *red, float *out) {
-        if (sh.lanes) return warp_sum(share, sh.lanes);
         red[tid] = share;
         __syncthreads();
         group_sums(red, out, sh, a.G, CgV);
         __syncthreads();
         return mine ? out[nb * a.G + g] : 0.f;
     };
-    for (int n0 = blockIdx.x * sh.NB; n0 < a.N; n0 += gridDim.x * sh.NB) {
+    auto fetch = [&](int n0, Pack<T, VEC>(&x)[U], Pack<T, VEC>(&dy)[BWD ? U : 1]) {
         const int n = n0 + nb;
-        const bool on = mine && n < a.N;
-        const int L = on ? norm_length(a, n) : 0;
+        const int L = mine && n < a.N ? norm_length(a, n) : 0;
         const long long base = ((long long)n * a.S) * a.C + c0;
-        Pack<T, VEC> x[U], dy[BWD ? U : 1];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = rl + u * sh.RL;
             if (s < L) {
                 x[u] = *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(a.x) + base + (long long)s * a.C);
                 if (BWD)
-                    dy[u] = *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(a.dy) + base +
-                                                                    (long long)s * a.C);
+                    dy[BWD ? u : 0] =
+                        *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(a.dy) + base + (long long)s * a.C);
             }
         }
+        return L;
+    };
+    for (int n0 = blockIdx.x * sh.NB; n0 < a.N; n0 += gridDim.x * sh.NB) {
+        const int n = n0 + nb;
+        const bool on = mine && n < a.N;
+        const long long base = ((long long)n * a.S) * a.C + c0;
+        Pack<T, VEC> x[U], dy[BWD ? U : 1];
+        const int L = fetch(n0, x, dy);
         const float inv = 1.f / fmaxf((float)L * Cg, 1.f);
         float mu, rs;
         if (!BWD) {
-            float sum = 0.f;
+            float sum = 0.f, f[VEC];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (rl + u * sh.RL < L)
+                if (rl + u * sh.RL < L) {
+                    unpack(x[u], f);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) sum += to_f<T>(x[u].v[e]);
+                    for (int e = 0; e < VEC; ++e) sum += f[e];
+                }
             mu = inv * total(sum, red, mean);
             sum = 0.f;
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (rl + u * sh.RL < L)
+                if (rl + u * sh.RL < L) {
+                    unpack(x[u], f);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float d = to_f<T>(x[u].v[e]) - mu;
-                        sum = fmaf(d, d, sum);
-                    }
-            rs = 1.f / sqrtf(fmaf(total(sum, red2, aux), inv, a.eps));
+                    for (int e = 0; e < VEC; ++e) sum = fmaf(f[e] - mu, f[e] - mu, sum);
+                }
+            rs = rsqrtf(fmaf(total(sum, red2, aux), inv, a.eps));
             if (on && a.stats && rl == 0 && c0 % Cg == 0) {
                 float *st = a.stats + 2 * ((long long)n * a.G + g);
                 st[0] = mu;
@@ -195,12 +212,12 @@ __global__ __launch_bounds__(kRegThreads, U == 1 ? (BWD ? 2 : 3) : 1) void norm_
                 for (int u = 0; u < U; ++u) {
                     const int s = rl + u * sh.RL;
                     if (!on || s >= a.S) continue;
-                    Pack<T, VEC> y;
+                    float y[VEC];
+                    unpack(x[u], f);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e)
-                        y.v[e] = from_f<T>(
-                            s < L ? activate<act.value>(fmaf((to_f<T>(x[u].v[e]) - mu) * rs, wt[e], bs[e])) : 0.f);
-                    *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(a.y) + base + (long long)s * a.C) = y;
+                        y[e] = s < L ? activate<act.value>(fmaf((f[e] - mu) * rs, wt[e], bs[e])) : 0.f;
+                    *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(a.y) + base + (long long)s * a.C) = pack<T, VEC>(y);
                 }
             });
         } else {
@@ -213,10 +230,13 @@ __global__ __launch_bounds__(kRegThreads, U == 1 ? (BWD ? 2 : 3) : 1) void norm_
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (rl + u * sh.RL >= L) continue;
+                    float f[VEC], g[VEC];
+                    unpack(x[u], f);
+                    unpack(dy[BWD ? u : 0], g);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        const float xh = (to_f<T>(x[u].v[e]) - mu) * rs;
-                        const float dz = to_f<T>(dy[u].v[e]) * slope<act.value>(fmaf(xh, wt[e], bs[e]));
+                        const float xh = (f[e] - mu) * rs;
+                        const float dz = g[e] * slope<act.value>(fmaf(xh, wt[e], bs[e]));
                         gz[u][e] = dz * wt[e];
                         s1 += gz[u][e];
                         s2 = fmaf(gz[u][e], xh, s2);
@@ -231,16 +251,14 @@ __global__ __launch_bounds__(kRegThreads, U == 1 ? (BWD ? 2 : 3) : 1) void norm_
             for (int u = 0; u < U; ++u) {
                 const int s = rl + u * sh.RL;
                 if (!on || s >= a.S) continue;
-                Pack<T, VEC> y;
+                float y[VEC], f[VEC];
+                unpack(x[u], f);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float xh = (to_f<T>(x[u].v[e]) - mu) * rs;
-                    y.v[e] = from_f<T>(s < L ? rs * (gz[u][e] - s1 - xh * s2) : 0.f);
-                }
-                *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(a.y) + base + (long long)s * a.C) = y;
+                for (int e = 0; e < VEC; ++e) y[e] = s < L ? rs * (gz[u][e] - s1 - (f[e] - mu) * rs * s2) : 0.f;
+                *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(a.y) + base + (long long)s * a.C) = pack<T, VEC>(y);
             }
         }
-        if (!sh.lanes) __syncthreads();   // the sums' buffers serve the next row blocks
+        __syncthreads();   // the sums' buffers serve the next row blocks
     }
     if (BWD) {
         // this block's share of dw and db: part[block][2][C]
@@ -256,6 +274,120 @@ __global__ __launch_bounds__(kRegThreads, U == 1 ? (BWD ? 2 : 3) : 1) void norm_
                 for (int j = col; j < sh.NB * sh.RL * sh.CV; j += sh.CV) {
                     sw += (double)acc[j];
                     sb += (double)acc[kRegThreads + j];
+                }
+                double *p = a.part + (long long)blockIdx.x * 2 * a.C + c0 + e;
+                p[0] = sw;
+                p[a.C] = sb;
+            }
+        }
+    }
+}
+
+// Row blocks of one row whose groups lie in `lanes` neighbouring threads (a power of two):
+// normalising each position by itself.  A thread keeps its channels, so their weights
+// stay in registers, and steps from row to row with the next one already on its way;
+// sums are shuffles.
+template <typename T, int VEC, bool BWD>
+__global__ __launch_bounds__(256) void norm_row_kernel(const __grid_constant__ NormArgs a, int CV, int rows, int lanes)
+{
+    __shared__ float acc[BWD ? 2 : 1][BWD ? 256 : 1];
+    const int tid = threadIdx.x, col = tid % CV, r = tid / CV, c0 = col * VEC;
+    const bool mine = r < rows;
+    const float inv = 1.f / (float)(a.C / a.G);
+    float wt[VEC], bs[VEC], dw[VEC], db[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        wt[e] = weight_at<T>(a.weight, a.wdtype, c0 + e, 1.f);
+        bs[e] = weight_at<T>(a.bias, a.wdtype, c0 + e, 0.f);
+        dw[e] = db[e] = 0.f;
+    }
+    const int step = gridDim.x * rows;
+    const long long stride = (long long)step * CV;
+    int n = blockIdx.x * rows + r;
+    const long long at = (long long)n * CV + col;
+    const Pack<T, VEC> *px = static_cast<const Pack<T, VEC> *>(a.x) + at, *pd = static_cast<const Pack<T, VEC> *>(a.dy) + at;
+    Pack<T, VEC> *py = static_cast<Pack<T, VEC> *>(a.y) + at;
+    float *st = a.stats + 2 * ((long long)n * a.G + c0 / (a.C / a.G));
+    const long long ststep = 2LL * step * a.G;
+    Pack<T, VEC> nx, nd;
+    auto fetch = [&](int m) {   // false: nothing there
+        const bool on = mine && m < a.N && (!a.lengths || norm_length(a, m) == 1);
+        if (on) {
+            nx = *px;
+            if (BWD) nd = *pd;
+        }
+        px += stride;
+        if (BWD) pd += stride;
+        return on;
+    };
+    by_activation(a.act, [&](auto act) {
+        bool next = fetch(n);
+        // (every lane takes part in the shuffles: the block's last rows decide)
+        for (int first = n - r; first < a.N; first += step) {
+            const bool on = next, write = mine && n < a.N;
+            float f[VEC], g[VEC], y[VEC], sum = 0.f, sq = 0.f;
+            if (on) {
+                unpack(nx, f);
+                if (BWD) unpack(nd, g);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) f[e] = g[e] = 0.f;
+            }
+            next = fetch(n + step);
+            if constexpr (!BWD) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) sum += f[e];
+                const float mu = warp_sum(sum, lanes) * inv;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    f[e] -= mu;
+                    sq = fmaf(f[e], f[e], sq);
+                }
+                const float rs = rsqrtf(fmaf(warp_sum(sq, lanes), inv, a.eps));
+                if (write && col % lanes == 0) *reinterpret_cast<float2 *>(st) = make_float2(mu, rs);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) y[e] = activate<act.value>(fmaf(f[e] * rs, wt[e], bs[e]));
+            } else {
+                float2 s = make_float2(0.f, 0.f);
+                if (on) s = *reinterpret_cast<const float2 *>(st);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    f[e] = (f[e] - s.x) * s.y;
+                    const float dz = g[e] * slope<act.value>(fmaf(f[e], wt[e], bs[e]));
+                    dw[e] = fmaf(dz, f[e], dw[e]);
+                    db[e] += dz;
+                    g[e] = dz * wt[e];
+                    sum += g[e];
+                    sq = fmaf(g[e], f[e], sq);
+                }
+                sum = warp_sum(sum, lanes) * inv;
+                sq = warp_sum(sq, lanes) * inv;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) y[e] = s.y * (g[e] - fmaf(f[e], sq, sum));
+            }
+            if (!on) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) y[e] = 0.f;
+            }
+            if (write) *py = pack<T, VEC>(y);
+            py += stride;
+            st += ststep;
+            n += step;
+        }
+    });
+    if constexpr (BWD) {
+        // this block's share of dw and db: part[block][2][C]
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            __syncthreads();
+            acc[0][tid] = mine ? dw[e] : 0.f;
+            acc[1][tid] = mine ? db[e] : 0.f;
+            __syncthreads();
+            if (r == 0) {
+                double sw = 0.0, sb = 0.0;
+                for (int j = col; j < rows * CV; j += CV) {
+                    sw += (double)acc[0][j];
+                    sb += (double)acc[1][j];
                 }
                 double *p = a.part + (long long)blockIdx.x * 2 * a.C + c0 + e;
                 p[0] = sw;
@@ -296,19 +428,19 @@ __global__ __launch_bounds__(512) void norm_params_kernel(const double *part, in
 // ---- long rows: two passes over the data ----
 //
 // Pass 1: per-channel sums of a strip of positions, part[n][strip][2][C] in float64
-// (forward: x and x^2; backward: dz xh and dz).  A thread sums up to kRun of a
-// channel's values in float32 about the first of them, which no mean can spoil, and
-// takes the two sums about zero to float64.  Then the groups' statistics, then pass 2
+// (forward: x and x^2; backward: dz xh and dz).  A thread sums a strip's values of a
+// channel, kRun at most, in float32 about the first of them, which no mean can spoil,
+// and takes the two sums about zero to float64.  Then the groups' statistics, then pass 2
 // writes y or dx, strips in the opposite order: the ones that pass 1 read last are
 // still in the L2 cache.
-constexpr int kLongThreads = 256, kRun = 64;
+constexpr int kLongThreads = 256, kRun = 128;
 
 struct LongShape {
     int CV, tiles, R, strips, rows;   // vectors a row, column tiles of <= 256 of them, row lanes, strips, rows a strip
 };
 
 template <typename T, int VEC, bool BWD>
-__global__ __launch_bounds__(kLongThreads) void norm_sums_kernel(const __grid_constant__ NormArgs a, const LongShape sh)
+__global__ __launch_bounds__(kLongThreads, 3) void norm_sums_kernel(const __grid_constant__ NormArgs a, const LongShape sh)
 {
     extern __shared__ double dsm[];
     const int cols = min(sh.CV, kLongThreads), tid = threadIdx.x, r = tid / cols;
@@ -316,53 +448,37 @@ __global__ __launch_bounds__(kLongThreads) void norm_sums_kernel(const __grid_co
     const bool mine = r < sh.R && cv < sh.CV;
     const int L = norm_length(a, n), s0 = strip * sh.rows, s1 = min(L, s0 + sh.rows), c0 = cv * VEC;
     const long long base = (long long)n * a.S * a.C + c0;
-    double A[VEC], B[VEC];
+    float p[VEC], q[VEC], about[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) A[e] = B[e] = 0.0;
-    if (mine) {
+    for (int e = 0; e < VEC; ++e) p[e] = q[e] = about[e] = 0.f;
+    int cnt = 0;
+    if (mine && s0 + r < s1) {
         const T *px = static_cast<const T *>(a.x) + base, *pd = static_cast<const T *>(a.dy) + base;
         if constexpr (!BWD) {
-            for (int from = s0 + r; from < s1; from += sh.R * kRun) {
-                const int to = min(s1, from + sh.R * kRun);
-                float about[VEC], p[VEC], q[VEC];
-                const Pack<T, VEC> first = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)from * a.C);
+            auto add = [&](const Pack<T, VEC> &x) {
+                float f[VEC];
+                unpack(x, f);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    about[e] = to_f<T>(first.v[e]);
-                    p[e] = q[e] = 0.f;
+                    const float d = f[e] - about[e];
+                    p[e] += d;
+                    q[e] = fmaf(d, d, q[e]);
                 }
-                int s = from + sh.R, cnt = 1;
-                constexpr int U = 8;
-                for (; s + (U - 1) * sh.R < to; s += U * sh.R, cnt += U) {
-                    Pack<T, VEC> x[U];
+            };
+            const Pack<T, VEC> first = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s0 + r) * a.C);
+            unpack(first, about);
+            int s = s0 + r + sh.R;
+            cnt = 1;
+            constexpr int U = 8;
+            for (; s + (U - 1) * sh.R < s1; s += U * sh.R, cnt += U) {
+                Pack<T, VEC> x[U];
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        x[u] = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s + u * sh.R) * a.C);
+                for (int u = 0; u < U; ++u)
+                    x[u] = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s + u * sh.R) * a.C);
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const float d = to_f<T>(x[u].v[e]) - about[e];
-                            p[e] += d;
-                            q[e] = fmaf(d, d, q[e]);
-                        }
-                }
-                for (; s < to; s += sh.R, ++cnt) {
-                    const Pack<T, VEC> x = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)s * a.C);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float d = to_f<T>(x.v[e]) - about[e];
-                        p[e] += d;
-                        q[e] = fmaf(d, d, q[e]);
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const double m = about[e], dp = p[e];
-                    A[e] += dp + cnt * m;
-                    B[e] += (double)q[e] + m * (2.0 * dp + cnt * m);
-                }
+                for (int u = 0; u < U; ++u) add(x[u]);
             }
+            for (; s < s1; s += sh.R, ++cnt) add(*reinterpret_cast<const Pack<T, VEC> *>(px + (long long)s * a.C));
         } else {
             float wt[VEC], bs[VEC];
 #pragma unroll
@@ -373,41 +489,33 @@ __global__ __launch_bounds__(kLongThreads) void norm_sums_kernel(const __grid_co
             const float *st = a.stats + 2 * ((long long)n * a.G + c0 / (a.C / a.G));   // a vector lies inside one group
             const float mu = st[0], rs = st[1];
             by_activation(a.act, [&](auto act) {
-                for (int from = s0 + r; from < s1; from += sh.R * kRun) {
-                    const int to = min(s1, from + sh.R * kRun);
-                    float p[VEC], q[VEC];
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) p[e] = q[e] = 0.f;
-                    auto add = [&](const Pack<T, VEC> &x, const Pack<T, VEC> &dy) {
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const float xh = (to_f<T>(x.v[e]) - mu) * rs;
-                            const float dz = to_f<T>(dy.v[e]) * slope<act.value>(fmaf(xh, wt[e], bs[e]));
-                            p[e] = fmaf(dz, xh, p[e]);
-                            q[e] += dz;
-                        }
-                    };
-                    int s = from;
-                    constexpr int U = 4;
-                    for (; s + (U - 1) * sh.R < to; s += U * sh.R) {
-                        Pack<T, VEC> x[U], dy[U];
-#pragma unroll
-                        for (int u = 0; u < U; ++u) {
-                            x[u] = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s + u * sh.R) * a.C);
-                            dy[u] = *reinterpret_cast<const Pack<T, VEC> *>(pd + (long long)(s + u * sh.R) * a.C);
-                        }
-#pragma unroll
-                        for (int u = 0; u < U; ++u) add(x[u], dy[u]);
-                    }
-                    for (; s < to; s += sh.R)
-                        add(*reinterpret_cast<const Pack<T, VEC> *>(px + (long long)s * a.C),
-                            *reinterpret_cast<const Pack<T, VEC> *>(pd + (long long)s * a.C));
+                auto add = [&](const Pack<T, VEC> &x, const Pack<T, VEC> &dy) {
+                    float f[VEC], g[VEC];
+                    unpack(x, f);
+                    unpack(dy, g);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        A[e] += (double)p[e];
-                        B[e] += (double)q[e];
+                        const float xh = (f[e] - mu) * rs;
+                        const float dz = g[e] * slope<act.value>(fmaf(xh, wt[e], bs[e]));
+                        p[e] = fmaf(dz, xh, p[e]);
+                        q[e] += dz;
                     }
+                };
+                int s = s0 + r;
+                constexpr int U = 4;
+                for (; s + (U - 1) * sh.R < s1; s += U * sh.R) {
+                    Pack<T, VEC> x[U], dy[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        x[u] = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s + u * sh.R) * a.C);
+                        dy[u] = *reinterpret_cast<const Pack<T, VEC> *>(pd + (long long)(s + u * sh.R) * a.C);
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) add(x[u], dy[u]);
                 }
+                for (; s < s1; s += sh.R)
+                    add(*reinterpret_cast<const Pack<T, VEC> *>(px + (long long)s * a.C),
+                        *reinterpret_cast<const Pack<T, VEC> *>(pd + (long long)s * a.C));
             });
         }
     }
@@ -416,8 +524,9 @@ __global__ __launch_bounds__(kLongThreads) void norm_sums_kernel(const __grid_co
     for (int e = 0; e < VEC; ++e) {
         __syncthreads();
         if (r < sh.R) {
-            dsm[tid] = A[e];
-            dsm[kLongThreads + tid] = B[e];
+            const double m = about[e], dp = p[e];
+            dsm[tid] = BWD ? dp : dp + cnt * m;
+            dsm[kLongThreads + tid] = BWD ? (double)q[e] : (double)q[e] + m * (2.0 * dp + cnt * m);
         }
         __syncthreads();
         if (r == 0 && mine) {
@@ -490,19 +599,28 @@ __global__ __launch_bounds__(kLongThreads, BWD ? 3 : 4) void norm_apply_kernel(c
     }
     const long long at = 2 * ((long long)n * a.G + c0 / (a.C / a.G));   // a vector lies inside one group
     const float mu = a.stats[at], rs = a.stats[at + 1], g1 = BWD ? gsum[at] : 0.f, g2 = BWD ? gsum[at + 1] : 0.f;
+    if (!BWD)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) wt[e] *= rs;
     const T *px = static_cast<const T *>(a.x) + base, *pd = static_cast<const T *>(a.dy) + base;
     T *py = static_cast<T *>(a.y) + base;
     const int in = min(s1, L);
     by_activation(a.act, [&](auto act) {
         auto value = [&](const Pack<T, VEC> &x, const Pack<T, VEC> &dy) {
-            Pack<T, VEC> y;
+            float y[VEC], f[VEC], g[VEC];
+            unpack(x, f);
+            if (BWD) unpack(dy, g);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float xh = (to_f<T>(x.v[e]) - mu) * rs, z = fmaf(xh, wt[e], bs[e]);
-                y.v[e] = from_f<T>(BWD ? rs * (to_f<T>(dy.v[e]) * slope<act.value>(z) * wt[e] - g1 - xh * g2)
-                                       : activate<act.value>(z));
+                const float d = f[e] - mu;
+                if constexpr (BWD) {
+                    const float xh = d * rs, z = fmaf(xh, wt[e], bs[e]);
+                    y[e] = rs * (g[e] * slope<act.value>(z) * wt[e] - g1 - xh * g2);
+                } else {
+                    y[e] = activate<act.value>(fmaf(d, wt[e], bs[e]));
+                }
             }
-            return y;
+            return pack<T, VEC>(y);
         };
         constexpr int U = 4;
         int s = s0 + r;
@@ -561,9 +679,7 @@ bool reg_shape(int S, int C, int G, int vec, RegShape *sh)
     sh->RL = R < S ? R : S;
     sh->NB = R / sh->RL;
     if ((S + sh->RL - 1) / sh->RL > 32 / vec) return false;
-    const int CgV = C / G / vec;
-    sh->W = pow2_at_least(sh->RL * CgV, 32);
-    sh->lanes = sh->RL == 1 && CgV <= 32 && (CgV & (CgV - 1)) == 0 ? CgV : 0;
+    sh->W = pow2_at_least(sh->RL * (C / G / vec), 32);
     return true;
 }
 
@@ -578,7 +694,8 @@ LongShape long_shape(int N, int S, int C, int vec)
     long long strips = (8LL * device_sm_count() + (long long)N * sh.tiles - 1) / ((long long)N * sh.tiles);
     const long long most = (S + sh.R * 8 - 1) / (sh.R * 8);
     if (strips > most) strips = most;
-    if (strips < 1) strips = 1;
+    const long long least = (S + (long long)sh.R * kRun - 1) / ((long long)sh.R * kRun);
+    if (strips < least) strips = least;
     sh.rows = (int)((S + strips - 1) / strips);
     sh.strips = (S + sh.rows - 1) / sh.rows;
     return sh;
@@ -587,6 +704,19 @@ LongShape long_shape(int N, int S, int C, int vec)
 int reg_blocks(int N, const RegShape &sh)
 {
     const int blocks = (N + sh.NB - 1) / sh.NB, most = 6 * device_sm_count();
+    return blocks < most ? blocks : most;
+}
+
+// Lanes of a group in norm_row_kernel, 0 where it does not apply.
+int row_lanes(int S, int C, int G, int vec)
+{
+    const int CgV = C / G / vec;
+    return S == 1 && C / vec <= 256 && CgV <= 32 && (CgV & (CgV - 1)) == 0 ? CgV : 0;
+}
+
+int row_blocks(int N, int rows)
+{
+    const int blocks = (N + rows - 1) / rows, most = 6 * device_sm_count();
     return blocks < most ? blocks : most;
 }
 
@@ -606,7 +736,12 @@ cudaError_t norm_go(NormArgs a, cudaStream_t st, int *n)
     RegShape rsh;
     cudaError_t e;
     int prows;
-    if (reg_shape(a.S, a.C, a.G, VEC, &rsh)) {
+    if (const int lanes = row_lanes(a.S, a.C, a.G, VEC)) {
+        const int CV = a.C / VEC, rows = 256 / CV, blocks = row_blocks(a.N, rows);
+        e = timed_launch(st, n, [&] { norm_row_kernel<T, VEC, BWD><<<blocks, 256, 0, st>>>(a, CV, rows, lanes); });
+        if (e != cudaSuccess) return e;
+        prows = blocks;
+    } else if (reg_shape(a.S, a.C, a.G, VEC, &rsh)) {
         const int blocks = reg_blocks(a.N, rsh);
         const size_t smem = (2 * kRegThreads + 2 * (size_t)rsh.NB * a.G) * sizeof(float);
         e = timed_launch(st, n, [&] {
@@ -658,7 +793,9 @@ size_t norm_scratch(int N, int S, int C, int G, int dtype, bool backward)
     for (int vec = norm_vec(C, G, dtype); vec >= 1; vec = narrower(vec, dtype)) {
         RegShape rsh;
         size_t n;
-        if (reg_shape(S, C, G, vec, &rsh)) {
+        if (row_lanes(S, C, G, vec)) {
+            n = backward ? (size_t)row_blocks(N, 256 / (C / vec)) * 2 * C * sizeof(double) : 0;
+        } else if (reg_shape(S, C, G, vec, &rsh)) {
             n = backward ? (size_t)reg_blocks(N, rsh) * 2 * C * sizeof(double) : 0;
         } else {
             const LongShape sh = long_shape(N, S, C, vec);

@@ -739,41 +739,62 @@ __global__ __launch_bounds__(256) void la_token_kernel(const __grid_constant__ L
     }
 }
 
-// One token: S = lam S + k v^T in place, o = scale q S.  A block holds 32 columns of
-// one head's state (lane = column, so that rows are read whole), its 8 warps share the rows.
-template <typename T>
-__global__ __launch_bounds__(256) void la_step_kernel(const __grid_constant__ LaStepArgs a, int slices)
+// One token: S = lam S + k v^T in place, o = scale q S.  Bound by the state, read and
+// written once: VEC columns a lane, `lanes` lanes a row, the rows shared by 8 warps with
+// four loads of each thread in flight.
+template <typename T, int VEC>
+__global__ __launch_bounds__(256) void la_step_kernel(const __grid_constant__ LaStepArgs a, int slices, int lanes)
 {
-    const int bh = blockIdx.x / slices, h = bh % a.H, b = bh / a.H;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = blockIdx.x % slices * 32 + lane;
-    const T *q = static_cast<const T *>(a.q) + b * a.qs[0] + h * a.qs[1];
-    const T *k = static_cast<const T *>(a.k) + b * a.ks[0] + h * a.ks[1];
+    const int bh = blockIdx.x / slices, h = bh % a.H, b = bh / a.H, tid = threadIdx.x;
+    const int lane = tid & 31, warp = tid >> 5, sub = lane / lanes, rows = 8 * (32 / lanes);
+    const int first = blockIdx.x % slices * lanes * VEC, col = first + lane % lanes * VEC;
+    __shared__ float sq[SEMICRF_MAX_HEAD], sk[SEMICRF_MAX_HEAD], red[8][32 * VEC];
+    for (int i = tid; i < a.dk; i += 256) {
+        sq[i] = to_f<T>((static_cast<const T *>(a.q) + b * a.qs[0] + h * a.qs[1])[i]);
+        sk[i] = to_f<T>((static_cast<const T *>(a.k) + b * a.ks[0] + h * a.ks[1])[i]);
+    }
     const T *v = static_cast<const T *>(a.v) + b * a.vs[0] + h * a.vs[1];
-    float *S = a.state + (long long)bh * a.dk * a.dv;
+    float *S = a.state + (long long)bh * a.dk * a.dv + col;
     const double lam = decay_pow(a.log_decay[h], 1);
     const float hi = (float)lam, lo = (float)(lam - (double)hi);
-    const bool in = col < a.dv;
-    const float vv = in ? to_f<T>(v[col]) : 0.f;
-    float o = 0.f;
-#pragma unroll 4
-    for (int i = warp; i < a.dk; i += 8) {
-        const float kk = to_f<T>(k[i]), qq = to_f<T>(q[i]);
-        if (in) {
-            const float s = S[(long long)i * a.dv + col];
-            const float n = fmaf(s, hi, fmaf(s, lo, kk * vv));
-            S[(long long)i * a.dv + col] = n;
-            o = fmaf(qq, n, o);
+    const bool in = col < a.dv;   // (VEC divides dv)
+    float vv[VEC], o[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        vv[e] = in ? to_f<T>(v[col + e]) : 0.f;
+        o[e] = 0.f;
+    }
+    __syncthreads();
+    if (in) {
+        constexpr int U = 4;
+        for (int i0 = warp * (32 / lanes) + sub; i0 < a.dk; i0 += U * rows) {
+            Pack<float, VEC> s[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * rows < a.dk)
+                    s[u] = *reinterpret_cast<const Pack<float, VEC> *>(S + (long long)(i0 + u * rows) * a.dv);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * rows;
+                if (i >= a.dk) break;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    s[u].v[e] = fmaf(s[u].v[e], hi, fmaf(s[u].v[e], lo, sk[i] * vv[e]));
+                    o[e] = fmaf(sq[i], s[u].v[e], o[e]);
+                }
+                *reinterpret_cast<Pack<float, VEC> *>(S + (long long)i * a.dv) = s[u];
+            }
         }
     }
-    __shared__ float red[8][32];
-    red[warp][lane] = o;
-    __syncthreads();
-    if (warp == 0 && in) {
-        o = 0.f;
+    // the row lanes' shares: red[warp][lane][e]
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o += red[j][lane];
-        (static_cast<T *>(a.o) + b * a.os[0] + h * a.os[1])[col] = from_f<T>(a.scale * o);
+    for (int e = 0; e < VEC; ++e) red[warp][lane * VEC + e] = o[e];
+    __syncthreads();
+    if (tid < lanes * VEC && first + tid < a.dv) {
+        float sum = 0.f;
+        for (int w = 0; w < 8; ++w)
+            for (int j = 0; j < 32 / lanes; ++j) sum += red[w][j * lanes * VEC + tid];
+        (static_cast<T *>(a.o) + b * a.os[0] + h * a.os[1])[first + tid] = from_f<T>(a.scale * sum);
     }
 }
 
@@ -841,11 +862,20 @@ cudaError_t go(const LaArgs &a, int width, cudaStream_t st, int *n)
     return go_walk<T, false>(a, width, st, n);
 }
 
-template <typename T>
+template <typename T, int VEC>
 cudaError_t go_step(const LaStepArgs &a, cudaStream_t st, int *n)
 {
-    const int slices = (a.dv + 31) / 32;
-    return timed_launch(st, n, [&] { la_step_kernel<T><<<a.B * a.H * slices, 256, 0, st>>>(a, slices); });
+    int lanes = 1;   // of one row: a power of two, 32 at most
+    while (lanes < 32 && lanes * VEC < a.dv) lanes *= 2;
+    const int slices = (a.dv + lanes * VEC - 1) / (lanes * VEC);
+    return timed_launch(st, n, [&] { la_step_kernel<T, VEC><<<a.B * a.H * slices, 256, 0, st>>>(a, slices, lanes); });
+}
+
+template <typename T>
+cudaError_t step_type(const LaStepArgs &a, cudaStream_t st, int *n)
+{
+    const bool wide = a.dv % 4 == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0;
+    return wide ? go_step<T, 4>(a, st, n) : go_step<T, 1>(a, st, n);
 }
 
 }  // namespace
@@ -891,9 +921,9 @@ cudaError_t launch_la(const LaArgs &a, int dtype, cudaStream_t st, int *launches
 cudaError_t launch_la_step(const LaStepArgs &a, int dtype, cudaStream_t st, int *launches)
 {
     *launches = 0;
-    if (dtype == SEMICRF_F32) return go_step<float>(a, st, launches);
-    if (dtype == SEMICRF_BF16) return go_step<__nv_bfloat16>(a, st, launches);
-    return go_step<__half>(a, st, launches);
+    if (dtype == SEMICRF_F32) return step_type<float>(a, st, launches);
+    if (dtype == SEMICRF_BF16) return step_type<__nv_bfloat16>(a, st, launches);
+    return step_type<__half>(a, st, launches);
 }
 
 }  // namespace semicrf

@@ -15,26 +15,27 @@ sequence's end is not read, and is zero in outputs.
 """
 from __future__ import annotations
 
-import contextlib
-import ctypes
-
 import torch
+from torch._C import _cuda_getCurrentRawStream as _raw_stream
 
 from . import _lib
 
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
 _TYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
-_SAME = contextlib.nullcontext()
-
-
-def _guard(device):
-    return _SAME if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+_functions = {}
 
 
 def _call(name, device, *args):
     """One library call on the device's current stream (appended as the last argument)."""
-    with _guard(device):
-        status = getattr(_lib.load(), "semicrf_" + name)(*args, torch.cuda.current_stream(device).cuda_stream)
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(_lib.load(), "semicrf_" + name)
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = f(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, _raw_stream(index))
     if status:
         _lib.check(status, name)
 
@@ -68,71 +69,74 @@ def _workspace(ws, need, device):
 
 # ---------------------------------------------------------------- linear attention
 
-def _operand(t, name, first, width=None):
-    """Checks one of q, k, v (or an upstream gradient) against `first`."""
+def _operand(t, name, q, shape):
+    """Checks k, v or an upstream gradient against q and the shape it has to have."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != first.dtype:
-        raise TypeError(f"{name} must be {first.dtype} like q, got {t.dtype}")
-    if t.dim() != first.dim() or t.shape[:-1] != first.shape[:-1] or (width is not None and t.shape[-1] != width):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, which does not match q {tuple(first.shape)}")
-    if t.device != first.device:
-        raise ValueError(f"{name} is on {t.device}, expected {first.device}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.dtype != q.dtype:
+        raise TypeError(f"{name} must be {q.dtype} like q, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, which does not match q {tuple(q.shape)}")
+    if t.device != q.device:
+        raise ValueError(f"{name} is on {t.device}, expected {q.device}")
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"the last axis of {name} must be dense")
+    return strides
 
 
-def _attention_dims(q, k, v, log_decay, scale, reverse, axes):
+def _attention(q, k, v, log_decay, axes):
+    """(device, type, shape of q, width of v, strides of q, k and v) of checked operands."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise TypeError("q must be a CUDA tensor")
-    if q.dtype not in _TYPES:
+    kind = _TYPES.get(q.dtype)
+    if kind is None:
         raise TypeError(f"q must be float32, bfloat16 or float16, got {q.dtype}")
-    if q.dim() != axes:
-        raise ValueError(f"q must have {axes} axes, got {q.dim()}")
-    dk, dv = q.shape[-1], v.shape[-1]
-    _operand(q, "q", q)
-    _operand(k, "k", q, dk)
-    _operand(v, "v", q)
+    shape = q.shape
+    if len(shape) != axes:
+        raise ValueError(f"q must have {axes} axes, got {len(shape)}")
+    device = q.device
+    qs = _operand(q, "q", q, shape)
+    ks = _operand(k, "k", q, shape)
+    dv = v.shape[-1] if isinstance(v, torch.Tensor) and v.dim() else 0
+    vs = _operand(v, "v", q, (*shape[:-1], dv))
     if log_decay.requires_grad:
         raise ValueError("log_decay is a constant: it has no gradient")
-    H = q.shape[-2]
-    _want(log_decay, "log_decay", torch.float32, (H,), q.device)
-    d = _lib.AttentionDims(q.shape[0], q.shape[1] if axes == 4 else 1, H, dk, dv, _TYPES[q.dtype], int(bool(reverse)),
-                           dk ** -0.5 if scale is None else scale)
-    _strides(d.q_stride, q)
-    _strides(d.k_stride, k)
-    _strides(d.v_stride, v)
-    return d
+    _want(log_decay, "log_decay", torch.float32, shape[-2:-1], device)
+    return device, kind, shape, dv, qs, ks, vs
 
 
-def _strides(to, t):
-    if t.dim() == 4:
-        to[0], to[1], to[2], _ = t.stride()
-    else:
-        to[0], to[2], _ = t.stride()
+def _dims(kind, shape, dv, scale, reverse, qs, ks, vs, os):
+    B, T, H, dk = shape
+    return _lib.ATTENTION_DIMS.pack(B, T, H, dk, dv, kind, 1 if reverse else 0, dk ** -0.5 if scale is None else scale,
+                                    *qs[:3], *ks[:3], *vs[:3], *os[:3])
 
 
-def _extras(q, dv, lengths, state, state_name):
-    B, H, dk = q.shape[0], q.shape[-2], q.shape[-1]
+def _extras(shape, dv, device, lengths, state, state_name):
     if lengths is not None:
-        _want(lengths, "lengths", torch.int32, (B,), q.device)
+        _want(lengths, "lengths", torch.int32, shape[:1], device)
     if state is not None:
-        _want(state, state_name, torch.float32, (B, H, dk, dv), q.device)
+        _want(state, state_name, torch.float32, (shape[0], shape[2], shape[3], dv), device)
 
 
 def linear_attention_workspace_bytes(q, v, backward=False) -> int:
     """Bytes of workspace of a call with operands like q [B,T,H,dk] and v [B,T,H,dv]."""
-    d = _lib.AttentionDims(*q.shape[:3], q.shape[3], v.shape[3], _TYPES[q.dtype], 0, 1.0)
-    return _attention_ws(d, backward)
+    none = (0, 0, 0)
+    return _attention_ws(_dims(_TYPES[q.dtype], q.shape, v.shape[3], 1.0, False, none, none, none, none), q.shape,
+                         v.shape[3], backward)
 
 
-def _attention_ws(d, backward):
-    n = _lib.load().semicrf_linear_attention_workspace_bytes(ctypes.byref(d), int(backward))
+def _attention_ws(dims, shape, dv, backward):
+    n = _lib.load().semicrf_linear_attention_workspace_bytes(dims, 1 if backward else 0)
     if n == 0:
-        bad = max(d.dk, d.dv) > _lib.MAX_HEAD
-        raise ValueError(f"unsupported dimensions: B {d.B}, T {d.T}, H {d.H}, dk {d.dk}, dv {d.dv}"
+        bad = max(shape[3], dv) > _lib.MAX_HEAD
+        raise ValueError(f"unsupported arguments: q {tuple(shape)}, width of v {dv}"
                          + (f" (at most {_lib.MAX_HEAD} wide)" if bad else ""))
     return n
+
+
+def _dense(shape, width):
+    return shape[1] * shape[2] * width, shape[2] * width, width
 
 
 def linear_attention_forward(q, k, v, log_decay, lengths=None, scale=None, initial_state=None, return_state=False,
@@ -140,14 +144,15 @@ def linear_attention_forward(q, k, v, log_decay, lengths=None, scale=None, initi
     """(o [B,T,H,dv], state [B,H,dk,dv] float32 or None): S = lam S + k v^T, o = scale q S
     with lam = exp(log_decay) (at most 1), from the first position on or, reversed, from
     the last valid one; scale None: dk ** -0.5."""
-    d = _attention_dims(q, k, v, log_decay, scale, reverse, 4)
-    _extras(q, d.dv, lengths, initial_state, "initial_state")
-    ws = _workspace(ws, _attention_ws(d, False), q.device)
-    o = torch.empty((d.B, d.T, d.H, d.dv), dtype=q.dtype, device=q.device)
-    _strides(d.o_stride, o)
-    state = torch.empty((d.B, d.H, d.dk, d.dv), dtype=torch.float32, device=q.device) if return_state else None
-    _call("linear_attention", q.device, ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lengths),
-          _ptr(initial_state), _ptr(o), _ptr(state), _ptr(ws), ws.numel())
+    device, kind, shape, dv, qs, ks, vs = _attention(q, k, v, log_decay, 4)
+    _extras(shape, dv, device, lengths, initial_state, "initial_state")
+    d = _dims(kind, shape, dv, scale, reverse, qs, ks, vs, _dense(shape, dv))
+    ws = _workspace(ws, _attention_ws(d, shape, dv, False), device)
+    B, T, H, dk = shape
+    o = torch.empty((B, T, H, dv), dtype=q.dtype, device=device)
+    state = torch.empty((B, H, dk, dv), dtype=torch.float32, device=device) if return_state else None
+    _call("linear_attention", device, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lengths),
+          _ptr(initial_state), o.data_ptr(), _ptr(state), ws.data_ptr(), ws.numel())
     return o, state
 
 
@@ -155,19 +160,20 @@ def linear_attention_backward(grad_o, q, k, v, log_decay, lengths=None, scale=No
                               grad_state=None, reverse=False, want_initial_state=False, ws=None):
     """(dq, dk, dv, d initial_state or None) for the upstream grad_o [B,T,H,dv] and, where
     the returned state was used, grad_state [B,H,dk,dv] float32."""
-    d = _attention_dims(q, k, v, log_decay, scale, reverse, 4)
-    _operand(grad_o, "grad_o", q, d.dv)
-    _extras(q, d.dv, lengths, initial_state, "initial_state")
-    _extras(q, d.dv, None, grad_state, "grad_state")
-    _strides(d.o_stride, grad_o)
-    ws = _workspace(ws, _attention_ws(d, True), q.device)
-    new = lambda width: torch.empty((d.B, d.T, d.H, width), dtype=q.dtype, device=q.device)  # noqa: E731
-    dq, dk, dv = new(d.dk), new(d.dk), new(d.dv)
-    ds = (torch.empty((d.B, d.H, d.dk, d.dv), dtype=torch.float32, device=q.device) if want_initial_state else None)
-    _call("linear_attention_backward", q.device, ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-          _ptr(lengths), _ptr(initial_state), _ptr(grad_o), _ptr(grad_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ds),
-          _ptr(ws), ws.numel())
-    return dq, dk, dv, ds
+    device, kind, shape, dv, qs, ks, vs = _attention(q, k, v, log_decay, 4)
+    os = _operand(grad_o, "grad_o", q, (*shape[:3], dv))
+    _extras(shape, dv, device, lengths, initial_state, "initial_state")
+    _extras(shape, dv, device, None, grad_state, "grad_state")
+    d = _dims(kind, shape, dv, scale, reverse, qs, ks, vs, os)
+    ws = _workspace(ws, _attention_ws(d, shape, dv, True), device)
+    B, T, H, dk = shape
+    new = lambda width: torch.empty((B, T, H, width), dtype=q.dtype, device=device)  # noqa: E731
+    dq, dk_, dv_ = new(dk), new(dk), new(dv)
+    ds = torch.empty((B, H, dk, dv), dtype=torch.float32, device=device) if want_initial_state else None
+    _call("linear_attention_backward", device, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+          _ptr(lengths), _ptr(initial_state), grad_o.data_ptr(), _ptr(grad_state), dq.data_ptr(), dk_.data_ptr(),
+          dv_.data_ptr(), _ptr(ds), ws.data_ptr(), ws.numel())
+    return dq, dk_, dv_, ds
 
 
 class LinearAttention(torch.autograd.Function):
@@ -222,14 +228,15 @@ def _differentiable(function, inputs, args, plain):
 def linear_attention_step(q, k, v, log_decay, state, scale=None):
     """One position: state [B,H,dk,dv] float32 becomes lam state + k v^T in place; returns
     o [B,H,dv] = scale q state.  q, k [B,H,dk], v [B,H,dv].  No gradient is recorded."""
-    d = _attention_dims(q, k, v, log_decay, scale, False, 3)
-    _want(state, "state", torch.float32, (d.B, d.H, d.dk, d.dv), q.device)
+    device, kind, (B, H, dk), dv, qs, ks, vs = _attention(q, k, v, log_decay, 3)
+    _want(state, "state", torch.float32, (B, H, dk, dv), device)
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or state.requires_grad):
         raise ValueError("linear_attention_step records no gradient: use linear_attention, or torch.no_grad()")
-    o = torch.empty((d.B, d.H, d.dv), dtype=q.dtype, device=q.device)
-    _strides(d.o_stride, o)
-    _call("linear_attention_step", q.device, ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state),
-          _ptr(o))
+    o = torch.empty((B, H, dv), dtype=q.dtype, device=device)
+    d = _lib.ATTENTION_DIMS.pack(B, 1, H, dk, dv, kind, 0, dk ** -0.5 if scale is None else scale, qs[0], 0, qs[1], ks[0],
+                                 0, ks[1], vs[0], 0, vs[1], H * dv, 0, dv)
+    _call("linear_attention_step", device, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+          state.data_ptr(), o.data_ptr())
     return o
 
 
@@ -247,7 +254,7 @@ def _norm_dims(x, groups, weight, bias, lengths, eps, activation):
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
     N, C = x.shape[0], x.shape[-1]
-    if groups < 1 or C % groups:
+    if not isinstance(groups, int) or groups < 1 or C % groups:
         raise ValueError(f"{C} channels do not split into {groups} groups")
     some = weight if weight is not None else bias
     wtype = torch.float32 if some is None else some.dtype
@@ -260,44 +267,46 @@ def _norm_dims(x, groups, weight, bias, lengths, eps, activation):
         if x.dim() != 3:
             raise ValueError("lengths need x of shape [N,S,C]")
         _want(lengths, "lengths", torch.int32, (N,), x.device)
-    return _lib.NormDims(N, x.numel() // (N * C), C, groups, _TYPES[x.dtype], _TYPES[wtype], ACTIVATIONS[activation],
-                         eps)
+    shape = (N, x.numel() // (N * C), C, groups)
+    return shape, _lib.NORM_DIMS.pack(*shape, _TYPES[x.dtype], _TYPES[wtype], ACTIVATIONS[activation], eps)
 
 
 def group_norm_workspace_bytes(x, groups, backward=False) -> int:
     """Bytes of workspace of a call with rows like x [N,...,C]."""
-    return _norm_ws(_norm_dims(x, groups, None, None, None, 1e-5, "none"), backward)
+    return _norm_ws(*_norm_dims(x, groups, None, None, None, 1e-5, "none"), backward)
 
 
-def _norm_ws(d, backward):
-    n = _lib.load().semicrf_group_norm_workspace_bytes(ctypes.byref(d), int(backward))
+def _norm_ws(shape, dims, backward):
+    n = _lib.load().semicrf_group_norm_workspace_bytes(dims, 1 if backward else 0)
     if n == 0:
-        raise ValueError(f"unsupported arguments: N {d.N}, S {d.S}, C {d.C}, groups {d.G}, eps {d.eps}")
+        raise ValueError(f"unsupported arguments: rows, positions, channels, groups {shape}, or eps")
     return n
 
 
 def group_norm_forward(x, groups, weight=None, bias=None, lengths=None, eps=1e-5, activation="none", ws=None):
     """(y like x, stats [N,groups,2] float32: mean and 1/std of the valid positions)."""
-    d = _norm_dims(x, groups, weight, bias, lengths, eps, activation)
-    ws = _workspace(ws, _norm_ws(d, False), x.device)
+    shape, d = _norm_dims(x, groups, weight, bias, lengths, eps, activation)
+    device = x.device
+    ws = _workspace(ws, _norm_ws(shape, d, False), device)
     y = torch.empty_like(x)
-    stats = torch.empty((d.N, d.G, 2), dtype=torch.float32, device=x.device)
-    _call("group_norm", x.device, ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(bias), _ptr(lengths), _ptr(y),
-          _ptr(stats), _ptr(ws), ws.numel())
+    stats = torch.empty((shape[0], groups, 2), dtype=torch.float32, device=device)
+    _call("group_norm", device, d, x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(lengths), y.data_ptr(),
+          stats.data_ptr(), ws.data_ptr(), ws.numel())
     return y, stats
 
 
 def group_norm_backward(dy, x, stats, groups, weight=None, bias=None, lengths=None, eps=1e-5, activation="none",
                         want_params=True, ws=None):
     """(dx like x, dweight [C] float32, dbias [C] float32); the last two None without want_params."""
-    d = _norm_dims(x, groups, weight, bias, lengths, eps, activation)
-    _want(dy, "dy", x.dtype, x.shape, x.device)
-    _want(stats, "stats", torch.float32, (d.N, d.G, 2), x.device)
-    ws = _workspace(ws, _norm_ws(d, True), x.device)
+    shape, d = _norm_dims(x, groups, weight, bias, lengths, eps, activation)
+    device = x.device
+    _want(dy, "dy", x.dtype, x.shape, device)
+    _want(stats, "stats", torch.float32, (shape[0], groups, 2), device)
+    ws = _workspace(ws, _norm_ws(shape, d, True), device)
     dx = torch.empty_like(x)
-    dw, db = (torch.empty((2, d.C), dtype=torch.float32, device=x.device) if want_params else (None, None))
-    _call("group_norm_backward", x.device, ctypes.byref(d), _ptr(dy), _ptr(x), _ptr(weight), _ptr(bias),
-          _ptr(lengths), _ptr(stats), _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), ws.numel())
+    dw, db = torch.empty((2, shape[2]), dtype=torch.float32, device=device) if want_params else (None, None)
+    _call("group_norm_backward", device, d, dy.data_ptr(), x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(lengths),
+          stats.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db), ws.data_ptr(), ws.numel())
     return dx, dw, db
 
 
