@@ -164,8 +164,9 @@ __device__ __forceinline__ void step8(const semicrf_adamw_tensor &t, const semic
         double gj = g[j] * c.grad_scale;
         double old = value_of<15>(cm.v[j] & 127u);
         old = cm.v[j] & 128u ? -old : old;
-        m[j] = fma(n1, gj, c.beta1 * (old * sm));
-        v[j] = fma(n2 * gj, gj, c.beta2 * (value_of<31>(cv.v[j]) * sv));
+        // (rounded operation by operation: what the formula gives on any machine, ties included)
+        m[j] = __dadd_rn(__dmul_rn(c.beta1, __dmul_rn(old, sm)), __dmul_rn(n1, gj));
+        v[j] = __dadd_rn(__dmul_rn(c.beta2, __dmul_rn(value_of<31>(cv.v[j]), sv)), __dmul_rn(__dmul_rn(n2, gj), gj));
         const float fm = (float)m[j], fv = (float)v[j];
         p[j] = next_param(p[j], fm, fv, f);
         mm = __uint_as_float(max(__float_as_uint(mm), __float_as_uint(fabsf(fm))));   // NaN above infinity

@@ -192,7 +192,7 @@ __global__ __launch_bounds__(kRegThreads, U == 1 ? (BWD ? 2 : 3) : 1) void norm_
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) sum += f[e];
                 }
-            mu = inv * total(sum, red, mean);
+            mu = total(sum, red, mean) / fmaxf((float)L * Cg, 1.f);   // (a constant's mean is that constant)
             sum = 0.f;
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -337,7 +337,7 @@ __global__ __launch_bounds__(256) void norm_row_kernel(const __grid_constant__ N
             if constexpr (!BWD) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) sum += f[e];
-                const float mu = warp_sum(sum, lanes) * inv;
+                const float mu = warp_sum(sum, lanes) / (float)(a.C / a.G);   // (a constant's mean is that constant)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     f[e] -= mu;
