@@ -21,11 +21,15 @@ namespace {
 constexpr int kThreads = 256, kPer = 8;            // values of one thread at a time
 constexpr int kBlock = 256;                        // values that share a scale
 constexpr int kSpan = 2 * kThreads * kPer;         // values of one thread block
-constexpr int kFew = 48, kMany = 448;              // tensors of one launch (3.4 and 32 KB of arguments)
+constexpr int kFew = 48, kMany = 440;              // tensors of one launch (3.4 and 32 KB of arguments)
 
 struct Entry {
     semicrf_adamw_tensor t;
     long long first;   // first thread block
+};
+
+struct Factors {
+    float b1, b2, n1, n2, decay, lr, root2, eps;
 };
 
 template <int N>
@@ -33,7 +37,22 @@ struct AdamArgs {
     Entry e[N];
     int count;
     semicrf_adamw_config c;
+    Factors f;   // of c, where step and lr are host values
 };
+
+__host__ __device__ inline Factors factors_of(const semicrf_adamw_config &c, double step, double lr)
+{
+    Factors f;
+    f.b1 = (float)c.beta1;
+    f.b2 = (float)c.beta2;
+    f.n1 = (float)(1.0 - c.beta1);
+    f.n2 = (float)(1.0 - c.beta2);
+    f.decay = (float)(1.0 - lr * c.weight_decay);
+    f.lr = (float)(lr / (1.0 - pow(c.beta1, step)));
+    f.root2 = (float)(1.0 / sqrt(1.0 - pow(c.beta2, step)));
+    f.eps = (float)c.eps;
+    return f;
+}
 
 template <typename R, typename T>
 __device__ __forceinline__ R cvt(T v)
@@ -54,8 +73,15 @@ __device__ __forceinline__ void load8(const void *p, long long i, int cnt, bool 
         Pack<T, n> h[kPer / n];
 #pragma unroll
         for (int j = 0; j < kPer / n; ++j) h[j] = reinterpret_cast<const Pack<T, n> *>(s)[j];
+        if constexpr (sizeof(T) == 2) {
+            float f[kPer];
+            unpack(h[0], f);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) o[j] = cvt<R, T>(h[j / n].v[j % n]);
+            for (int j = 0; j < kPer; ++j) o[j] = (R)f[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) o[j] = (R)h[j / n].v[j % n];
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) o[j] = j < cnt ? cvt<R, T>(s[j]) : (R)0;
@@ -83,10 +109,10 @@ __device__ __forceinline__ void store8(void *p, long long i, int cnt, bool vec, 
     if (vec) {
 #pragma unroll
         for (int j = 0; j < kPer / n; ++j) {
-            Pack<T, n> h;
+            float f[n];
 #pragma unroll
-            for (int e = 0; e < n; ++e) h.v[e] = from_f<T>(o[j * n + e]);
-            reinterpret_cast<Pack<T, n> *>(s)[j] = h;
+            for (int e = 0; e < n; ++e) f[e] = o[j * n + e];
+            reinterpret_cast<Pack<T, n> *>(s)[j] = pack<T, n>(f);
         }
     } else {
 #pragma unroll
@@ -108,13 +134,23 @@ __device__ __forceinline__ uint32_t code_of(double y)
     return ((h + 0xffffu + ((h >> 17) & 1u)) >> 17) - ((1023u - BIAS) << 3);
 }
 
-// The value of a code, without its block's scale.
+// The value of a code, without its block's scale: its bits are those of a double (or
+// float) with another bias, but for the codes below 8, which have no leading bit.
 template <int BIAS>
-__device__ __forceinline__ double value_of(uint32_t c)
+__device__ __forceinline__ double value_of(uint32_t c, bool some_small)
 {
-    const uint32_t e = c >> 3, f = c & 7;
-    const double v = __hiloint2double((int)(((max(e, 1u) + 1023u - BIAS) << 20) | (f << 17)), 0);
-    return e ? v : v - pow2(1 - BIAS);
+    if (some_small) {   // of this warp
+        const bool small = c < 8;
+        const double v = __hiloint2double((int)((c + (small ? 8u : 0u) + (1023u - BIAS) * 8) << 17), 0);
+        return small ? v - pow2(1 - BIAS) : v;
+    }
+    return __hiloint2double((int)((c + (1023u - BIAS) * 8) << 17), 0);
+}
+
+template <int BIAS>
+__device__ __forceinline__ float float_value_of(uint32_t c)
+{
+    return __uint_as_float(c << 20) * __uint_as_float((127u + 127u - BIAS) << 23);   // (a float's own small values)
 }
 
 __device__ __forceinline__ float block_scale(float most)
@@ -123,13 +159,12 @@ __device__ __forceinline__ float block_scale(float most)
     return (float)((double)__uint_as_float(bits) / 1.875);
 }
 
-struct Factors {
-    float b1, b2, n1, n2, decay, lr, root2, eps;
-};
-
 __device__ __forceinline__ float next_param(float p, float m, float v, const Factors &f)
 {
-    return fmaf(p, f.decay, -f.lr * m / fmaf(sqrtf(v), f.root2, f.eps));
+    // square root and quotient to two units of the last place: far inside the parameter's rounding
+    float root;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));
+    return fmaf(p, f.decay, __fdividef(-f.lr * m, fmaf(root, f.root2, f.eps)));
 }
 
 // One call of a warp: 256 consecutive values, which is one block of scales.
@@ -159,14 +194,23 @@ __device__ __forceinline__ void step8(const semicrf_adamw_tensor &t, const semic
     const double n1 = 1.0 - c.beta1, n2 = 1.0 - c.beta2;
     double m[kPer], v[kPer];
     float mm = 0.f, mv = 0.f;
+    bool small_m = false, small_v = false;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        double gj = g[j] * c.grad_scale;
-        double old = value_of<15>(cm.v[j] & 127u);
-        old = cm.v[j] & 128u ? -old : old;
+        small_m |= (cm.v[j] & 127u) < 8;
+        small_v |= cv.v[j] < 8;
+    }
+    small_m = __any_sync(0xffffffffu, small_m);
+    small_v = __any_sync(0xffffffffu, small_v);
+    const bool scaled = c.grad_scale != 1.0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const double gj = scaled ? g[j] * c.grad_scale : g[j];
+        const double mag = value_of<15>(cm.v[j] & 127u, small_m);
+        const double old = __hiloint2double(__double2hiint(mag) | (int)((uint32_t)(cm.v[j] & 128u) << 24), __double2loint(mag));
         // (rounded operation by operation: what the formula gives on any machine, ties included)
         m[j] = __dadd_rn(__dmul_rn(c.beta1, __dmul_rn(old, sm)), __dmul_rn(n1, gj));
-        v[j] = __dadd_rn(__dmul_rn(c.beta2, __dmul_rn(value_of<31>(cv.v[j]), sv)), __dmul_rn(__dmul_rn(n2, gj), gj));
+        v[j] = __dadd_rn(__dmul_rn(c.beta2, __dmul_rn(value_of<31>(cv.v[j], small_v), sv)), __dmul_rn(__dmul_rn(n2, gj), gj));
         const float fm = (float)m[j], fv = (float)v[j];
         p[j] = next_param(p[j], fm, fv, f);
         mm = __uint_as_float(max(__float_as_uint(mm), __float_as_uint(fabsf(fm))));   // NaN above infinity
@@ -240,20 +284,14 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const __grid_constant__
     const Entry &en = a.e[entry_of<N>(a, blockIdx.x)];
     const semicrf_adamw_tensor &t = en.t;
     const semicrf_adamw_config &c = a.c;
-    __shared__ Factors sf;
-    if (threadIdx.x == 0) {
-        const double step = (double)(c.step_ptr ? *c.step_ptr : c.step), lr = c.lr_ptr ? (double)*c.lr_ptr : c.lr;
-        sf.b1 = (float)c.beta1;
-        sf.b2 = (float)c.beta2;
-        sf.n1 = (float)(1.0 - c.beta1);
-        sf.n2 = (float)(1.0 - c.beta2);
-        sf.decay = (float)(1.0 - lr * c.weight_decay);
-        sf.lr = (float)(lr / (1.0 - pow(c.beta1, step)));
-        sf.root2 = (float)(1.0 / sqrt(1.0 - pow(c.beta2, step)));
-        sf.eps = (float)c.eps;
+    Factors f = a.f;
+    if (c.step_ptr || c.lr_ptr) {   // two float64 powers: not each block's work where the host knows them
+        __shared__ Factors sf;
+        if (threadIdx.x == 0)
+            sf = factors_of(c, (double)(c.step_ptr ? *c.step_ptr : c.step), c.lr_ptr ? (double)*c.lr_ptr : c.lr);
+        __syncthreads();
+        f = sf;
     }
-    __syncthreads();
-    const Factors f = sf;
     const bool all = aligned16(t.param) && aligned16(t.grad) &&
                      (EIGHT || (aligned16(t.exp_avg) && aligned16(t.exp_avg_sq)));
     const long long from = (blockIdx.x - en.first) * (long long)kSpan;
@@ -305,8 +343,8 @@ __global__ __launch_bounds__(kThreads) void adamw_values_kernel(const __grid_con
         float o[kPer];
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            const float mag = (float)(SECOND ? value_of<31>(c.v[j]) : value_of<15>(c.v[j] & 127u)) * s;
-            o[j] = !SECOND && (c.v[j] & 128u) ? -mag : mag;
+            const float mag = (SECOND ? float_value_of<31>(c.v[j]) : float_value_of<15>(c.v[j] & 127u)) * s;
+            o[j] = SECOND ? mag : __uint_as_float(__float_as_uint(mag) | (uint32_t)(c.v[j] & 128u) << 24);
         }
         store8<float>(t.param, i, cnt, vec, o);
     }
@@ -318,6 +356,7 @@ cudaError_t launch_some(const semicrf_adamw_tensor *t, int count, const semicrf_
 {
     static thread_local AdamArgs<N> a;   // 32 KB at most: kept off the stack
     a.c = c;
+    a.f = factors_of(c, (double)c.step, c.lr);
     a.count = 0;
     long long blocks = 0;
     for (int i = 0; i < count; ++i) {
