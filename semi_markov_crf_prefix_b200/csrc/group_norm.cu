@@ -465,20 +465,31 @@ __global__ __launch_bounds__(kLongThreads, 3) void norm_sums_kernel(const __grid
                     q[e] = fmaf(d, d, q[e]);
                 }
             };
-            const Pack<T, VEC> first = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s0 + r) * a.C);
-            unpack(first, about);
-            int s = s0 + r + sh.R;
-            cnt = 1;
-            constexpr int U = 8;
+            constexpr int U = 8;   // loads in flight
+            int s = s0 + r;
             for (; s + (U - 1) * sh.R < s1; s += U * sh.R, cnt += U) {
                 Pack<T, VEC> x[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     x[u] = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s + u * sh.R) * a.C);
+                if (cnt == 0) unpack(x[0], about);
 #pragma unroll
                 for (int u = 0; u < U; ++u) add(x[u]);
             }
-            for (; s < s1; s += sh.R, ++cnt) add(*reinterpret_cast<const Pack<T, VEC> *>(px + (long long)s * a.C));
+            if (s < s1) {   // the strip's last rows, together as well
+                Pack<T, VEC> x[U];
+#pragma unroll
+                for (int u = 0; u < U - 1; ++u)
+                    if (s + u * sh.R < s1)
+                        x[u] = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s + u * sh.R) * a.C);
+                if (cnt == 0) unpack(x[0], about);
+#pragma unroll
+                for (int u = 0; u < U - 1; ++u)
+                    if (s + u * sh.R < s1) {
+                        add(x[u]);
+                        ++cnt;
+                    }
+            }
         } else {
             float wt[VEC], bs[VEC];
 #pragma unroll
@@ -501,21 +512,19 @@ __global__ __launch_bounds__(kLongThreads, 3) void norm_sums_kernel(const __grid
                         q[e] += dz;
                     }
                 };
-                int s = s0 + r;
                 constexpr int U = 4;
-                for (; s + (U - 1) * sh.R < s1; s += U * sh.R) {
+                for (int s = s0 + r; s < s1; s += U * sh.R) {
                     Pack<T, VEC> x[U], dy[U];
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        x[u] = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s + u * sh.R) * a.C);
-                        dy[u] = *reinterpret_cast<const Pack<T, VEC> *>(pd + (long long)(s + u * sh.R) * a.C);
-                    }
+                    for (int u = 0; u < U; ++u)
+                        if (s + u * sh.R < s1) {
+                            x[u] = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s + u * sh.R) * a.C);
+                            dy[u] = *reinterpret_cast<const Pack<T, VEC> *>(pd + (long long)(s + u * sh.R) * a.C);
+                        }
 #pragma unroll
-                    for (int u = 0; u < U; ++u) add(x[u], dy[u]);
+                    for (int u = 0; u < U; ++u)
+                        if (s + u * sh.R < s1) add(x[u], dy[u]);
                 }
-                for (; s < s1; s += sh.R)
-                    add(*reinterpret_cast<const Pack<T, VEC> *>(px + (long long)s * a.C),
-                        *reinterpret_cast<const Pack<T, VEC> *>(pd + (long long)s * a.C));
             });
         }
     }
@@ -541,20 +550,53 @@ __global__ __launch_bounds__(kLongThreads, 3) void norm_sums_kernel(const __grid
     }
 }
 
-// (n, g): mean and 1/std (forward), or the means of w dz and w dz xh (backward, to gsum [N,G,2]).
+// (n, g): mean and 1/std (forward), or the means of w dz and w dz xh (backward, to gsum
+// [N,G,2]) and row block n's share of dw and db (to total [N][2][C]).  Thread (x, y): channel
+// x of the group (and x + X, ..), strand y of the strips.
 template <typename T, bool BWD>
-__global__ void norm_group_kernel(const __grid_constant__ NormArgs a, int strips, float *gsum)
+__global__ __launch_bounds__(256) void norm_group_kernel(const __grid_constant__ NormArgs a, int strips, float *gsum,
+                                                         double *total, int X)
 {
-    const int n = blockIdx.x / a.G, g = blockIdx.x % a.G, Cg = a.C / a.G;
+    const int n = blockIdx.x / a.G, g = blockIdx.x % a.G, Cg = a.C / a.G, Y = 256 / X;
+    const int x = threadIdx.x % X, y = threadIdx.x / X;
     const double *part = a.part + (long long)n * strips * 2 * a.C + g * Cg;
-    double A = 0.0, B = 0.0;
-    for (int i = threadIdx.x; i < strips * Cg; i += blockDim.x) {
-        const double *p = part + (long long)(i / Cg) * 2 * a.C + i % Cg;
-        const double w = BWD ? (double)weight_at<T>(a.weight, a.wdtype, g * Cg + i % Cg, 1.f) : 1.0;
-        A += w * p[0];
-        B += w * p[a.C];
+    __shared__ double sa[256], sb[256];
+    double A = 0.0, B = 0.0;   // the group's
+    for (int c0 = 0; c0 < Cg; c0 += X) {
+        const int c = c0 + x;
+        double p = 0.0, q = 0.0;
+        if (c < Cg) {
+#pragma unroll 4
+            for (int i = y; i < strips; i += Y) {
+                p += part[(long long)i * 2 * a.C + c];
+                q += part[(long long)i * 2 * a.C + a.C + c];
+            }
+        }
+        if (!BWD) {
+            A += p;
+            B += q;
+            continue;
+        }
+        __syncthreads();
+        sa[threadIdx.x] = p;
+        sb[threadIdx.x] = q;
+        for (int half = Y / 2; half > 0; half >>= 1) {
+            __syncthreads();
+            if (y < half) {
+                sa[threadIdx.x] += sa[threadIdx.x + half * X];
+                sb[threadIdx.x] += sb[threadIdx.x + half * X];
+            }
+        }
+        if (y == 0 && c < Cg) {
+            const double w = (double)weight_at<T>(a.weight, a.wdtype, g * Cg + c, 1.f);
+            A += w * sa[x];
+            B += w * sb[x];
+            double *t = total + (long long)n * 2 * a.C + g * Cg + c;
+            t[0] = sa[x];
+            t[a.C] = sb[x];
+        }
     }
-    __shared__ double sa[32], sb[32];
+    __syncthreads();
     A = warp_sum(A, 32);
     B = warp_sum(B, 32);
     if ((threadIdx.x & 31) == 0) {
@@ -564,7 +606,7 @@ __global__ void norm_group_kernel(const __grid_constant__ NormArgs a, int strips
     __syncthreads();
     if (threadIdx.x == 0) {
         A = B = 0.0;
-        for (int j = 0; j < (int)(blockDim.x >> 5); ++j) {
+        for (int j = 0; j < 8; ++j) {
             A += sa[j];
             B += sb[j];
         }
@@ -714,9 +756,10 @@ int row_lanes(int S, int C, int G, int vec)
     return S == 1 && C / vec <= 256 && CgV <= 32 && (CgV & (CgV - 1)) == 0 ? CgV : 0;
 }
 
-int row_blocks(int N, int rows)
+// As many as an SM holds of them (48 and 80 registers a thread).
+int row_blocks(int N, int rows, bool backward)
 {
-    const int blocks = (N + rows - 1) / rows, most = 6 * device_sm_count();
+    const int blocks = (N + rows - 1) / rows, most = (backward ? 3 : 5) * device_sm_count();
     return blocks < most ? blocks : most;
 }
 
@@ -737,7 +780,7 @@ cudaError_t norm_go(NormArgs a, cudaStream_t st, int *n)
     cudaError_t e;
     int prows;
     if (const int lanes = row_lanes(a.S, a.C, a.G, VEC)) {
-        const int CV = a.C / VEC, rows = 256 / CV, blocks = row_blocks(a.N, rows);
+        const int CV = a.C / VEC, rows = 256 / CV, blocks = row_blocks(a.N, rows, BWD);
         e = timed_launch(st, n, [&] { norm_row_kernel<T, VEC, BWD><<<blocks, 256, 0, st>>>(a, CV, rows, lanes); });
         if (e != cudaSuccess) return e;
         prows = blocks;
@@ -755,16 +798,19 @@ cudaError_t norm_go(NormArgs a, cudaStream_t st, int *n)
     } else {
         const LongShape sh = long_shape(a.N, a.S, a.C, VEC);
         const dim3 grid((unsigned)(a.N * sh.strips), sh.tiles);
-        float *gsum = reinterpret_cast<float *>(a.part + (size_t)a.N * sh.strips * 2 * a.C);
+        double *total = a.part + (size_t)a.N * sh.strips * 2 * a.C;
+        float *gsum = reinterpret_cast<float *>(total + (BWD ? (size_t)a.N * 2 * a.C : 0));
+        const int X = pow2_at_least(a.C / a.G, 256);
         e = timed_launch(st, n, [&] {
             norm_sums_kernel<T, VEC, BWD><<<grid, kLongThreads, 2 * kLongThreads * sizeof(double), st>>>(a, sh);
         });
         if (e != cudaSuccess) return e;
-        e = timed_launch(st, n, [&] { norm_group_kernel<T, BWD><<<a.N * a.G, 256, 0, st>>>(a, sh.strips, gsum); });
+        e = timed_launch(st, n, [&] { norm_group_kernel<T, BWD><<<a.N * a.G, 256, 0, st>>>(a, sh.strips, gsum, total, X); });
         if (e != cudaSuccess) return e;
         e = timed_launch(st, n, [&] { norm_apply_kernel<T, VEC, BWD><<<grid, kLongThreads, 0, st>>>(a, sh, gsum); });
         if (e != cudaSuccess) return e;
-        prows = a.N * sh.strips;
+        prows = a.N;
+        a.part = total;
     }
     if (!BWD || (!a.dw && !a.db)) return cudaSuccess;
     return timed_launch(st, n, [&] {
@@ -794,12 +840,13 @@ size_t norm_scratch(int N, int S, int C, int G, int dtype, bool backward)
         RegShape rsh;
         size_t n;
         if (row_lanes(S, C, G, vec)) {
-            n = backward ? (size_t)row_blocks(N, 256 / (C / vec)) * 2 * C * sizeof(double) : 0;
+            n = backward ? (size_t)row_blocks(N, 256 / (C / vec), true) * 2 * C * sizeof(double) : 0;
         } else if (reg_shape(S, C, G, vec, &rsh)) {
             n = backward ? (size_t)reg_blocks(N, rsh) * 2 * C * sizeof(double) : 0;
         } else {
             const LongShape sh = long_shape(N, S, C, vec);
-            n = (size_t)N * sh.strips * 2 * C * sizeof(double) + (backward ? (size_t)N * G * 2 * sizeof(float) : 0);
+            n = (size_t)N * sh.strips * 2 * C * sizeof(double) +
+                (backward ? (size_t)N * 2 * C * sizeof(double) + (size_t)N * G * 2 * sizeof(float) : 0);
         }
         if (n > most) most = n;
     }
