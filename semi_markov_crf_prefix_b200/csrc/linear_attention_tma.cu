@@ -423,13 +423,17 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
                 tc_after_sync();
                 const float f = lead ? ofull : w.b * (float)decay_pow(ld, rev ? kChunk - 1 - row : row);
 #pragma unroll 1
-                for (int c = 0; c < D / 2; c += 16) {
-                    uint32_t r[16];
-                    tmem_ld16(tlane + G::kO + c0 + c, r);
+                for (int c = 0; c < D / 2; c += 32) {
+                    uint32_t r[2][16];
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) tmem_ld16(tlane + G::kO + c0 + c + 16 * g, r[g]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-                    tmem_st16(tlane + G::kO + c0 + c, r);
+                    for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) r[g][e] = __float_as_uint(__uint_as_float(r[g][e]) * f);
+                        tmem_st16(tlane + G::kO + c0 + c + 16 * g, r[g]);
+                    }
                 }
                 tmem_wait_st();
                 tc_before_sync();
@@ -447,18 +451,24 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
             }
             if constexpr (G::kStateTmem) {
 #pragma unroll 1
-                for (int c = c0; c < min(c0 + D / 2, nv); c += 16) {
-                    uint32_t r[16], old[16];
-                    tmem_ld16(tlane + G::kKV + c, r);
-                    tmem_ld16(tlane + G::kState + c, old);
+                for (int c = c0; c < min(c0 + D / 2, nv); c += 32) {
+                    uint32_t r[2][16], old[2][16];
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        tmem_ld16(tlane + G::kKV + c + 16 * g, r[g]);
+                        tmem_ld16(tlane + G::kState + c + 16 * g, old[g]);
+                    }
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float prev = __uint_as_float(old[e]);
-                        old[e] = __float_as_uint(fmaf(prev, hi, fmaf(prev, lo, __uint_as_float(r[e]))));
+                    for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float prev = __uint_as_float(old[g][e]);
+                            old[g][e] = __float_as_uint(fmaf(prev, hi, fmaf(prev, lo, __uint_as_float(r[g][e]))));
+                        }
+                        tmem_st16(tlane + G::kState + c + 16 * g, old[g]);
+                        if (!STATE_ONLY) put_row(c + 16 * g, old[g]);
                     }
-                    tmem_st16(tlane + G::kState + c, old);
-                    if (!STATE_ONLY) put_row(c, old);
                 }
                 tmem_wait_st();
                 tc_before_sync();
@@ -476,12 +486,12 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
                 await(done_pv, parity);
                 tc_after_sync();
 #pragma unroll 1
-                for (int c = 0; c < D / 2; c += 16) {
-                    uint32_t r[16];
-                    tmem_ld16(tlane + G::kO + c0 + c, r);
+                for (int c = 0; c < D / 2; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(tlane + G::kO + c0 + c, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
+                    for (int g = 0; g < 4; ++g) {
                         uint32_t o[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
