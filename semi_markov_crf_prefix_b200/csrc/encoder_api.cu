@@ -44,10 +44,7 @@ semicrf_status attention_ok(const semicrf_attention_dims *d)
 
 size_t attention_ws(const semicrf_attention_dims &d, bool backward)
 {
-    int seg_len;
-    const int walks = backward ? 3 : 1;
-    const int n = la_segments(d.B, d.T, d.H, d.dk, d.dv, d.dtype, walks, &seg_len);
-    return kStatusBytes + (n > 1 ? walks * up256((size_t)d.B * d.H * n * d.dk * d.dv * sizeof(float)) : 0);
+    return kStatusBytes + la_workspace(d.B, d.T, d.H, d.dk, d.dv, d.dtype, backward ? 3 : 1);
 }
 
 // Pieces of 8 values can be moved in 16-byte accesses: width, strides and address allow it.
@@ -81,13 +78,9 @@ LaArgs attention_args(const semicrf_attention_dims &d, const float *log_decay, c
     a.B = d.B;
     a.T = d.T;
     a.H = d.H;
-    a.nseg = la_segments(d.B, d.T, d.H, d.dk, d.dv, d.dtype, nwalk, &a.seg_len);
     a.log_decay = log_decay;
     a.lengths = lengths;
     a.status = static_cast<int32_t *>(ws);
-    const size_t one = up256((size_t)d.B * d.H * a.nseg * d.dk * d.dv * sizeof(float));
-    for (int i = 0; i < nwalk && a.nseg > 1; ++i)
-        a.w[i].seg = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + kStatusBytes + i * one);
     return a;
 }
 
@@ -174,7 +167,7 @@ semicrf_status semicrf_linear_attention(const semicrf_attention_dims *dims, cons
     w.lead = 1;
     finish_walk(w, d.dtype);
     int n = 0;
-    cudaError_t e = launch_la(a, d.dtype, static_cast<cudaStream_t>(stream), &n);
+    cudaError_t e = launch_la(a, d.dtype, static_cast<unsigned char *>(ws) + kStatusBytes, static_cast<cudaStream_t>(stream), &n);
     return ended(e, n);
 }
 
@@ -253,7 +246,7 @@ semicrf_status semicrf_linear_attention_backward(const semicrf_attention_dims *d
     z.lead = 0;
     for (LaWalk &w : a.w) finish_walk(w, d.dtype);
     int n = 0;
-    cudaError_t e = launch_la(a, d.dtype, static_cast<cudaStream_t>(stream), &n);
+    cudaError_t e = launch_la(a, d.dtype, static_cast<unsigned char *>(ws) + kStatusBytes, static_cast<cudaStream_t>(stream), &n);
     return ended(e, n);
 }
 

@@ -102,7 +102,8 @@ struct LaWalk {
     const float *s_in;                      // [B,H] states, element (i,j) at i * s_rs + j * s_cs, or null
     float *s_out;                           // same addressing, or null
     int s_rs, s_cs;
-    float *seg;                             // [B,H,nseg] states at the segments' starts (dk x dv), or null
+    float *seg;                             // [B,H,slices,nseg] states at the segments' starts (width x width), or null
+    float *part;                            // [B,T,H,dv] float32 sums over the first blocks of the contraction, or null
     float b, c;
     int reverse;                            // walk from the last valid position to the first
     int lead;                               // power of lam the given state has at the first position
@@ -115,6 +116,7 @@ struct LaArgs {
     int nwalk;
     int B, T, H;
     int nseg, seg_len;                      // segments of seg_len positions (whole sequences when nseg == 1)
+    int width, slices, kblock;              // tiles of `width`: a launch takes block kblock of dk, and every slice of dv
     const float *log_decay;
     const int32_t *lengths;                 // or null
     int32_t *status;
@@ -130,9 +132,10 @@ struct LaStepArgs {
     float scale;
 };
 
-int la_segments(int B, int T, int H, int dk, int dv, int dtype, int nwalk, int *seg_len);
-cudaError_t launch_la(const LaArgs &a, int dtype, cudaStream_t st, int *launches);
-bool la_tma_walk(const LaArgs &a, int width, bool state_only, cudaStream_t st, int *launches, cudaError_t *e);
+size_t la_workspace(int B, int T, int H, int dk, int dv, int dtype, int nwalk);
+cudaError_t launch_la(LaArgs a, int dtype, unsigned char *ws, cudaStream_t st, int *launches);
+bool la_tma_ok(const LaArgs &a, int dtype);
+cudaError_t launch_la_tma(const LaArgs &a, bool state_only, cudaStream_t st, int *launches);
 cudaError_t launch_la_step(const LaStepArgs &a, int dtype, cudaStream_t st, int *launches);
 
 // ---- group norm ----

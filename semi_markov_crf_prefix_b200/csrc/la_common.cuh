@@ -18,19 +18,26 @@ __device__ __forceinline__ double decay_pow(float log_decay, long long n)
     return n == 0 ? 1.0 : exp((double)log_decay * (double)n);
 }
 
-// One block of the walk: (sequence b, head h, segment seg).
+// One block of the walk: sequence b, head h, columns j0 .. j0 + dv of the values (slice z),
+// rows d0 .. d0 + dk of the state, segment seg.
 struct LaSpan {
-    int b, h, seg, L, p0, pe, p1;
+    int b, h, z, seg, L, p0, pe, p1;
+    int d0, dk, j0, dv;   // dk or dv <= 0: nothing here
     bool last;
 };
 
-__device__ __forceinline__ LaSpan la_span(const LaArgs &a, int idx)
+__device__ __forceinline__ LaSpan la_span(const LaArgs &a, const LaWalk &w, int idx)
 {
     LaSpan s;
     s.seg = idx % a.nseg;
-    const int bh = idx / a.nseg;
+    const int bhz = idx / a.nseg, bh = bhz / a.slices;
+    s.z = bhz % a.slices;
     s.h = bh % a.H;
     s.b = bh / a.H;
+    s.d0 = a.kblock * a.width;
+    s.dk = min(a.width, w.dk - s.d0);
+    s.j0 = s.z * a.width;
+    s.dv = min(a.width, w.dv - s.j0);
     int L = a.T;
     if (a.lengths) {
         L = a.lengths[s.b];
@@ -50,25 +57,36 @@ __device__ __forceinline__ LaSpan la_span(const LaArgs &a, int idx)
 
 // Positions behind the sequence's end: zeros.
 template <typename T>
-__device__ __forceinline__ void zero_rows(const LaWalk &w, const LaSpan &s, int d_begin, int d_end)
+__device__ __forceinline__ void zero_rows(const LaWalk &w, const LaSpan &s)
 {
-    T *o = static_cast<T *>(w.o) + s.b * w.os[0] + s.h * w.os[2];
-    const int n = d_end - d_begin;
+    T *o = static_cast<T *>(w.o) + s.b * w.os[0] + s.h * w.os[2] + s.j0;
     const int from = max(s.p0, s.L);
-    for (long long i = threadIdx.x; i < (long long)(s.p1 - from) * n; i += blockDim.x)
-        o[(from + i / n) * w.os[1] + d_begin + i % n] = from_f<T>(0.f);
+    for (long long i = threadIdx.x; i < (long long)(s.p1 - from) * s.dv; i += blockDim.x)
+        o[(from + i / s.dv) * w.os[1] + i % s.dv] = from_f<T>(0.f);
+}
+
+// Where this block's rows and columns of a given or returned state begin.
+__device__ __forceinline__ long long state_at(const LaWalk &w, const LaArgs &a, const LaSpan &s)
+{
+    return ((long long)s.b * a.H + s.h) * w.dk * w.dv + (long long)s.d0 * w.s_rs + (long long)s.j0 * w.s_cs;
 }
 
 // A sequence without positions hands its state on.
-__device__ __forceinline__ void copy_state(const LaWalk &w, const LaArgs &a, const LaSpan &s, int j0, int j1)
+__device__ __forceinline__ void copy_state(const LaWalk &w, const LaArgs &a, const LaSpan &s)
 {
     if (!w.s_out) return;
-    const long long base = ((long long)s.b * a.H + s.h) * w.dk * w.dv;
-    const int n = j1 - j0;
-    for (int i = threadIdx.x; i < w.dk * n; i += blockDim.x) {
-        const long long at = base + (long long)(i / n) * w.s_rs + (long long)(j0 + i % n) * w.s_cs;
+    const long long base = state_at(w, a, s);
+    for (int i = threadIdx.x; i < s.dk * s.dv; i += blockDim.x) {
+        const long long at = base + (long long)(i / s.dv) * w.s_rs + (long long)(i % s.dv) * w.s_cs;
         w.s_out[at] = w.s_in ? w.s_in[at] : 0.f;
     }
+}
+
+// This segment's state in the workspace: width x width.
+__device__ __forceinline__ float *segment_at(const LaWalk &w, const LaArgs &a, const LaSpan &s)
+{
+    const long long bhz = ((long long)s.b * a.H + s.h) * a.slices + s.z;
+    return w.seg + (bhz * a.nseg + s.seg) * a.width * a.width;
 }
 
 // Where the walk of this segment takes its state from, element (i, j) at i * rs + j * cs.
@@ -79,9 +97,8 @@ struct StateAt {
 
 __device__ __forceinline__ StateAt state_from(const LaWalk &w, const LaArgs &a, const LaSpan &s)
 {
-    const long long bh = (long long)s.b * a.H + s.h, sz = (long long)w.dk * w.dv;
-    if (w.seg) return {w.seg + (bh * a.nseg + s.seg) * sz, w.dv, 1};
-    return {w.s_in ? w.s_in + bh * sz : nullptr, w.s_rs, w.s_cs};
+    if (w.seg) return {segment_at(w, a, s), a.width, 1};
+    return {w.s_in ? w.s_in + state_at(w, a, s) : nullptr, w.s_rs, w.s_cs};
 }
 
 // Products of operands in NA and NB terms: go(x, y, accumulate) for the pairs of terms

@@ -1,7 +1,7 @@
 // linear_attention.cu -- linear attention with a decay for each head:
 //   S_p = lam S_{p-1} + c k_p v_p^T,   o_p = b q_p S_p = b c sum_{j<=p} lam^{p-j} (q_p . k_j) v_j + b lam^{p+1} q_p S_in
-// over whole sequences (la_chunk_kernel, la_token_kernel) and for single tokens
-// (la_step_kernel).  The backward runs the same walks with exchanged operands:
+// over whole sequences (la_chunk_kernel; la_tma_kernel for bf16 that the copy engine can
+// address) and for single tokens (la_step_kernel).  The backward runs the same walks with exchanged operands:
 //   dq = walk(dO, V, K)   dv = walk back in time(K, Q, dO)   dk = walk back in time(V, dO, Q).
 #include "la_common.cuh"
 #include "tensor_core.cuh"
@@ -25,37 +25,43 @@ struct Track {
 // registers to spare for it, and a spilled register comes back from L2 (400 cycles:
 // the tiles leave next to nothing of the L1 cache).
 struct LaHot {
-    Track q, k, v, o;
+    Track q, k, v, o, part;
     float b, c;
-    int lead, pe;
+    int lead, pe, adds, final;
 };
 
-// Shapes of the chunked walk for padded width D.  Operands enter the matrix unit as
-// sums of bf16 terms: NI for the inputs (exact), NM for the products P and for the
-// state as an operand of q S (2: 2^-17 relative, far inside the rounding of a 16-bit
-// output; 3 for float32), NK = 3 for the decayed keys, whose products make the
-// float32 state.
-template <typename T, int D>
+// Shapes of the chunked walk.  Tiles are 64 wide: wider heads are sums over blocks of
+// the contraction (o is linear in the scores, and the state's rows are independent), a
+// launch each, and slices of the values' columns, which are independent.  Operands
+// enter the matrix unit as sums of bf16 terms: NI for the inputs (exact), NM for the
+// products P and for the state as an operand of q S (2: 2^-17 relative, far inside the
+// rounding of a 16-bit output; 3 for float32), NK = 3 for the decayed keys, whose
+// products make the float32 state.
+constexpr int D = 64;
+
+template <typename T>
 struct LaCfg {
     static constexpr int NI = kTerms<T>, NM = NI == 3 ? 3 : 2, NK = 3;
-    static constexpr bool kStateTmem = D == 128;   // the float32 state: tensor memory, or 16 registers a thread
     static constexpr int kCol = tile_col(kChunk), kSCol = D * 16;   // (threads write S along columns)
     static constexpr int kTile = D / 8 * kCol, kSTile = D / 8 * kSCol;
     static constexpr int kQ = 0, kK = kQ + NI * kTile, kV = kK + NK * kTile, kS = kV + NI * kTile;
     // decays lam^0 .. lam^128, and P's factors by (row - column) + 127, zero above the diagonal
     static constexpr int kDec = kS + NM * kSTile, kPf = kDec + (kChunk + 4) * 4, kMisc = kPf + 2 * kChunk * 4;
     static constexpr int kSmem = kMisc + 32 + (int)sizeof(LaHot);
-    // tensor memory columns: scores (P replaces them where two terms fit the same columns), o, k v^T, state
-    static constexpr int kP = NM == 3 ? 128 : 0, kO = NM == 3 ? 320 : 128, kKV = kO + D, kState = kKV + D;
-    static constexpr int kCols = kState + (kStateTmem ? D : 0) <= 256 ? 256 : 512;
+    // tensor memory columns: scores (P replaces them where two terms fit the same columns), o, k v^T
+    static constexpr int kP = NM == 3 ? 128 : 0, kO = NM == 3 ? 320 : 128, kKV = kO + D;
+    static constexpr int kCols = kKV + D <= 256 ? 256 : 512;
     static constexpr int kBlocks = kCols == 256 && kSmem <= 113 * 1024 ? 2 : 1;
     // where q S waits for the scores' part of o: scaled in its accumulator, or (float32,
     // where that costs 1e-6 to the accumulator's rounding) in registers
     static constexpr bool kKeep = NI == 3;
     static constexpr int NP = kChunk * (D / 8) / 256;   // 8-value pieces of a tile for each of 256 threads
     static constexpr int kRows = 256 / (D / 8);         // tile rows between a thread's pieces
+    // a chunk's outputs on their way, in float32: in K~'s tiles, behind the one that the next keys of
+    // bf16 go to at once
+    static constexpr int kOut = kK + (NI == 1 ? kTile : 0);
     static_assert(kSmem <= 227 * 1024, "shared memory");
-    static_assert((NK - (NI == 3 ? 0 : NI)) * kTile >= kChunk * D * (int)sizeof(T), "room for a chunk's outputs");
+    static_assert(kK + NK * kTile - kOut >= kChunk * D * 4, "room for a chunk's outputs");
 };
 
 template <typename T>
@@ -87,10 +93,10 @@ __device__ __forceinline__ void store_terms(unsigned char *at, int tile_stride, 
 }
 
 template <typename T>
-__device__ __forceinline__ Track track_of(const void *base, const long long (&st)[3], int d, int vec, const LaSpan &s,
-                                          int reverse)
+__device__ __forceinline__ Track track_of(const void *base, const long long (&st)[3], int from, int d, int vec,
+                                          const LaSpan &s, int reverse)
 {
-    const T *p = static_cast<const T *>(base) + s.b * st[0] + s.h * st[2] + (reverse ? (s.L - 1) * st[1] : 0);
+    const T *p = static_cast<const T *>(base) + s.b * st[0] + s.h * st[2] + (reverse ? (s.L - 1) * st[1] : 0) + from;
     return {reinterpret_cast<unsigned char *>(const_cast<T *>(p)), reverse ? -st[1] : st[1], d, vec};
 }
 
@@ -161,23 +167,25 @@ __device__ __forceinline__ void bring_pieces(const Track &g, unsigned char *to, 
 // each 8 steps of 16), which a state carried in them over thousands of chunks would
 // show; so they hold one chunk's sums only, small terms first, and the state is
 // advanced by float32 multiply-adds to nearest.
-template <typename T, int D, bool STATE_ONLY>
-__global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(const __grid_constant__ LaArgs args)
+template <typename T, bool STATE_ONLY>
+__global__ __launch_bounds__(256, (LaCfg<T>::kBlocks)) void la_chunk_kernel(const __grid_constant__ LaArgs args)
 {
-    using G = LaCfg<T, D>;
+    using G = LaCfg<T>;
     constexpr int NI = G::NI, NM = G::NM, NK = G::NK, NP = G::NP;
     // steps of 16 values of a contraction, and of one tile, in a descriptor's units
     constexpr uint64_t kCol2 = 2 * G::kCol >> 4, kRow2 = 2 * 128 >> 4, 
                        kTileD = G::kTile >> 4, kSTileD = G::kSTile >> 4;
     extern __shared__ __align__(128) unsigned char sm[];
     const LaWalk &w = args.w[blockIdx.y];
-    const LaSpan s = la_span(args, blockIdx.x);
+    const LaSpan s = la_span(args, w, blockIdx.x);
+    if (s.dk <= 0 || s.dv <= 0) return;
+    const bool final = s.d0 + s.dk == w.dk;   // this launch completes the sums of o
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int quad = warp & 3, half = warp >> 2;
     if (STATE_ONLY && s.seg == args.nseg - 1) return;
     if (!STATE_ONLY) {
-        zero_rows<T>(w, s, 0, w.dv);
-        if (s.L == 0 && s.last) copy_state(w, args, s, 0, w.dv);
+        if (final) zero_rows<T>(w, s);
+        if (s.L == 0 && s.last) copy_state(w, args, s);
     }
     if (s.pe == s.p0) return;
 
@@ -209,10 +217,15 @@ __global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(c
 
     const int r0 = tid / (D / 8), d8 = tid % (D / 8), at0 = d8 * G::kCol + r0 * 16;
     if (tid == 0) {
-        hot.q = track_of<T>(w.q, w.qs, w.dk, w.q_vec, s, w.reverse);
-        hot.k = track_of<T>(w.k, w.ks, w.dk, w.k_vec, s, w.reverse);
-        hot.v = track_of<T>(w.v, w.vs, w.dv, w.v_vec, s, w.reverse);
-        hot.o = track_of<T>(w.o, w.os, w.dv, w.o_vec, s, w.reverse);
+        hot.q = track_of<T>(w.q, w.qs, s.d0, s.dk, w.q_vec, s, w.reverse);
+        hot.k = track_of<T>(w.k, w.ks, s.d0, s.dk, w.k_vec, s, w.reverse);
+        hot.v = track_of<T>(w.v, w.vs, s.j0, s.dv, w.v_vec, s, w.reverse);
+        hot.o = track_of<T>(w.o, w.os, s.j0, s.dv, w.o_vec, s, w.reverse);
+        // sums over the contraction's first blocks: in o itself where that is float32
+        const long long ps[3] = {(long long)args.T * args.H * w.dv, (long long)args.H * w.dv, w.dv};
+        hot.part = sizeof(T) == 4 ? hot.o : track_of<float>(w.part, ps, s.j0, s.dv, w.dv % 4 == 0, s, w.reverse);
+        hot.adds = s.d0 > 0;
+        hot.final = final;
         hot.b = w.b;
         hot.c = w.c;
         hot.lead = w.lead;
@@ -235,16 +248,15 @@ __global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(c
     __syncthreads();
     tc_after_sync();
     const uint32_t tm = __shfl_sync(0xffffffffu, *slot, 0), tlane = tm + ((uint32_t)(quad * 32) << 16);
-    const int nv = (w.dv + 15) / 16 * 16, kd = (w.dk + 15) / 16, c0 = half * (D / 2);
+    const int nv = (s.dv + 15) / 16 * 16, kd = (s.dk + 15) / 16, c0 = half * (D / 2);
 
-    // The state.  D = 64: rows quad * 16 + lane / 4 (+ 8), column pairs c0 + 8 j + 2 (lane % 4)
-    // in registers; D = 128: row quad * 32 + lane, columns c0 .. c0 + 63 in tensor memory.
-    float S[G::kStateTmem ? 1 : 16];
+    // the state: rows quad * 16 + lane / 4 (+ 8), column pairs c0 + 8 j + 2 (lane % 4)
+    float S[16];
     const StateAt from = STATE_ONLY ? StateAt{nullptr, 0, 0} : state_from(w, args, s);
     auto given = [&](int row, int col) {
-        return from.p && row < w.dk && col < w.dv ? from.p[(long long)row * from.rs + (long long)col * from.cs] : 0.f;
+        return from.p && row < s.dk && col < s.dv ? from.p[(long long)row * from.rs + (long long)col * from.cs] : 0.f;
     };
-    auto put_pairs = [&] {   // D = 64: the terms of S to shared memory
+    auto put_pairs = [&] {   // its terms to shared memory
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -256,39 +268,10 @@ __global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(c
                 for (int x = 0; x < NM; ++x) *reinterpret_cast<uint32_t *>(to + x * G::kSTile) = t[x];
             }
     };
-    auto put_row = [&](int c, const uint32_t (&r)[16]) {   // D = 128: 16 columns of this thread's row
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            uint32_t o[NM][4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t t[NM];
-                split2<NM>(__uint_as_float(r[8 * g + 2 * e]), __uint_as_float(r[8 * g + 2 * e + 1]), t);
-#pragma unroll
-                for (int x = 0; x < NM; ++x) o[x][e] = t[x];
-            }
-#pragma unroll
-            for (int x = 0; x < NM; ++x)
-                *reinterpret_cast<uint4 *>(sm + G::kS + x * G::kSTile + (c / 8 + g) * G::kSCol + (quad * 32 + lane) * 16) =
-                    make_uint4(o[x][0], o[x][1], o[x][2], o[x][3]);
-        }
-    };
-    if constexpr (G::kStateTmem) {
-#pragma unroll 1
-        for (int c = c0; c < c0 + D / 2; c += 16) {
-            uint32_t r[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(given(quad * 32 + lane, c + e));
-            tmem_st16(tlane + G::kState + c, r);
-            put_row(c, r);
-        }
-        tmem_wait_st();
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            S[i] = given(quad * 16 + (lane >> 2) + (i & 2) * 4, c0 + (i >> 2) * 8 + (lane & 3) * 2 + (i & 1));
-        put_pairs();
-    }
+    for (int i = 0; i < 16; ++i)
+        S[i] = given(quad * 16 + (lane >> 2) + (i & 2) * 4, c0 + (i >> 2) * 8 + (lane & 3) * 2 + (i & 1));
+    put_pairs();
 
     if constexpr (kDirect) {
         bring(hot.q, G::kQ, s.p0);
@@ -481,11 +464,10 @@ __global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(c
             }
 
         if (!STATE_ONLY) {
-            // rows to shared memory (the part of K~'s tiles that the next keys leave
-            // alone), then whole rows to global memory; 16-byte pieces of a row are
-            // exchanged by the row's number so that neither side meets bank conflicts
-            constexpr int n = 16 / sizeof(T), W = D / n;   // values of a piece, pieces of a row
-            unsigned char *ob = sm + G::kK + (NI == 3 ? 0 : NI * G::kTile);
+            // rows to shared memory, then whole rows to global memory; 16-byte pieces of a
+            // row are exchanged by the row's number so that neither side meets bank conflicts
+            constexpr int W = D / 4;   // pieces of a row
+            unsigned char *ob = sm + G::kOut;
             const int row = quad * 32 + lane;
 #pragma unroll
             for (int c = 0; c < D / 2; c += 16) {
@@ -493,32 +475,46 @@ __global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(c
                 tmem_ld16(tlane + G::kO + c0 + c, r);
                 tmem_wait_ld();
 #pragma unroll
-                for (int g = 0; g < 16 / n; ++g) {
-                    Pack<T, n> o;
+                for (int g = 0; g < 4; ++g) {
+                    float o[4];
 #pragma unroll
-                    for (int e = 0; e < n; ++e)
-                        o.v[e] = from_f<T>(__uint_as_float(r[g * n + e]) + (G::kKeep ? qs[G::kKeep ? c + g * n + e : 0] : 0.f));
-                    *reinterpret_cast<Pack<T, n> *>(ob + (row * W + (((c0 + c) / n + g) ^ (row & 7))) * 16) = o;
+                    for (int e = 0; e < 4; ++e)
+                        o[e] = __uint_as_float(r[g * 4 + e]) + (G::kKeep ? qs[G::kKeep ? c + g * 4 + e : 0] : 0.f);
+                    *reinterpret_cast<float4 *>(ob + (row * W + (((c0 + c) / 4 + g) ^ (row & 7))) * 16) =
+                        make_float4(o[0], o[1], o[2], o[3]);
                 }
             }
             asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");   // the two halves of these 32 rows
-            const Track to = hot.o;
+            const Track to = hot.o, part = hot.part;
+            const bool adds = hot.adds, ends = hot.final;
             T *og = reinterpret_cast<T *>(to.at) + pc * to.step;
-#pragma unroll
+            float *pg = reinterpret_cast<float *>(part.at) + pc * part.step;
+#pragma unroll 2
             for (int j = 0; j < W / 2; ++j) {
-                const int i = j * 64 + half * 32 + lane, rr = quad * 32 + i / W, piece = i % W, col = piece * n;
+                const int i = j * 64 + half * 32 + lane, rr = quad * 32 + i / W, piece = i % W, col = piece * 4;
                 if (pc + rr >= hot.pe || col >= to.d) continue;
-                const Pack<T, n> o = *reinterpret_cast<const Pack<T, n> *>(ob + (rr * W + (piece ^ (rr & 7))) * 16);
+                const float4 v = *reinterpret_cast<const float4 *>(ob + (rr * W + (piece ^ (rr & 7))) * 16);
+                float o[4] = {v.x, v.y, v.z, v.w};
+                float *p = pg + rr * part.step + col;
                 T *at = og + rr * to.step + col;
-                if (to.vec) {
-                    *reinterpret_cast<Pack<T, n> *>(at) = o;
+                if (adds) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col + e < to.d) o[e] += p[e];
+                }
+                if (!ends) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col + e < to.d) p[e] = o[e];
+                } else if (to.vec) {
+                    *reinterpret_cast<Pack<T, 4> *>(at) = pack<T, 4>(o);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < n; ++e)
-                        if (col + e < to.d) at[e] = o.v[e];
+                    for (int e = 0; e < 4; ++e)
+                        if (col + e < to.d) at[e] = from_f<T>(o[e]);
                 }
             }
-            if (NI == 3) __syncthreads();   // the next keys go where these rows were
+            if (NI != 1) __syncthreads();   // the next keys go where these rows were
         }
         // S = lam^n S + KV, and its terms for the next chunk.  The float32 rounding of
         // lam^n alone would bias a state that lives for many chunks: two parts.
@@ -528,56 +524,25 @@ __global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(c
             hi = (float)step;
             lo = (float)(step - (double)hi);
         }
-        if constexpr (G::kStateTmem) {
-#pragma unroll 1
-            for (int c = c0; c < min(c0 + D / 2, nv); c += 16) {
-                uint32_t r[16], old[16];
-                tmem_ld16(tlane + G::kKV + c, r);
-                tmem_ld16(tlane + G::kState + c, old);
-                tmem_wait_ld();
+        uint32_t r[16];
+        tmem_ld16x256(tlane + G::kKV + c0, r);
+        tmem_wait_ld();
+        // (columns from nv on are not computed: their values stay out of every result)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float prev = __uint_as_float(old[e]);
-                    old[e] = __float_as_uint(fmaf(prev, hi, fmaf(prev, lo, __uint_as_float(r[e]))));
-                }
-                tmem_st16(tlane + G::kState + c, old);
-                if (!STATE_ONLY) put_row(c, old);
-            }
-            tmem_wait_st();
-        } else {
-            uint32_t r[16];
-            tmem_ld16x256(tlane + G::kKV + c0, r);
-            tmem_wait_ld();
-            // (columns from nv on are not computed: their values stay out of every result)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) S[i] = fmaf(S[i], hi, fmaf(S[i], lo, __uint_as_float(r[i])));
-            if (!STATE_ONLY) put_pairs();
-        }
+        for (int i = 0; i < 16; ++i) S[i] = fmaf(S[i], hi, fmaf(S[i], lo, __uint_as_float(r[i])));
+        if (!STATE_ONLY) put_pairs();
     }
     if (!alive && tid == 0) set_status(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
 
     // the state behind the last position (or behind this segment)
-    const long long bh = (long long)s.b * args.H + s.h, sz = (long long)w.dk * w.dv;
-    float *to = STATE_ONLY ? w.seg + (bh * args.nseg + s.seg) * sz : s.last && w.s_out ? w.s_out + bh * sz : nullptr;
+    float *to = STATE_ONLY ? segment_at(w, args, s) : s.last && w.s_out ? w.s_out + state_at(w, args, s) : nullptr;
     if (to) {
-        const int rs = STATE_ONLY ? w.dv : w.s_rs, cs = STATE_ONLY ? 1 : w.s_cs;
+        const int rs = STATE_ONLY ? args.width : w.s_rs, cs = STATE_ONLY ? 1 : w.s_cs;
         const float f = !STATE_ONLY && w.out_decay ? dec[1] : 1.f;
-        auto keep = [&](int row, int col, float v) {
-            if (row < w.dk && col < w.dv) to[(long long)row * rs + (long long)col * cs] = f * v;
-        };
-        if constexpr (G::kStateTmem) {
-#pragma unroll 1
-            for (int c = c0; c < min(c0 + D / 2, nv); c += 16) {
-                uint32_t r[16];
-                tmem_ld16(tlane + G::kState + c, r);
-                tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) keep(quad * 32 + lane, c + e, __uint_as_float(r[e]));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                keep(quad * 16 + (lane >> 2) + (i & 2) * 4, c0 + (i >> 2) * 8 + (lane & 3) * 2 + (i & 1), S[i]);
+        for (int i = 0; i < 16; ++i) {
+            const int row = quad * 16 + (lane >> 2) + (i & 2) * 4, col = c0 + (i >> 2) * 8 + (lane & 3) * 2 + (i & 1);
+            if (row < s.dk && col < s.dv) to[(long long)row * rs + (long long)col * cs] = f * S[i];
         }
     }
     tc_before_sync();
@@ -589,152 +554,28 @@ __global__ __launch_bounds__(256, (LaCfg<T, D>::kBlocks)) void la_chunk_kernel(c
 __global__ void la_join_kernel(const __grid_constant__ LaArgs args)
 {
     const LaWalk &w = args.w[blockIdx.z];
-    const int sz = w.dk * w.dv, i = blockIdx.y * blockDim.x + threadIdx.x, nseg = args.nseg;
-    const LaSpan s = la_span(args, blockIdx.x * nseg);
+    const int W = args.width, i = blockIdx.y * blockDim.x + threadIdx.x, row = i / W, col = i % W, nseg = args.nseg;
+    const LaSpan s = la_span(args, w, blockIdx.x * nseg);
     __shared__ double power[2];   // of a whole segment: the first one, the others
     if (threadIdx.x < 2)
         power[threadIdx.x] = decay_pow(args.log_decay[s.h], args.seg_len - 1 + (threadIdx.x ? 1 : w.lead));
     __syncthreads();
-    if (i >= sz) return;
-    const long long bh = blockIdx.x;
-    float *seg = w.seg + bh * nseg * sz + i;
+    if (row >= s.dk || col >= s.dv) return;
+    float *seg = segment_at(w, args, s) + i;
+    const long long sz = (long long)W * W;
     // segments before the last one that are whole: their sums exist
     const int whole = min(nseg - 1, s.L / args.seg_len);
-    float carry = w.s_in ? w.s_in[bh * sz + (long long)(i / w.dv) * w.s_rs + (long long)(i % w.dv) * w.s_cs] : 0.f;
+    float carry = w.s_in ? w.s_in[state_at(w, args, s) + (long long)row * w.s_rs + (long long)col * w.s_cs] : 0.f;
     constexpr int U = 8;   // loads in flight
     for (int j0 = 0; j0 <= whole; j0 += U) {
         float add[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) add[u] = j0 + u < whole ? seg[(long long)(j0 + u) * sz] : 0.f;
+        for (int u = 0; u < U; ++u) add[u] = j0 + u < whole ? seg[(j0 + u) * sz] : 0.f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (j0 + u > whole) break;
-            seg[(long long)(j0 + u) * sz] = carry;
+            seg[(j0 + u) * sz] = carry;
             carry = (float)(power[j0 + u > 0] * (double)carry + (double)add[u]);
-        }
-    }
-}
-
-// The walk token by token, for widths and types whose chunk tiles do not fit one SM.
-// A block holds 32 of the state's columns: lane = column, warp = an eighth of the
-// rows (RP registers a thread).  Inside 16 positions the state is kept relative to
-// its block's start, A = sum lam^{-p} c k v^T, so that a position costs two
-// multiply-adds a state element and rounding enters once in 16 positions; where
-// lam^{-16} would be large (few positions remembered) the decay is applied at each position.
-
-template <typename T, int RP, bool STATE_ONLY>
-__global__ __launch_bounds__(256) void la_token_kernel(const __grid_constant__ LaArgs args, int slices)
-{
-    const LaWalk &w = args.w[blockIdx.y];
-    const LaSpan s = la_span(args, blockIdx.x / slices);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int j0 = blockIdx.x % slices * 32, j1 = min(w.dv, j0 + 32), col = j0 + lane;
-    if (j0 >= w.dv) return;
-    if (STATE_ONLY && s.seg == args.nseg - 1) return;
-    if (!STATE_ONLY) {
-        zero_rows<T>(w, s, j0, j1);
-        if (s.L == 0 && s.last) copy_state(w, args, s, j0, j1);
-    }
-    if (s.pe == s.p0) return;
-    constexpr int DK = RP * 8, kTok = RP > 16 ? 8 : 16;   // (the tiles stay below 48 KB)
-    __shared__ __align__(16) float sq[STATE_ONLY ? 1 : kTok][DK], sk[kTok][DK], sv[kTok][32];
-    __shared__ float red[kTok][8][33], sg[kTok], sd[kTok];
-    const float ld = args.log_decay[s.h];
-    const bool far = ld * kTok < -20.f;   // lam^-16 > e^20
-    const double lam1 = decay_pow(ld, 1);
-    if (tid < kTok) {
-        sg[tid] = far ? w.c : (float)(w.c * decay_pow(ld, -(tid + 1)));
-        sd[tid] = far ? 1.f : (float)decay_pow(ld, tid + 1);
-    }
-    const T *qb = static_cast<const T *>(w.q) + s.b * w.qs[0] + s.h * w.qs[2];
-    const T *kb = static_cast<const T *>(w.k) + s.b * w.ks[0] + s.h * w.ks[2];
-    const T *vb = static_cast<const T *>(w.v) + s.b * w.vs[0] + s.h * w.vs[2];
-    T *ob = static_cast<T *>(w.o) + s.b * w.os[0] + s.h * w.os[2];
-    float S[RP];
-    const StateAt from = STATE_ONLY ? StateAt{nullptr, 0, 0} : state_from(w, args, s);
-#pragma unroll
-    for (int i = 0; i < RP; ++i) {
-        const int row = warp * RP + i;
-        S[i] = from.p && row < w.dk && col < w.dv ? from.p[(long long)row * from.rs + (long long)col * from.cs] : 0.f;
-    }
-    int skip = s.seg == 0 && w.lead == 0;   // the given state's first decay is left out
-    for (int pc = s.p0; pc < s.pe; pc += kTok) {
-        const int cnt = min(kTok, s.pe - pc);
-        __syncthreads();
-        for (int i = tid; i < kTok * DK; i += 256) {
-            const int r = i / DK, d = i % DK, p = pc + r;
-            const long long t = w.reverse ? s.L - 1 - p : p;
-            const bool in = r < cnt && d < w.dk;
-            if (!STATE_ONLY) sq[r][d] = in ? to_f<T>(qb[t * w.qs[1] + d]) : 0.f;
-            sk[r][d] = in ? to_f<T>(kb[t * w.ks[1] + d]) : 0.f;
-        }
-        for (int i = tid; i < kTok * 32; i += 256) {
-            const int r = i / 32, d = j0 + i % 32, p = pc + r;
-            const long long t = w.reverse ? s.L - 1 - p : p;
-            sv[r][i % 32] = r < cnt && d < w.dv ? to_f<T>(vb[t * w.vs[1] + d]) : 0.f;
-        }
-        __syncthreads();
-        if (skip && !far) {   // lam^{p} instead of lam^{p+1} for the state that was given
-            const double up = decay_pow(ld, -1);
-#pragma unroll
-            for (int i = 0; i < RP; ++i) S[i] = (float)((double)S[i] * up);
-            skip = 0;
-        }
-#pragma unroll 1
-        for (int r = 0; r < cnt; ++r) {
-            if (far) {
-                if (!skip) {
-#pragma unroll
-                    for (int i = 0; i < RP; ++i) S[i] *= (float)lam1;
-                }
-                skip = 0;
-            }
-            const float vc = sv[r][lane] * sg[r];
-            float o = 0.f;
-#pragma unroll
-            for (int i = 0; i < RP; i += 4) {
-                const float4 k4 = *reinterpret_cast<const float4 *>(&sk[r][warp * RP + i]);
-                S[i] = fmaf(k4.x, vc, S[i]);
-                S[i + 1] = fmaf(k4.y, vc, S[i + 1]);
-                S[i + 2] = fmaf(k4.z, vc, S[i + 2]);
-                S[i + 3] = fmaf(k4.w, vc, S[i + 3]);
-                if (!STATE_ONLY) {
-                    const float4 q4 = *reinterpret_cast<const float4 *>(&sq[r][warp * RP + i]);
-                    o = fmaf(q4.x, S[i], o);
-                    o = fmaf(q4.y, S[i + 1], o);
-                    o = fmaf(q4.z, S[i + 2], o);
-                    o = fmaf(q4.w, S[i + 3], o);
-                }
-            }
-            if (!STATE_ONLY) red[r][warp][lane] = o * sd[r];
-        }
-        if (!far) {
-            const double step = decay_pow(ld, cnt);
-            const float hi = (float)step, lo = (float)(step - (double)hi);
-#pragma unroll
-            for (int i = 0; i < RP; ++i) S[i] = fmaf(S[i], hi, S[i] * lo);
-        }
-        if (!STATE_ONLY) {
-            __syncthreads();
-            for (int i = tid; i < cnt * 32; i += 256) {
-                const int r = i / 32, d = i % 32, p = pc + r;
-                const long long t = w.reverse ? s.L - 1 - p : p;
-                float o = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o += red[r][j][d];
-                if (j0 + d < w.dv) ob[t * w.os[1] + j0 + d] = from_f<T>(w.b * o);
-            }
-        }
-    }
-    const long long bh = (long long)s.b * args.H + s.h, sz = (long long)w.dk * w.dv;
-    float *to = STATE_ONLY ? w.seg + (bh * args.nseg + s.seg) * sz : s.last && w.s_out ? w.s_out + bh * sz : nullptr;
-    if (to && col < w.dv) {
-        const int rs = STATE_ONLY ? w.dv : w.s_rs, cs = STATE_ONLY ? 1 : w.s_cs;
-        const float f = !STATE_ONLY && w.out_decay ? (float)lam1 : 1.f;
-#pragma unroll
-        for (int i = 0; i < RP; ++i) {
-            const int row = warp * RP + i;
-            if (row < w.dk) to[(long long)row * rs + (long long)col * cs] = f * S[i];
         }
     }
 }
@@ -798,68 +639,24 @@ __global__ __launch_bounds__(256) void la_step_kernel(const __grid_constant__ La
     }
 }
 
-// Which walk serves these widths: the padded width of the chunked walk (64 or 128), or 0
-// for the token walk.  Chunk tiles hold kTerms terms of q, k, v: 128 columns fit an SM's
-// shared memory in one term (bf16) only.
-int la_width(int dk, int dv, int dtype)
-{
-    const int d = dk > dv ? dk : dv;
-    if (d <= 64) return 64;
-    return d <= 128 && dtype == SEMICRF_BF16 ? 128 : 0;
-}
-
-template <typename T, int D, bool STATE_ONLY>
+template <typename T, bool STATE_ONLY>
 cudaError_t go_chunk(const LaArgs &a, cudaStream_t st, int *n)
 {
-    using G = LaCfg<T, D>;
-    cudaError_t e = cudaFuncSetAttribute(la_chunk_kernel<T, D, STATE_ONLY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         G::kSmem);
+    using G = LaCfg<T>;
+    cudaError_t e = cudaFuncSetAttribute(la_chunk_kernel<T, STATE_ONLY>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
     if (e != cudaSuccess) return e;
     return timed_launch(st, n, [&] {
-        la_chunk_kernel<T, D, STATE_ONLY><<<dim3(a.B * a.H * a.nseg, a.nwalk), 256, G::kSmem, st>>>(a);
+        la_chunk_kernel<T, STATE_ONLY><<<dim3(a.B * a.H * a.slices * a.nseg, a.nwalk), 256, G::kSmem, st>>>(a);
     });
 }
 
-template <typename T, int RP, bool STATE_ONLY>
-cudaError_t go_token(const LaArgs &a, cudaStream_t st, int *n)
+template <bool STATE_ONLY>
+cudaError_t go_walk(const LaArgs &a, int dtype, bool tma, cudaStream_t st, int *n)
 {
-    int dv = 0;
-    for (int i = 0; i < a.nwalk; ++i) dv = a.w[i].dv > dv ? a.w[i].dv : dv;
-    const int slices = (dv + 31) / 32;
-    return timed_launch(st, n, [&] {
-        la_token_kernel<T, RP, STATE_ONLY><<<dim3(a.B * a.H * a.nseg * slices, a.nwalk), 256, 0, st>>>(a, slices);
-    });
-}
-
-template <typename T, bool STATE_ONLY>
-cudaError_t go_walk(const LaArgs &a, int width, cudaStream_t st, int *n)
-{
-    if constexpr (sizeof(T) == 2 && kTerms<T> == 1) {
-        cudaError_t e;
-        if (width && la_tma_walk(a, width, STATE_ONLY, st, n, &e)) return e;
-    }
-    if (width == 64) return go_chunk<T, 64, STATE_ONLY>(a, st, n);
-    if constexpr (sizeof(T) == 2 && kTerms<T> == 1)
-        if (width == 128) return go_chunk<T, 128, STATE_ONLY>(a, st, n);
-    int dk = 0;
-    for (int i = 0; i < a.nwalk; ++i) dk = a.w[i].dk > dk ? a.w[i].dk : dk;
-    if (dk <= 64) return go_token<T, 8, STATE_ONLY>(a, st, n);
-    if (dk <= 128) return go_token<T, 16, STATE_ONLY>(a, st, n);
-    return go_token<T, 32, STATE_ONLY>(a, st, n);
-}
-
-template <typename T>
-cudaError_t go(const LaArgs &a, int width, cudaStream_t st, int *n)
-{
-    cudaError_t e = cudaSuccess;
-    if (a.nseg > 1) {
-        e = go_walk<T, true>(a, width, st, n);
-        if (e != cudaSuccess) return e;
-        const int sz = a.w[0].dk * a.w[0].dv;
-        e = timed_launch(st, n, [&] { la_join_kernel<<<dim3(a.B * a.H, (sz + 255) / 256, a.nwalk), 256, 0, st>>>(a); });
-        if (e != cudaSuccess) return e;
-    }
-    return go_walk<T, false>(a, width, st, n);
+    if (tma) return launch_la_tma(a, STATE_ONLY, st, n);
+    if (dtype == SEMICRF_F32) return go_chunk<float, STATE_ONLY>(a, st, n);
+    if (dtype == SEMICRF_BF16) return go_chunk<__nv_bfloat16, STATE_ONLY>(a, st, n);
+    return go_chunk<__half, STATE_ONLY>(a, st, n);
 }
 
 template <typename T, int VEC>
@@ -880,42 +677,85 @@ cudaError_t step_type(const LaStepArgs &a, cudaStream_t st, int *n)
 
 }  // namespace
 
-// Segments of each sequence, which walk side by side: a split walk first forms what each
+namespace {
+
+// How a call is walked: by the copy engine's kernel in one tile of 64 or 128, or in tiles of
+// 64; and its segments, which walk side by side.  A split walk first forms what each
 // segment adds to the state (K and V read twice), so it pays where the sequences and
 // heads leave most of the GPU idle.  Blocks that share an SM (two at width 64 in bf16)
 // take 4.6 us a chunk and 1.8 us for the state alone, one by itself 3.2 us: three
 // segments are the fewest that gain (100 000 positions of 8 heads: 151 us in 36 segments,
 // 209 us in 18; 4000 positions of 128 heads: 115 us in two, 102 us in one).  One block an
 // SM elsewhere (4.6 and 3.0 us a chunk at width 128): two gain.
-int la_segments(int B, int T, int H, int dk, int dv, int dtype, int nwalk, int *seg_len)
+struct LaPlan {
+    int width, slices, kblocks, nseg, seg_len;
+    size_t seg_bytes, part_bytes;   // of one walk
+};
+
+LaPlan la_plan(int B, int T, int H, int dk, int dv, int dtype, int nwalk, bool tma)
 {
-    const int width = la_width(dk, dv, dtype);
-    const bool shared = width == 0 || (width == 64 && dtype == SEMICRF_BF16);
-    const long long rows = (long long)B * H * nwalk * (width ? 1 : (dv + 31) / 32);
+    const int most = dk > dv ? dk : dv;   // (the backward's walks exchange the two)
+    LaPlan p;
+    p.width = tma && most > 64 ? 128 : 64;
+    p.slices = ((nwalk > 1 ? most : dv) + p.width - 1) / p.width;
+    p.kblocks = ((nwalk > 1 ? most : dk) + p.width - 1) / p.width;
+    const bool shared = p.width == 64 && dtype == SEMICRF_BF16;
+    const long long rows = (long long)B * H * nwalk * p.slices;
     long long n = (shared ? 2LL : 1LL) * device_sm_count() / rows;
     if (n > T / 512) n = T / 512;
-    if (n < (shared ? 3 : 2)) {
-        *seg_len = (T + kChunk - 1) / kChunk * kChunk;
-        return 1;
-    }
-    long long len = (T + n - 1) / n;
-    len = (len + kChunk - 1) / kChunk * kChunk;
-    *seg_len = (int)len;
-    return (int)((T + len - 1) / len);
+    if (n < (shared ? 3 : 2)) n = 1;
+    const long long len = ((T + n - 1) / n + kChunk - 1) / kChunk * kChunk;
+    p.seg_len = (int)len;
+    p.nseg = (int)((T + len - 1) / len);
+    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    p.seg_bytes = p.nseg > 1 ? up((size_t)B * H * p.slices * p.nseg * p.width * p.width * sizeof(float)) : 0;
+    p.part_bytes = p.kblocks > 1 && dtype != SEMICRF_F32 ? up((size_t)B * T * H * (nwalk > 1 ? most : dv) * sizeof(float)) : 0;
+    return p;
 }
 
-cudaError_t launch_la(const LaArgs &a, int dtype, cudaStream_t st, int *launches)
+}  // namespace
+
+size_t la_workspace(int B, int T, int H, int dk, int dv, int dtype, int nwalk)
 {
-    int d = 0;
-    for (int i = 0; i < a.nwalk; ++i) {
-        d = a.w[i].dk > d ? a.w[i].dk : d;
-        d = a.w[i].dv > d ? a.w[i].dv : d;
+    size_t most = 0;   // operands that the copy engine cannot address take the other plan: room for either
+    for (int tma = 0; tma < 2; ++tma) {
+        if (tma && (dtype != SEMICRF_BF16 || dk > 128 || dv > 128)) continue;
+        const LaPlan p = la_plan(B, T, H, dk, dv, dtype, nwalk, tma);
+        const size_t n = nwalk * (p.seg_bytes + p.part_bytes);
+        if (n > most) most = n;
     }
-    const int width = la_width(d, d, dtype);
+    return most;
+}
+
+cudaError_t launch_la(LaArgs a, int dtype, unsigned char *ws, cudaStream_t st, int *launches)
+{
     *launches = 0;
-    if (dtype == SEMICRF_F32) return go<float>(a, width, st, launches);
-    if (dtype == SEMICRF_BF16) return go<__nv_bfloat16>(a, width, st, launches);
-    return go<__half>(a, width, st, launches);
+    const bool tma = la_tma_ok(a, dtype);
+    const LaPlan p = la_plan(a.B, a.T, a.H, a.w[0].dk, a.w[0].dv, dtype, a.nwalk, tma);
+    a.width = p.width;
+    a.slices = p.slices;
+    a.nseg = p.nseg;
+    a.seg_len = p.seg_len;
+    for (int i = 0; i < a.nwalk; ++i) {
+        a.w[i].seg = p.seg_bytes ? reinterpret_cast<float *>(ws) : nullptr;
+        ws += p.seg_bytes;
+        a.w[i].part = p.part_bytes ? reinterpret_cast<float *>(ws) : nullptr;
+        ws += p.part_bytes;
+    }
+    for (a.kblock = 0; a.kblock < p.kblocks; ++a.kblock) {
+        cudaError_t e;
+        if (a.nseg > 1) {
+            e = go_walk<true>(a, dtype, tma, st, launches);
+            if (e != cudaSuccess) return e;
+            e = timed_launch(st, launches, [&] {
+                la_join_kernel<<<dim3(a.B * a.H * a.slices, a.width * a.width / 256, a.nwalk), 256, 0, st>>>(a);
+            });
+            if (e != cudaSuccess) return e;
+        }
+        e = go_walk<false>(a, dtype, tma, st, launches);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_la_step(const LaStepArgs &a, int dtype, cudaStream_t st, int *launches)

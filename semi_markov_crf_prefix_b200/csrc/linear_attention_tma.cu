@@ -72,12 +72,12 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
     constexpr uint64_t kTileD = G::kTile >> 4, kSTileD = G::kSTile >> 4, kRow16 = 2048 >> 4;
     extern __shared__ __align__(1024) unsigned char sm[];
     const LaWalk &w = args.w[blockIdx.y];
-    const LaSpan s = la_span(args, blockIdx.x);
+    const LaSpan s = la_span(args, w, blockIdx.x);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (STATE_ONLY && s.seg == args.nseg - 1) return;
     if (!STATE_ONLY) {
-        zero_rows<T>(w, s, 0, w.dv);
-        if (s.L == 0 && s.last) copy_state(w, args, s, 0, w.dv);
+        zero_rows<T>(w, s);
+        if (s.L == 0 && s.last) copy_state(w, args, s);
     }
     if (s.pe == s.p0) return;
 
@@ -521,10 +521,9 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
         }
 
         // the state behind the last position (or behind this segment)
-        const long long bh = (long long)s.b * args.H + s.h, sz = (long long)w.dk * w.dv;
-        float *to = STATE_ONLY ? w.seg + (bh * args.nseg + s.seg) * sz : s.last && w.s_out ? w.s_out + bh * sz : nullptr;
+        float *to = STATE_ONLY ? segment_at(w, args, s) : s.last && w.s_out ? w.s_out + state_at(w, args, s) : nullptr;
         if (to) {
-            const int rs = STATE_ONLY ? w.dv : w.s_rs, cs = STATE_ONLY ? 1 : w.s_cs;
+            const int rs = STATE_ONLY ? args.width : w.s_rs, cs = STATE_ONLY ? 1 : w.s_cs;
             const float f = !STATE_ONLY && w.out_decay ? (float)decay_pow(ld, 1) : 1.f;
             auto keep = [&](int i, int j, float v) {
                 if (i < w.dk && j < w.dv) to[(long long)i * rs + (long long)j * cs] = f * v;
@@ -605,31 +604,38 @@ constexpr Kernel kernel_of{allow_smem<D, STATE_ONLY, NK>, go<D, STATE_ONLY, NK>}
 
 }  // namespace
 
-// False where the copy engine cannot address an operand (nothing is launched then).
-bool la_tma_walk(const LaArgs &a, int width, bool state_only, cudaStream_t st, int *n, cudaError_t *e)
+// Whether the copy engine can address every operand of these widths.
+bool la_tma_ok(const LaArgs &a, int dtype)
 {
-    if (!encoder()) return false;
+    if (dtype != SEMICRF_BF16 || !encoder()) return false;
+    for (int i = 0; i < a.nwalk; ++i) {
+        const LaWalk &w = a.w[i];
+        if (w.dk > 128 || w.dv > 128 || !w.q_vec || !w.k_vec || !w.v_vec || !w.o_vec) return false;
+    }
+    return true;
+}
+
+cudaError_t launch_la_tma(const LaArgs &a, bool state_only, cudaStream_t st, int *n)
+{
     bool keeps = false;   // some walk's state leaves the call
     for (int i = 0; i < a.nwalk; ++i) keeps |= a.w[i].s_out != nullptr;
-    const Kernel k = width == 64 ? (state_only ? (keeps ? kernel_of<64, true, 3> : kernel_of<64, true, 2>)
-                                               : (keeps ? kernel_of<64, false, 3> : kernel_of<64, false, 2>))
-                                 : (state_only ? (keeps ? kernel_of<128, true, 3> : kernel_of<128, true, 2>)
-                                               : (keeps ? kernel_of<128, false, 3> : kernel_of<128, false, 2>));
+    const Kernel k = a.width == 64 ? (state_only ? (keeps ? kernel_of<64, true, 3> : kernel_of<64, true, 2>)
+                                                 : (keeps ? kernel_of<64, false, 3> : kernel_of<64, false, 2>))
+                                   : (state_only ? (keeps ? kernel_of<128, true, 3> : kernel_of<128, true, 2>)
+                                                 : (keeps ? kernel_of<128, false, 3> : kernel_of<128, false, 2>));
     // (also binds the device's context to a thread that makes its first call, which the
     // driver's encoder wants: the backward pass runs in a thread of its own)
-    *e = k.allow();
-    if (*e != cudaSuccess) return true;
+    cudaError_t e = k.allow();
+    if (e != cudaSuccess) return e;
     LaMaps maps;
     for (int i = 0; i < a.nwalk; ++i) {
         const LaWalk &w = a.w[i];
-        if (!w.q_vec || !w.k_vec || !w.v_vec || !w.o_vec) return false;
         auto &m = maps.w[i];
         if (!make_map(&m.q, w.q, w.qs, w.dk, a) || !make_map(&m.k, w.k, w.ks, w.dk, a) ||
             !make_map(&m.v, w.v, w.vs, w.dv, a) || !make_map(&m.o, w.o, w.os, w.dv, a))
-            return false;
+            return cudaErrorInvalidValue;
     }
-    *e = timed_launch(st, n, [&] { k.go(a, maps, st); });
-    return true;
+    return timed_launch(st, n, [&] { k.go(a, maps, st); });
 }
 
 }  // namespace semicrf
