@@ -147,6 +147,10 @@ def linear_attention_forward(q, k, v, log_decay, lengths=None, scale=None, initi
     device, kind, shape, dv, qs, ks, vs = _attention(q, k, v, log_decay, 4)
     _extras(shape, dv, device, lengths, initial_state, "initial_state")
     d = _dims(kind, shape, dv, scale, reverse, qs, ks, vs, _dense(shape, dv))
+    return _attention_run(q, k, v, log_decay, lengths, initial_state, return_state, d, shape, dv, device, ws)
+
+
+def _attention_run(q, k, v, log_decay, lengths, initial_state, return_state, d, shape, dv, device, ws):
     ws = _workspace(ws, _attention_ws(d, shape, dv, False), device)
     B, T, H, dk = shape
     o = torch.empty((B, T, H, dv), dtype=q.dtype, device=device)
@@ -286,10 +290,14 @@ def _norm_ws(shape, dims, backward):
 def group_norm_forward(x, groups, weight=None, bias=None, lengths=None, eps=1e-5, activation="none", ws=None):
     """(y like x, stats [N,groups,2] float32: mean and 1/std of the valid positions)."""
     shape, d = _norm_dims(x, groups, weight, bias, lengths, eps, activation)
+    return _norm_forward(x, weight, bias, lengths, shape, d, ws)
+
+
+def _norm_forward(x, weight, bias, lengths, shape, d, ws=None):
     device = x.device
     ws = _workspace(ws, _norm_ws(shape, d, False), device)
     y = torch.empty_like(x)
-    stats = torch.empty((shape[0], groups, 2), dtype=torch.float32, device=device)
+    stats = torch.empty((shape[0], shape[3], 2), dtype=torch.float32, device=device)
     _call("group_norm", device, d, x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(lengths), y.data_ptr(),
           stats.data_ptr(), ws.data_ptr(), ws.numel())
     return y, stats
@@ -299,9 +307,13 @@ def group_norm_backward(dy, x, stats, groups, weight=None, bias=None, lengths=No
                         want_params=True, ws=None):
     """(dx like x, dweight [C] float32, dbias [C] float32); the last two None without want_params."""
     shape, d = _norm_dims(x, groups, weight, bias, lengths, eps, activation)
+    _want(dy, "dy", x.dtype, x.shape, x.device)
+    _want(stats, "stats", torch.float32, (shape[0], groups, 2), x.device)
+    return _norm_backward(dy, x, stats, weight, bias, lengths, shape, d, want_params, ws)
+
+
+def _norm_backward(dy, x, stats, weight, bias, lengths, shape, d, want_params, ws=None):
     device = x.device
-    _want(dy, "dy", x.dtype, x.shape, device)
-    _want(stats, "stats", torch.float32, (shape[0], groups, 2), device)
     ws = _workspace(ws, _norm_ws(shape, d, True), device)
     dx = torch.empty_like(x)
     dw, db = torch.empty((2, shape[2]), dtype=torch.float32, device=device) if want_params else (None, None)
@@ -313,21 +325,19 @@ def group_norm_backward(dy, x, stats, groups, weight=None, bias=None, lengths=No
 class GroupNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, groups, lengths, eps, activation):
-        y, stats = group_norm_forward(x, groups, weight, bias, lengths, eps, activation)
+        ctx.shape, ctx.dims = _norm_dims(x, groups, weight, bias, lengths, eps, activation)
+        y, stats = _norm_forward(x, weight, bias, lengths, ctx.shape, ctx.dims)
         ctx.save_for_backward(x, weight, bias, lengths, stats)
-        ctx.how = (groups, eps, activation)
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, weight, bias, lengths, stats = ctx.saved_tensors
-        groups, eps, activation = ctx.how
-        want = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
-        dx, dw, db = group_norm_backward(dy.contiguous(), x, stats, groups, weight, bias, lengths, eps, activation,
-                                         want)
-        return (dx, dw.to(weight.dtype) if ctx.needs_input_grad[1] else None,
-                db.to(bias.dtype) if ctx.needs_input_grad[2] else None, None, None, None, None)
+        _, want_w, want_b = ctx.needs_input_grad[:3]
+        dx, dw, db = _norm_backward(dy.contiguous(), x, stats, weight, bias, lengths, ctx.shape, ctx.dims, want_w or want_b)
+        return (dx, dw.to(weight.dtype) if want_w else None, db.to(bias.dtype) if want_b else None, None, None, None,
+                None)
 
 
 def group_norm(x, groups, weight=None, bias=None, lengths=None, eps=1e-5, activation="none"):

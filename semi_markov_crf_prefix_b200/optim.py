@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import itertools
 
 import torch
 
@@ -44,27 +45,33 @@ def _same_length(lists):
             raise ValueError(f"{n} params, but {len(ts)} of {name}")
 
 
-def _check(ts, name, like, dtypes, device, scales=False):
-    for t, p in zip(ts, like):
+def _check(ts, name, sizes, dtypes, device):
+    """Types, sizes, device and layout of a list's tensors; one pass where all is well."""
+    for t, n in zip(ts, sizes):
+        if t.dtype in dtypes and t.numel() == n and t.device == device and t.is_contiguous():
+            continue
         if t.dtype not in dtypes:
             raise TypeError(f"{name} has type {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-        if t.numel() != (-(-p.numel() // BLOCK) if scales else p.numel()):
-            raise ValueError(f"{name} of a tensor of shape {tuple(p.shape)} has shape {tuple(t.shape)}")
+        if t.numel() != n:
+            raise ValueError(f"{name} has a tensor of {t.numel()} values, expected {n}")
         if t.device != device:
             raise ValueError(f"{name} is on {t.device}, expected {device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _table(params, grads, m, v, ms, vs):
+def _pointers(ts, n):
+    return [0] * n if ts is None else [t.data_ptr() for t in ts]
+
+
+def _table(params, grads, m, v, ms, vs, sizes):
     """The library's array of semicrf_adamw_tensor, one of eight 64-bit words each."""
-    words = array.array("q")
-    for i, p in enumerate(params):
-        g = grads[i] if grads is not None else None
-        words.extend((p.data_ptr(), g.data_ptr() if g is not None else 0, m[i].data_ptr() if m else 0,
-                      v[i].data_ptr() if v else 0, ms[i].data_ptr() if ms else 0, vs[i].data_ptr() if vs else 0,
-                      p.numel(), _TYPES[p.dtype] | (_TYPES[g.dtype] << 32 if g is not None else 0)))
-    return words
+    n = len(params)
+    kinds = [_TYPES[p.dtype] for p in params]
+    if grads is not None:
+        kinds = [k | _TYPES[g.dtype] << 32 for k, g in zip(kinds, grads)]
+    rows = zip(_pointers(params, n), _pointers(grads, n), _pointers(m, n), _pointers(v, n), _pointers(ms, n),
+               _pointers(vs, n), sizes, kinds)
+    return array.array("q", [word for row in rows for word in row])
 
 
 def _scalar(x, name, dtype, device):
@@ -94,16 +101,18 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     if not params[0].is_cuda:
         raise TypeError("params must be CUDA tensors")
     kind = (torch.uint8,) if eight else (torch.float32,)
-    _check(params, "params", params, (torch.float32, torch.bfloat16, torch.float16), device)
-    _check(grads, "grads", params, tuple(_TYPES), device)
+    sizes = [p.numel() for p in params]
+    _check(params, "params", sizes, (torch.float32, torch.bfloat16, torch.float16), device)
+    _check(grads, "grads", sizes, tuple(_TYPES), device)
     for p, g in zip(params, grads):
         if g.shape != p.shape:
             raise ValueError(f"a gradient of shape {tuple(g.shape)} for a tensor of shape {tuple(p.shape)}")
-    _check(exp_avg, "exp_avg", params, kind, device)
-    _check(exp_avg_sq, "exp_avg_sq", params, kind, device)
+    _check(exp_avg, "exp_avg", sizes, kind, device)
+    _check(exp_avg_sq, "exp_avg_sq", sizes, kind, device)
     if eight:
-        _check(exp_avg_scale, "exp_avg_scale", params, (torch.float32,), device, scales=True)
-        _check(exp_avg_sq_scale, "exp_avg_sq_scale", params, (torch.float32,), device, scales=True)
+        blocks = [-(-n // BLOCK) for n in sizes]
+        _check(exp_avg_scale, "exp_avg_scale", blocks, (torch.float32,), device)
+        _check(exp_avg_sq_scale, "exp_avg_sq_scale", blocks, (torch.float32,), device)
     c = _lib.AdamWConfig(0.0, betas[0], betas[1], eps, weight_decay, grad_scale, 0)
     if isinstance(step, torch.Tensor):
         c.step_ptr = _scalar(step, "step", torch.int64, device)
@@ -113,8 +122,8 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
         c.lr_ptr = _scalar(lr, "lr", torch.float32, device)
     else:
         c.lr = lr
-    words = _table(params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale)
-    full = [p for p, n in zip(words[0::8], words[6::8]) if n]
+    words = _table(params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, sizes)
+    full = [p for p, n in zip(words[0::8], sizes) if n]
     if len(set(full)) != len(full):
         raise ValueError("the same tensor is given twice")
     _call("adamw", device, words.buffer_info()[0], len(params), ctypes.byref(c))
@@ -131,11 +140,15 @@ def adamw_state_values(codes, scales, which):
     device = codes[0].device
     if not codes[0].is_cuda:
         raise TypeError("codes must be CUDA tensors")
-    _check(codes, "codes", codes, (torch.uint8,), device)
-    _check(scales, "scales", codes, (torch.float32,), device, scales=True)
-    out = [torch.empty(c.shape, dtype=torch.float32, device=device) for c in codes]
+    sizes = [c.numel() for c in codes]
+    _check(codes, "codes", sizes, (torch.uint8,), device)
+    _check(scales, "scales", [-(-n // BLOCK) for n in sizes], (torch.float32,), device)
+    # one allocation, each tensor at a multiple of 256 bytes
+    starts = list(itertools.accumulate((-(-n // 64) * 64 for n in sizes), initial=0))
+    flat = torch.empty(starts[-1], dtype=torch.float32, device=device)
+    out = [flat.as_strided(c.shape, c.stride(), at) for c, at in zip(codes, starts)]
     second = which == "exp_avg_sq"
     words = _table(out, None, None if second else codes, codes if second else None, None if second else scales,
-                   scales if second else None)
+                   scales if second else None, sizes)
     _call("adamw_state_values", device, words.buffer_info()[0], len(out), int(second))
     return out
