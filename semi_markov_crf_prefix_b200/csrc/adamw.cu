@@ -8,8 +8,13 @@
 // bits (bias 15), v: 5 exponent bits (bias 31), so that v keeps the square of m's range;
 // a v that is not zero never gets code 0, which would make the next step's quotient huge.
 // The moments are formed in float64: a value next to the border of two codes then falls
-// on the side the formula says, and 3 conversions and 7 float64 operations a value stay
-// below the time of its 16 bytes.
+// on the side the formula says.
+//
+// Measured on 26 million parameters.  float32 states: 90 us, which is 591 MB at the
+// measured copy rate, so what is left is the memory's.  8 bits: 143 us for 420 MB (64 us):
+// bound by issue, about 110 instructions a value, of which 12 are float64 and 30 find the
+// two codes; square root and quotient to two units of the last place instead of correctly
+// rounded, powers of beta on the host and bit patterns for decoding took it from 178.
 #include <math.h>
 
 #include "device_util.cuh"

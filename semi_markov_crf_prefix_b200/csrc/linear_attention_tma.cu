@@ -15,6 +15,12 @@
 // they round towards zero, which the state, float32 in registers (tensor memory at
 // width 128), must not.
 //
+// Measured: 512 sequences and heads of 1024 positions at width 64 (268 MB, 41 us at the copy
+// rate) 77 us; of 128 x 4000, which fill the SMs once, 100 us, the time of one block's 32
+// chunks in a row (3.1 us each).  Bounds, of some 4200 cycles a chunk and SM: shared
+// memory's traffic about 2600 (matrix operands 1400, K~ 400, tiles in and out 500, the
+// state 130), the matrix unit 1500 (`sm__pipe_tensor_cycles_active` 40 %), memory 2750.
+//
 // A walk against time takes a chunk's rows in memory order too: row r is position
 // 127 - r of the chunk, and the tables of decays are mirrored.
 #include <cuda.h>
