@@ -127,6 +127,8 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     if len(set(full)) != len(full):
         raise ValueError("the same tensor is given twice")
     _call("adamw", device, words.buffer_info()[0], len(params), ctypes.byref(c))
+    # autograd refuses a graph that saved what was just overwritten
+    torch.autograd.graph.increment_version([*params, *exp_avg, *exp_avg_sq])
 
 
 @torch.no_grad()

@@ -191,6 +191,15 @@ def test_many_tensors_and_odd_places(bits):
     assert close(torch.cat(p), ep, move, torch.float32, flat.double())
 
 
+def test_overwritten_parameters_are_noticed():
+    w = torch.randn(8, device="cuda", requires_grad=True)
+    y = (w * w).sum()
+    m, v, _, _ = sc.new_adamw_state([w])
+    sc.adamw_step([w], [torch.ones(8, device="cuda")], m, v, 1)
+    with pytest.raises(RuntimeError):
+        y.backward()
+
+
 def test_refusals():
     p, g = make([(8, 4), (5,)], KINDS[:1])
     m, v, _, _ = sc.new_adamw_state(p)
