@@ -274,7 +274,8 @@ semicrf_status semicrf_nll_backward(const semicrf_dims *dims, const double *S, c
  * and errors as above: caller-owned device memory, asynchronous, arguments checked
  * on the host before any launch.  Device findings (a length outside its range) go
  * to the status word at the start of the call's workspace; such a length is taken
- * as the nearest one in range.
+ * as the nearest one in range.  A workspace serves one call at a time: calls that
+ * may overlap on the GPU (two streams, two graphs) need one each.
  */
 
 /* Element types. */

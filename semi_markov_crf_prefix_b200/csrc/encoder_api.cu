@@ -47,13 +47,15 @@ size_t attention_ws(const semicrf_attention_dims &d, bool backward)
     return kStatusBytes + la_workspace(d.B, d.T, d.H, d.dk, d.dv, d.dtype, backward ? 3 : 1);
 }
 
-// Pieces of 8 values can be moved in 16-byte accesses: width, strides and address allow it.
-int vectors(const void *p, const long long (&st)[3], int width, int dtype)
+// Pieces of 8 values can be moved in 16-byte accesses: width, address and the strides of
+// axes longer than one allow it.
+int vectors(const void *p, const long long (&st)[3], const LaArgs &a, int width, int dtype)
 {
     const size_t size = type_size(dtype);
+    const int length[3] = {a.B, a.T, a.H};
     if (width % 8 || reinterpret_cast<uintptr_t>(p) % 16) return 0;
     for (int i = 0; i < 3; ++i)
-        if (st[i] * size % 16) return 0;
+        if (length[i] > 1 && st[i] * size % 16) return 0;
     return 1;
 }
 
@@ -84,12 +86,12 @@ LaArgs attention_args(const semicrf_attention_dims &d, const float *log_decay, c
     return a;
 }
 
-void finish_walk(LaWalk &w, int dtype)
+void finish_walk(LaWalk &w, const LaArgs &a, int dtype)
 {
-    w.q_vec = vectors(w.q, w.qs, w.dk, dtype);
-    w.k_vec = vectors(w.k, w.ks, w.dk, dtype);
-    w.v_vec = vectors(w.v, w.vs, w.dv, dtype);
-    w.o_vec = vectors(w.o, w.os, w.dv, dtype);
+    w.q_vec = vectors(w.q, w.qs, a, w.dk, dtype);
+    w.k_vec = vectors(w.k, w.ks, a, w.dk, dtype);
+    w.v_vec = vectors(w.v, w.vs, a, w.dv, dtype);
+    w.o_vec = vectors(w.o, w.os, a, w.dv, dtype);
 }
 
 semicrf_status norm_ok(const semicrf_norm_dims *d)
@@ -165,7 +167,7 @@ semicrf_status semicrf_linear_attention(const semicrf_attention_dims *dims, cons
     w.c = 1.f;
     w.reverse = d.reverse;
     w.lead = 1;
-    finish_walk(w, d.dtype);
+    finish_walk(w, a, d.dtype);
     int n = 0;
     cudaError_t e = launch_la(a, d.dtype, static_cast<unsigned char *>(ws) + kStatusBytes, static_cast<cudaStream_t>(stream), &n);
     return ended(e, n);
@@ -244,7 +246,7 @@ semicrf_status semicrf_linear_attention_backward(const semicrf_attention_dims *d
     z.c = d.scale;
     z.reverse = !d.reverse;
     z.lead = 0;
-    for (LaWalk &w : a.w) finish_walk(w, d.dtype);
+    for (LaWalk &w : a.w) finish_walk(w, a, d.dtype);
     int n = 0;
     cudaError_t e = launch_la(a, d.dtype, static_cast<unsigned char *>(ws) + kStatusBytes, static_cast<cudaStream_t>(stream), &n);
     return ended(e, n);

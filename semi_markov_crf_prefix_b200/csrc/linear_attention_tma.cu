@@ -127,7 +127,9 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
         // all of these in a branch of one lane, which is elected anew each time: a flag of the
         // election kept in a variable made each instruction 60 to 180 cycles long
         auto await = [&](uint32_t bar, uint32_t parity) { alive = mbar_wait_bounded(bar, parity) && alive; };
+        int fetched[3] = {0, 0, 0};   // tiles of Q, K, V asked for
         auto fetch = [&](const CUtensorMap &m, int tile, uint32_t bar, int n) {
+            ++fetched[(bar - bars) / 8];
             mbar_expect(bar, G::kTile);
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
@@ -148,9 +150,11 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
             mma_commit(done_qk);
         };
         // the warp whole again, then all warps: false once a wait has run out
+        bool broken = false;
         auto meet = [&] {
             __syncwarp();
-            return !__syncthreads_or(!alive);
+            broken = __syncthreads_or(!alive);
+            return !broken;
         };
         if (whole > 0 && elect_lane()) {
             if (!STATE_ONLY) fetch(map.q, G::kQ, full_q, 0);
@@ -242,6 +246,11 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
         if (elect_lane()) {
             tma_store_done();
             if (!alive) set_status(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
+            if (broken) {   // somebody's wait has run out: the copies under way end before the block does
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    if (fetched[i]) mbar_wait_bounded(bars + 8 * i, (fetched[i] - 1) & 1);
+            }
         }
         __syncwarp();
     } else {
@@ -579,7 +588,9 @@ Encode encoder()
 bool make_map(CUtensorMap *m, const void *p, const long long (&st)[3], int d, const LaArgs &a)
 {
     const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)a.H, (cuuint64_t)a.T, (cuuint64_t)a.B};
-    const cuuint64_t strides[3] = {(cuuint64_t)st[2] * 2, (cuuint64_t)st[1] * 2, (cuuint64_t)st[0] * 2};
+    // (an axis of length one may have any stride; the map wants one it could use)
+    auto bytes = [](long long stride, int length) { return length > 1 ? (cuuint64_t)stride * 2 : (cuuint64_t)256; };
+    const cuuint64_t strides[3] = {bytes(st[2], a.H), bytes(st[1], a.T), bytes(st[0], a.B)};
     const cuuint32_t box[4] = {64, 1, kChunk, 1}, step[4] = {1, 1, 1, 1};
     return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, step,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -610,13 +621,17 @@ constexpr Kernel kernel_of{allow_smem<D, STATE_ONLY, NK>, go<D, STATE_ONLY, NK>}
 
 }  // namespace
 
-// Whether the copy engine can address every operand of these widths.
+// Whether the copy engine can address every operand of these widths: aligned, and no axis
+// repeated by a stride of 0 (an expanded tensor's).
 bool la_tma_ok(const LaArgs &a, int dtype)
 {
     if (dtype != SEMICRF_BF16 || !encoder()) return false;
     for (int i = 0; i < a.nwalk; ++i) {
         const LaWalk &w = a.w[i];
         if (w.dk > 128 || w.dv > 128 || !w.q_vec || !w.k_vec || !w.v_vec || !w.o_vec) return false;
+        const int length[3] = {a.B, a.T, a.H};
+        for (int j = 0; j < 3; ++j)
+            if (length[j] > 1 && (w.qs[j] == 0 || w.ks[j] == 0 || w.vs[j] == 0)) return false;
     }
     return true;
 }

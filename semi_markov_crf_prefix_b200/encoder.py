@@ -241,6 +241,7 @@ def linear_attention_step(q, k, v, log_decay, state, scale=None):
                                  0, ks[1], vs[0], 0, vs[1], H * dv, 0, dv)
     _call("linear_attention_step", device, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
           state.data_ptr(), o.data_ptr())
+    torch.autograd.graph.increment_version(state)   # autograd refuses a graph that saved it
     return o
 
 

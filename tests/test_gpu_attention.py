@@ -242,6 +242,46 @@ def test_gradient_of_a_sum_and_of_the_state_alone():
     assert torch.autograd.grad(o.float().sum(), leaves[0])[0].shape == q.shape
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_shared_heads_by_expanding(dtype):
+    # one key and value head for all query heads, one query for all sequences: strides of 0
+    q, k, v, ld, _ = inputs(2, 200, 3, 64, 64, dtype)
+    one_q, one_k, one_v = (x.detach().clone().requires_grad_(True) for x in (q[:1], k[:, :, :1], v[:, :, :1]))
+    full = [x.detach().expand(2, 200, 3, 64).contiguous().requires_grad_(True) for x in (one_q, one_k, one_v)]
+    do = torch.randn(2, 200, 3, 64, device="cuda").to(dtype)
+    o = sc.linear_attention(one_q.expand(2, -1, 3, -1), one_k.expand(-1, -1, 3, -1), one_v.expand(-1, -1, 3, -1), ld)
+    w = sc.linear_attention(*full, ld)
+    # (two kernels may serve the two, each right to its tolerance)
+    M, _ = definition(*[x.detach().double().abs() for x in full], ld, None, 0.125, None, False)
+    assert torch.all((o.double() - w.double()).abs() <= 2 * tol(w.double(), M, dtype))
+    got = torch.autograd.grad(o, (one_q, one_k, one_v), do)
+    want = torch.autograd.grad(w, full, do)
+    a = [x.detach().double().abs().requires_grad_(True) for x in full]
+    mo, _ = definition(*a, ld, None, 0.125, None, False)
+    bound = torch.autograd.grad(mo, a, do.double().abs())
+    for g, h, m, axis in zip(got, want, bound, (0, 2, 2)):
+        lim = 2 * tol(h.double(), m, dtype).sum(axis, keepdim=True)      # autograd adds the heads' shares in dtype
+        lim = lim + 4 * half_step(dtype) * h.double().abs().sum(axis, keepdim=True)
+        assert torch.all((g.double() - h.double().sum(axis, keepdim=True)).abs() <= lim)
+
+
+def test_overwritten_state_is_noticed():
+    q, k, v, ld, s0 = inputs(1, 3, 1, 16, 16, torch.float32, state=True)
+    s0.requires_grad_(True)
+    held = s0 * 1.0
+    o = sc.linear_attention(q, k, v, ld, initial_state=held)
+    sc.linear_attention_step(q[:, 0], k[:, 0], v[:, 0], ld, held.detach())
+    with pytest.raises(RuntimeError):
+        o.sum().backward()
+
+
+def test_axes_of_length_one():
+    # their strides say nothing
+    q, k, v, ld, _ = inputs(1, 150, 1, 64, 64, torch.bfloat16)
+    odd = [x.as_strided(x.shape, (7, 64, 3, 1)) for x in (q, k, v)]
+    assert torch.equal(sc.linear_attention(*odd, ld), sc.linear_attention(q, k, v, ld))
+
+
 def test_same_call_same_bits():
     for dtype, d in ((torch.bfloat16, 64), (torch.bfloat16, 128), (torch.float32, 64), (torch.float32, 80)):
         q, k, v, ld, s0 = inputs(2, 1500, 2, d, d, dtype, state=True)
