@@ -67,7 +67,7 @@ struct TmaCfg {
 // NK: terms of K~.  Three (24 bits) where a float32 state leaves the call; two leave 2^-17,
 // which 16-bit outputs do not show, and cost a third less of the shared memory's traffic,
 // the first bound of this kernel (2.9 of 4.2 thousand cycles a chunk at width 64).
-template <int D, bool STATE_ONLY, int NK>
+template <int D, int NK>
 __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(const __grid_constant__ LaArgs args,
                                                                                 const __grid_constant__ LaMaps maps)
 {
@@ -80,11 +80,8 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
     const LaWalk &w = args.w[blockIdx.y];
     const LaSpan s = la_span(args, w, blockIdx.x);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    if (STATE_ONLY && s.seg == args.nseg - 1) return;
-    if (!STATE_ONLY) {
-        zero_rows<T>(w, s);
-        if (s.L == 0 && s.last) copy_state(w, args, s);
-    }
+    zero_rows<T>(w, s);
+    if (s.L == 0 && s.last) copy_state(w, args, s);
     if (s.pe == s.p0) return;
 
     LaTables &tab = *reinterpret_cast<LaTables *>(sm + G::kTab);
@@ -157,41 +154,39 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
             return !broken;
         };
         if (whole > 0 && elect_lane()) {
-            if (!STATE_ONLY) fetch(map.q, G::kQ, full_q, 0);
+            fetch(map.q, G::kQ, full_q, 0);
             fetch(map.k, G::kK, full_k, 0);
             fetch(map.v, G::kV, full_v, 0);
-            if (!STATE_ONLY && G::kApart) scores(0);
+            if (G::kApart) scores(0);
         }
-        if (!STATE_ONLY) meet();   // the state's terms are there
+        meet();   // the state's terms are there
         for (int n = 0; n < chunks; ++n) {
             const uint32_t parity = n & 1;
             const bool next = n + 1 < whole;
-            if (!STATE_ONLY) {
-                if (n >= whole && !meet()) break;   // the shorter chunk's tiles are there
-                if (elect_lane()) {
-                    if (n >= whole || !G::kApart) scores(n);
-                    tc_after_sync();
-                    const uint32_t i2 = mma_idesc(128, nv, false, true);
-                    const uint64_t dq = desc_swz(smem + G::kQ, 16), ds = desc_swz(smem + G::kS, 16384);
+            if (n >= whole && !meet()) break;   // the shorter chunk's tiles are there
+            if (elect_lane()) {
+                if (n >= whole || !G::kApart) scores(n);
+                tc_after_sync();
+                const uint32_t i2 = mma_idesc(128, nv, false, true);
+                const uint64_t dq = desc_swz(smem + G::kQ, 16), ds = desc_swz(smem + G::kS, 16384);
 #pragma unroll(kUnroll)
-                    for (int i = 0; i < 2 * kd; ++i) {   // the state's second term first
-                        const int k = i < kd ? i : i - kd;
-                        const uint64_t at = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                        mma_ss(tm + G::kO, dq + at, ds + (i < kd ? kSTileD : 0) + k * kRow16, i2, i > 0);
-                    }
-                    mma_commit(done_qs);
-                    tma_store_read();   // the last outputs have left
-                    if (NK == 2 && next) {
-                        await(done_qs, parity);
-                        fetch(map.q, G::kQ, full_q, n + 1);
-                    }
+                for (int i = 0; i < 2 * kd; ++i) {   // the state's second term first
+                    const int k = i < kd ? i : i - kd;
+                    const uint64_t at = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                    mma_ss(tm + G::kO, dq + at, ds + (i < kd ? kSTileD : 0) + k * kRow16, i2, i > 0);
                 }
-                if (NK == 3) {
-                    if (!meet()) break;   // K~'s third term may be written
-                    if (next && elect_lane()) {
-                        await(done_qs, parity);
-                        fetch(map.q, G::kQ, full_q, n + 1);
-                    }
+                mma_commit(done_qs);
+                tma_store_read();   // the last outputs have left
+                if (NK == 2 && next) {
+                    await(done_qs, parity);
+                    fetch(map.q, G::kQ, full_q, n + 1);
+                }
+            }
+            if (NK == 3) {
+                if (!meet()) break;   // K~'s third term may be written
+                if (next && elect_lane()) {
+                    await(done_qs, parity);
+                    fetch(map.q, G::kQ, full_q, n + 1);
                 }
             }
             if (!meet()) break;   // K~ is there
@@ -207,13 +202,7 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
                     for (int k = 0; k < kChunk / 16; ++k)
                         mma_ss(tm + G::kKV, dk + x * kTileD + k * kRow16, dv + k * kRow16, i4, x < NK - 1 || k > 0);
                 mma_commit(done_kv);
-                if (STATE_ONLY && next) {
-                    await(done_kv, parity);
-                    if (!G::kApart) fetch(map.k, G::kK, full_k, n + 1);
-                    fetch(map.v, G::kV, full_v, n + 1);
-                }
             }
-            if (STATE_ONLY) continue;
             if (!meet()) break;   // P is there, o scaled
             if (elect_lane()) {
                 tc_after_sync();
@@ -305,7 +294,7 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
             }
         };
         {
-            const StateAt from = STATE_ONLY ? StateAt{nullptr, 0, 0} : state_from(w, args, s);
+            const StateAt from = state_from(w, args, s);
             auto given = [&](int i, int j) {
                 return from.p && i < w.dk && j < w.dv ? from.p[(long long)i * from.rs + (long long)j * from.cs] : 0.f;
             };
@@ -316,21 +305,19 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
 #pragma unroll
                     for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(given(row, c + e));
                     tmem_st16(tlane + G::kState + c, r);
-                    if (!STATE_ONLY) put_row(c, r);
+                    put_row(c, r);
                 }
                 tmem_wait_st();
             } else {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     S[i] = given(quad * 16 + (lane >> 2) + (i & 2) * 4, c0 + (i >> 2) * 8 + (lane & 3) * 2 + (i & 1));
-                if (!STATE_ONLY) put_pairs();
+                put_pairs();
             }
         }
 
-        if (!STATE_ONLY) {
-            smem_to_mma();
-            __syncthreads_or(!alive);
-        }
+        smem_to_mma();
+        __syncthreads_or(!alive);
         for (int n = 0; n < chunks; ++n) {
             const uint32_t parity = n & 1;
             const int cnt = min(kChunk, s.pe - s.p0 - n * kChunk);
@@ -347,17 +334,17 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
                         *reinterpret_cast<uint4 *>(sm + tile + at0 + i * G::kRows * 128) = v;
                     }
                 };
-                if (!STATE_ONLY) bring(w.q, w.qs, w.dk, G::kQ);
+                bring(w.q, w.qs, w.dk, G::kQ);
                 bring(w.k, w.ks, w.dk, G::kK);
                 bring(w.v, w.vs, w.dv, G::kV);
             }
-            if (!STATE_ONLY && !is_whole) {
+            if (!is_whole) {
                 smem_to_mma();
                 if (__syncthreads_or(!alive)) break;
             }
             const int lead = s.p0 + n == 0 ? w.lead : 1;
             if (is_whole) await(full_k, parity);
-            if (!G::kApart && !STATE_ONLY) await(done_qk, parity);   // K~ replaces K
+            if (!G::kApart) await(done_qk, parity);   // K~ replaces K
             uint4 third[NK == 3 ? NP : 1];   // K~'s third term, whose tile the last outputs may still be leaving
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
@@ -380,13 +367,13 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
 #pragma unroll
                 for (int x = 0; x < NK; ++x) {
                     const uint4 v = make_uint4(o[x][0], o[x][1], o[x][2], o[x][3]);
-                    if (x == 2 && !STATE_ONLY)
+                    if (x == 2)
                         third[NK == 3 ? i : 0] = v;
                     else
                         *reinterpret_cast<uint4 *>(sm + G::kKt + x * G::kTile + at0 + i * G::kRows * 128) = v;
                 }
             }
-            if (NK == 3 && !STATE_ONLY) {
+            if (NK == 3) {
                 if (__syncthreads_or(!alive)) break;
 #pragma unroll
                 for (int i = 0; i < NP; ++i)
@@ -395,65 +382,63 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
             smem_to_mma();
             if (__syncthreads_or(!alive)) break;
 
-            if (!STATE_ONLY) {
-                if (G::kApart) await(done_qk, parity);
-                tc_after_sync();
-                // scores -> P: 32 columns at a time, 16 scores becoming 8 columns of each term
+            if (G::kApart) await(done_qk, parity);
+            tc_after_sync();
+            // scores -> P: 32 columns at a time, 16 scores becoming 8 columns of each term
 #pragma unroll 1
-                for (int c = half * 64; c < half * 64 + 64; c += 32) {
-                    const int away = rev ? c / 32 - quad : quad - c / 32;
-                    uint32_t r[32];
-                    if (away >= 0) {
-                        tmem_ld32(tlane + c, r);
-                        tmem_wait_ld();
-                    }
-                    if (away > 0) {
-                        const float g = beside * tab.block[away - 1];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * (g * tab.side[e]));
-                    } else if (away == 0) {
-                        const float *f = tab.diag + 31 + lane;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f[-e]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) r[e] = 0;
-                    }
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        uint32_t o[NM][8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            uint32_t t[NM];
-                            split2<NM>(__uint_as_float(r[16 * g + 2 * e]), __uint_as_float(r[16 * g + 2 * e + 1]), t);
-#pragma unroll
-                            for (int x = 0; x < NM; ++x) o[x][e] = t[x];
-                        }
-#pragma unroll
-                        for (int x = 0; x < NM; ++x) tmem_st8(tlane + (c / 16 + g) * (8 * NM) + x * 8, o[x]);
-                    }
-                }
-                // o starts as b lam^{i+1} q S
-                await(done_qs, parity);
-                tc_after_sync();
-                const float f = lead ? ofull : w.b * (float)decay_pow(ld, rev ? kChunk - 1 - row : row);
-#pragma unroll 1
-                for (int c = 0; c < D / 2; c += 32) {
-                    uint32_t r[2][16];
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) tmem_ld16(tlane + G::kO + c0 + c + 16 * g, r[g]);
+            for (int c = half * 64; c < half * 64 + 64; c += 32) {
+                const int away = rev ? c / 32 - quad : quad - c / 32;
+                uint32_t r[32];
+                if (away >= 0) {
+                    tmem_ld32(tlane + c, r);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) r[g][e] = __float_as_uint(__uint_as_float(r[g][e]) * f);
-                        tmem_st16(tlane + G::kO + c0 + c + 16 * g, r[g]);
-                    }
                 }
-                tmem_wait_st();
-                tc_before_sync();
-                if (__syncthreads_or(!alive)) break;
+                if (away > 0) {
+                    const float g = beside * tab.block[away - 1];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * (g * tab.side[e]));
+                } else if (away == 0) {
+                    const float *f = tab.diag + 31 + lane;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f[-e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = 0;
+                }
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t o[NM][8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t t[NM];
+                        split2<NM>(__uint_as_float(r[16 * g + 2 * e]), __uint_as_float(r[16 * g + 2 * e + 1]), t);
+#pragma unroll
+                        for (int x = 0; x < NM; ++x) o[x][e] = t[x];
+                    }
+#pragma unroll
+                    for (int x = 0; x < NM; ++x) tmem_st8(tlane + (c / 16 + g) * (8 * NM) + x * 8, o[x]);
+                }
             }
+            // o starts as b lam^{i+1} q S
+            await(done_qs, parity);
+            tc_after_sync();
+            const float f = lead ? ofull : w.b * (float)decay_pow(ld, rev ? kChunk - 1 - row : row);
+#pragma unroll 1
+            for (int c = 0; c < D / 2; c += 32) {
+                uint32_t r[2][16];
+#pragma unroll
+                for (int g = 0; g < 2; ++g) tmem_ld16(tlane + G::kO + c0 + c + 16 * g, r[g]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) r[g][e] = __float_as_uint(__uint_as_float(r[g][e]) * f);
+                    tmem_st16(tlane + G::kO + c0 + c + 16 * g, r[g]);
+                }
+            }
+            tmem_wait_st();
+            tc_before_sync();
+            if (__syncthreads_or(!alive)) break;
             await(done_kv, parity);
             tc_after_sync();
             // S = lam^n S + KV; the float32 rounding of lam^n alone would bias a state that
@@ -482,7 +467,7 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
                             old[g][e] = __float_as_uint(fmaf(prev, hi, fmaf(prev, lo, __uint_as_float(r[g][e]))));
                         }
                         tmem_st16(tlane + G::kState + c + 16 * g, old[g]);
-                        if (!STATE_ONLY) put_row(c + 16 * g, old[g]);
+                        put_row(c + 16 * g, old[g]);
                     }
                 }
                 tmem_wait_st();
@@ -495,51 +480,49 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
                 // (columns from nv on are not computed: their values stay out of every result)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) S[i] = fmaf(S[i], hi, fmaf(S[i], lo, __uint_as_float(r[i])));
-                if (!STATE_ONLY) put_pairs();
+                put_pairs();
             }
-            if (!STATE_ONLY) {
-                await(done_pv, parity);
-                tc_after_sync();
+            await(done_pv, parity);
+            tc_after_sync();
 #pragma unroll 1
-                for (int c = 0; c < D / 2; c += 32) {
-                    uint32_t r[32];
-                    tmem_ld32(tlane + G::kO + c0 + c, r);
-                    tmem_wait_ld();
+            for (int c = 0; c < D / 2; c += 32) {
+                uint32_t r[32];
+                tmem_ld32(tlane + G::kO + c0 + c, r);
+                tmem_wait_ld();
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        uint32_t o[4];
+                for (int g = 0; g < 4; ++g) {
+                    uint32_t o[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[8 * g + 2 * e]),
-                                                                          __uint_as_float(r[8 * g + 2 * e + 1]));
-                            o[e] = *reinterpret_cast<const uint32_t *>(&v);
-                        }
-                        const int p = (c0 + c) / 8 + g;
-                        *reinterpret_cast<uint4 *>(sm + G::kOut + (p >> 3) * 16384 + swz(row, p & 7)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int e = 0; e < 4; ++e) {
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[8 * g + 2 * e]),
+                                                                      __uint_as_float(r[8 * g + 2 * e + 1]));
+                        o[e] = *reinterpret_cast<const uint32_t *>(&v);
                     }
+                    const int p = (c0 + c) / 8 + g;
+                    *reinterpret_cast<uint4 *>(sm + G::kOut + (p >> 3) * 16384 + swz(row, p & 7)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
                 }
-                smem_to_mma();
-                tc_before_sync();
-                if (__syncthreads_or(!alive)) break;
-                if (!is_whole && j8 * 8 < w.dv) {
-                    T *o = static_cast<T *>(w.o) + s.b * w.os[0] + s.h * w.os[2] + (long long)j8 * 8;
+            }
+            smem_to_mma();
+            tc_before_sync();
+            if (__syncthreads_or(!alive)) break;
+            if (!is_whole && j8 * 8 < w.dv) {
+                T *o = static_cast<T *>(w.o) + s.b * w.os[0] + s.h * w.os[2] + (long long)j8 * 8;
 #pragma unroll 1
-                    for (int i = 0; i < NP; ++i) {
-                        const int r = r0 + i * G::kRows, pos = rev ? kChunk - 1 - r : r;
-                        if (pos < cnt)
-                            *reinterpret_cast<uint4 *>(o + (row_of(n) + r) * w.os[1]) =
-                                *reinterpret_cast<const uint4 *>(sm + G::kOut + at0 + i * G::kRows * 128);
-                    }
+                for (int i = 0; i < NP; ++i) {
+                    const int r = r0 + i * G::kRows, pos = rev ? kChunk - 1 - r : r;
+                    if (pos < cnt)
+                        *reinterpret_cast<uint4 *>(o + (row_of(n) + r) * w.os[1]) =
+                            *reinterpret_cast<const uint4 *>(sm + G::kOut + at0 + i * G::kRows * 128);
                 }
             }
         }
 
         // the state behind the last position (or behind this segment)
-        float *to = STATE_ONLY ? segment_at(w, args, s) : s.last && w.s_out ? w.s_out + state_at(w, args, s) : nullptr;
+        float *to = s.last && w.s_out ? w.s_out + state_at(w, args, s) : nullptr;
         if (to) {
-            const int rs = STATE_ONLY ? args.width : w.s_rs, cs = STATE_ONLY ? 1 : w.s_cs;
-            const float f = !STATE_ONLY && w.out_decay ? (float)decay_pow(ld, 1) : 1.f;
+            const int rs = w.s_rs, cs = w.s_cs;
+            const float f = w.out_decay ? (float)decay_pow(ld, 1) : 1.f;
             auto keep = [&](int i, int j, float v) {
                 if (i < w.dk && j < w.dv) to[(long long)i * rs + (long long)j * cs] = f * v;
             };
@@ -556,6 +539,217 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     keep(quad * 16 + (lane >> 2) + (i & 2) * 4, c0 + (i >> 2) * 8 + (lane & 3) * 2 + (i & 1), S[i]);
+            }
+        }
+        if (!alive && tid == 0) set_status(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
+    }
+    tc_before_sync();
+    __syncthreads();
+    if (warp == 8) tmem_free(tm, G::kCols);
+}
+
+// What a whole segment adds to the state: KV of each chunk as above, S = lam^128 S + KV.
+// K~ and KV are double (K~ where two terms are enough), so that a chunk's products run
+// while the next one's keys are weighted and the last one's sums are taken up.
+// Segments that end inside the sequence's last chunk are not asked for.
+//
+// Measured: 32 walks of 40 chunks at width 128 in 90 us, 2.2 us a chunk (two terms at the
+// matrix unit 0.8), the call of 4 x 20000 positions and 8 heads 309 us; 334 with the outputs'
+// kernel less its outputs, one tile of each kind.  At width 64 two blocks share an SM and the
+// second tiles change nothing (52 us for 288 segments of 22 chunks).
+template <int D, int NK>
+struct StateCfg {
+    static constexpr int kTile = D / 64 * 16384, NB = NK == 2 ? 2 : 1;
+    static constexpr int kK = 0, kV = kK + kTile, kKt = kV + 2 * kTile, kBars = kKt + NB * NK * kTile, kSmem = kBars + 64;
+    static constexpr int kKV = 0, kState = 2 * D, kCols = D == 64 ? 128 : 512;
+    static constexpr int NP = kChunk * (D / 8) / kWorkers, kRows = kWorkers / (D / 8);
+    static constexpr int kBlocks = D == 64 ? 2 : 1;
+    static_assert(kSmem <= (kBlocks == 2 ? 113 : 227) * 1024, "shared memory");
+};
+
+template <int D, int NK>
+__global__ __launch_bounds__(kThreads, (StateCfg<D, NK>::kBlocks)) void la_state_kernel(const __grid_constant__ LaArgs args,
+                                                                                    const __grid_constant__ LaMaps maps)
+{
+    using G = StateCfg<D, NK>;
+    constexpr int NB = G::NB, NP = G::NP;
+    constexpr uint64_t kTileD = G::kTile >> 4, kRow16 = 2048 >> 4;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const LaWalk &w = args.w[blockIdx.y];
+    const LaSpan s = la_span(args, w, blockIdx.x);
+    if (s.seg == args.nseg - 1 || s.pe - s.p0 < args.seg_len) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    uint32_t *slot = reinterpret_cast<uint32_t *>(sm + G::kBars + 56);
+    const uint32_t smem = static_cast<uint32_t>(__cvta_generic_to_shared(sm)), bars = smem + G::kBars;
+    const uint32_t full_k = bars, full_v = bars + 8, done = bars + 24;   // K; V, even and odd; KV, even and odd
+    if (warp == 8) {
+        tmem_alloc(static_cast<uint32_t>(__cvta_generic_to_shared(slot)), G::kCols);
+        if (lane == 0) {
+            for (int i = 0; i < 5; ++i) mbar_init(bars + 8 * i, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+    }
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tm = __shfl_sync(0xffffffffu, *slot, 0);
+    const int nv = (w.dv + 15) / 16 * 16, chunks = args.seg_len / kChunk, rev = w.reverse;
+    const float ld = args.log_decay[s.h];
+    bool alive = true;
+
+    if (warp == 8) {
+        const auto &map = maps.w[blockIdx.y];
+        int fetched[3] = {0, 0, 0};
+        auto await = [&](uint32_t bar, uint32_t parity) { alive = mbar_wait_bounded(bar, parity) && alive; };
+        auto fetch = [&](const CUtensorMap &m, int tile, int which, int n) {
+            ++fetched[which];
+            mbar_expect(bars + 8 * which, G::kTile);
+            const int row = rev ? s.L - s.p0 - (n + 1) * kChunk : s.p0 + n * kChunk;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+                tma_load(smem + tile + c * 16384, &m, c * 64, s.h, row, s.b, bars + 8 * which);
+        };
+        if (elect_lane()) {
+            fetch(map.k, G::kK, 0, 0);
+            fetch(map.v, G::kV, 1, 0);
+            if (chunks > 1) fetch(map.v, G::kV + G::kTile, 2, 1);
+        }
+        bool broken = false;
+        for (int n = 0; n < chunks && !broken; ++n) {
+            __syncwarp();
+            broken = __syncthreads_or(!alive);   // K~ is there
+            if (!broken && elect_lane()) {
+                const int odd = n & 1;
+                if (n + 1 < chunks) fetch(map.k, G::kK, 0, n + 1);
+                await(full_v + 8 * odd, n >> 1 & 1);
+                tc_after_sync();
+                const uint32_t id = mma_idesc(D, nv, true, true);
+                const uint64_t dk = desc_swz(smem + G::kKt + (NB == 2 ? odd * NK * G::kTile : 0), 16384);
+                const uint64_t dv = desc_swz(smem + G::kV + odd * G::kTile, 16384);
+#pragma unroll
+                for (int x = NK - 1; x >= 0; --x)
+#pragma unroll(D == 128 ? 8 : 1)
+                    for (int k = 0; k < kChunk / 16; ++k)
+                        mma_ss(tm + G::kKV + odd * D, dk + x * kTileD + k * kRow16, dv + k * kRow16, id, x < NK - 1 || k > 0);
+                mma_commit(done + 8 * odd);
+                if (n > 0 && n + 1 < chunks) {   // the other tile of V is free once its products are there
+                    await(done + 8 * (odd ^ 1), (n - 1) >> 1 & 1);
+                    if (odd)
+                        fetch(map.v, G::kV, 1, n + 1);
+                    else
+                        fetch(map.v, G::kV + G::kTile, 2, n + 1);
+                }
+            }
+        }
+        if (elect_lane()) {
+            if (!alive) set_status(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
+            if (broken) {   // somebody's wait has run out: the copies under way end before the block does
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    if (fetched[i]) mbar_wait_bounded(bars + 8 * i, (fetched[i] - 1) & 1);
+            }
+        }
+        __syncwarp();
+    } else {
+        auto await = [&](uint32_t bar, uint32_t parity) {
+            alive = mbar_wait_bounded(bar, parity) && alive;
+            __syncwarp();
+        };
+        const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane, c0 = half * (D / 2);
+        const uint32_t tlane = tm + ((uint32_t)(quad * 32) << 16);
+        const int r0 = tid / (D / 8), j8 = tid % (D / 8);
+        const int at0 = (j8 >> 3) * 16384 + swz(r0, j8 & 7);
+        float wk[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int r = r0 + i * G::kRows;
+            wk[i] = (float)(w.c * decay_pow(ld, rev ? r : kChunk - 1 - r));
+        }
+        const double full = decay_pow(ld, kChunk);
+        const float whole_hi = (float)full, whole_lo = (float)(full - (double)whole_hi);
+        float S[D == 64 ? 16 : 1];
+        if constexpr (D == 64) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[i] = 0.f;
+        }
+        auto take_up = [&](int n) {   // S = lam^128 S + KV of chunk n
+            await(done + 8 * (n & 1), n >> 1 & 1);
+            tc_after_sync();
+            float hi = whole_hi, lo = whole_lo;
+            if (n == 0) hi = lo = 0.f;
+            if constexpr (D == 64) {
+                uint32_t r[16];
+                tmem_ld16x256(tlane + G::kKV + (n & 1) * D + c0, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[i] = fmaf(S[i], hi, fmaf(S[i], lo, __uint_as_float(r[i])));
+            } else {
+#pragma unroll 1
+                for (int c = c0; c < min(c0 + D / 2, nv); c += 32) {
+                    uint32_t r[32], old[2][16];
+                    tmem_ld32(tlane + G::kKV + (n & 1) * D + c, r);
+                    if (n > 0) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) tmem_ld16(tlane + G::kState + c + 16 * g, old[g]);
+                    }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float prev = n > 0 ? __uint_as_float(old[g][e]) : 0.f;
+                            old[g][e] = __float_as_uint(fmaf(prev, hi, fmaf(prev, lo, __uint_as_float(r[16 * g + e]))));
+                        }
+                        tmem_st16(tlane + G::kState + c + 16 * g, old[g]);
+                    }
+                }
+                tmem_wait_st();
+            }
+            tc_before_sync();
+        };
+        bool broken = false;
+        for (int n = 0; n < chunks && !broken; ++n) {
+            if (NB == 1 && n > 0) take_up(n - 1);   // K~'s only tiles are read
+            await(full_k, n & 1);
+            unsigned char *to = sm + G::kKt + (NB == 2 ? (n & 1) * NK * G::kTile : 0) + at0;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(sm + G::kK + at0 + i * G::kRows * 128);
+                uint32_t o[NK][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t v = reinterpret_cast<const uint32_t *>(&u)[e];
+                    uint32_t t[NK];
+                    split2<NK>(__uint_as_float(v << 16) * wk[i], __uint_as_float(v & 0xffff0000u) * wk[i], t);
+#pragma unroll
+                    for (int x = 0; x < NK; ++x) o[x][e] = t[x];
+                }
+#pragma unroll
+                for (int x = 0; x < NK; ++x)
+                    *reinterpret_cast<uint4 *>(to + x * G::kTile + i * G::kRows * 128) =
+                        make_uint4(o[x][0], o[x][1], o[x][2], o[x][3]);
+            }
+            smem_to_mma();
+            broken = __syncthreads_or(!alive);
+            if (NB == 2 && n > 0 && !broken) take_up(n - 1);
+        }
+        if (!broken) take_up(chunks - 1);
+        float *to = segment_at(w, args, s);
+        auto keep = [&](int i, int j, float v) {
+            if (i < w.dk && j < w.dv) to[i * D + j] = v;
+        };
+        if constexpr (D == 64) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                keep(quad * 16 + (lane >> 2) + (i & 2) * 4, c0 + (i >> 2) * 8 + (lane & 3) * 2 + (i & 1), S[i]);
+        } else {
+#pragma unroll 1
+            for (int c = c0; c < min(c0 + D / 2, nv); c += 16) {
+                uint32_t r[16];
+                tmem_ld16(tlane + G::kState + c, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) keep(row, c + e, __uint_as_float(r[e]));
             }
         }
         if (!alive && tid == 0) set_status(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
@@ -597,27 +791,23 @@ bool make_map(CUtensorMap *m, const void *p, const long long (&st)[3], int d, co
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool STATE_ONLY, int NK>
-cudaError_t allow_smem()
+using Kernel = void (*)(LaArgs, LaMaps);
+
+// The kernel for a width, a pass and the terms of K~, and its shared memory.
+Kernel kernel_of(int width, bool state_only, bool keeps, int *smem)
 {
-    return cudaFuncSetAttribute(la_tma_kernel<D, STATE_ONLY, NK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                TmaCfg<D>::kSmem);
+    if (state_only) {
+        if (width == 64) {
+            *smem = keeps ? StateCfg<64, 3>::kSmem : StateCfg<64, 2>::kSmem;
+            return keeps ? la_state_kernel<64, 3> : la_state_kernel<64, 2>;
+        }
+        *smem = keeps ? StateCfg<128, 3>::kSmem : StateCfg<128, 2>::kSmem;
+        return keeps ? la_state_kernel<128, 3> : la_state_kernel<128, 2>;
+    }
+    *smem = width == 64 ? TmaCfg<64>::kSmem : TmaCfg<128>::kSmem;
+    if (width == 64) return keeps ? la_tma_kernel<64, 3> : la_tma_kernel<64, 2>;
+    return keeps ? la_tma_kernel<128, 3> : la_tma_kernel<128, 2>;
 }
-
-template <int D, bool STATE_ONLY, int NK>
-void go(const LaArgs &a, const LaMaps &maps, cudaStream_t st)
-{
-    using G = TmaCfg<D>;
-    la_tma_kernel<D, STATE_ONLY, NK><<<dim3(a.B * a.H * a.nseg, a.nwalk), kThreads, G::kSmem, st>>>(a, maps);
-}
-
-struct Kernel {
-    cudaError_t (*allow)();
-    void (*go)(const LaArgs &, const LaMaps &, cudaStream_t);
-};
-
-template <int D, bool STATE_ONLY, int NK>
-constexpr Kernel kernel_of{allow_smem<D, STATE_ONLY, NK>, go<D, STATE_ONLY, NK>};
 
 }  // namespace
 
@@ -640,13 +830,11 @@ cudaError_t launch_la_tma(const LaArgs &a, bool state_only, cudaStream_t st, int
 {
     bool keeps = false;   // some walk's state leaves the call
     for (int i = 0; i < a.nwalk; ++i) keeps |= a.w[i].s_out != nullptr;
-    const Kernel k = a.width == 64 ? (state_only ? (keeps ? kernel_of<64, true, 3> : kernel_of<64, true, 2>)
-                                                 : (keeps ? kernel_of<64, false, 3> : kernel_of<64, false, 2>))
-                                   : (state_only ? (keeps ? kernel_of<128, true, 3> : kernel_of<128, true, 2>)
-                                                 : (keeps ? kernel_of<128, false, 3> : kernel_of<128, false, 2>));
+    int smem;
+    const Kernel k = kernel_of(a.width, state_only, keeps, &smem);
     // (also binds the device's context to a thread that makes its first call, which the
     // driver's encoder wants: the backward pass runs in a thread of its own)
-    cudaError_t e = k.allow();
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     LaMaps maps;
     for (int i = 0; i < a.nwalk; ++i) {
@@ -656,7 +844,7 @@ cudaError_t launch_la_tma(const LaArgs &a, bool state_only, cudaStream_t st, int
             !make_map(&m.v, w.v, w.vs, w.dv, a) || !make_map(&m.o, w.o, w.os, w.dv, a))
             return cudaErrorInvalidValue;
     }
-    return timed_launch(st, n, [&] { k.go(a, maps, st); });
+    return timed_launch(st, n, [&] { k<<<dim3(a.B * a.H * a.nseg, a.nwalk), kThreads, smem, st>>>(a, maps); });
 }
 
 }  // namespace semicrf
