@@ -11,10 +11,12 @@
 // on the side the formula says.
 //
 // Measured on 26 million parameters.  float32 states: 90 us, which is 591 MB at the
-// measured copy rate, so what is left is the memory's.  8 bits: 143 us for 420 MB (64 us):
-// bound by issue, about 110 instructions a value, of which 12 are float64 and 30 find the
-// two codes; square root and quotient to two units of the last place instead of correctly
-// rounded, powers of beta on the host and bit patterns for decoding took it from 178.
+// measured copy rate, so what is left is the memory's.  8 bits: 113 us for 420 MB (64 us):
+// bound by issue (68 % of the cycles) and by the loads' latency, about 95 instructions a
+// value, of which 14 are float64.  Square root and quotient to two units of the last place
+// instead of correctly rounded and powers of beta on the host took it from 178 to 143;
+// codes read and written as the high words of doubles 2^1008 (2^992) times too small, a
+// multiplication for a change of the bias and a case for small codes, to 125.
 #include <math.h>
 
 #include "device_util.cuh"
@@ -128,28 +130,23 @@ __device__ __forceinline__ void store8(void *p, long long i, int cnt, bool vec, 
 
 __device__ __forceinline__ bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Code of y >= 0: exponent bits over 3 mantissa bits, nearest even, from the double's
-// bits (the low word only decides ties).
+// Code of y >= 0: y 2^(BIAS - 1023), whose bits are the code's with 49 more behind it, small
+// codes included (those are a double's own small values); nearest even, the low word only
+// decides ties.
 template <int BIAS>
 __device__ __forceinline__ uint32_t code_of(double y)
 {
-    const uint32_t hi = (uint32_t)__double2hiint(y);
-    if ((int)(hi >> 20) - 1023 + BIAS < 1) return (uint32_t)__double2int_rn(y * pow2(BIAS + 2));
-    const uint32_t h = hi | (__double2loint(y) != 0);
-    return ((h + 0xffffu + ((h >> 17) & 1u)) >> 17) - ((1023u - BIAS) << 3);
+    const double x = y * pow2(BIAS - 1023);
+    const uint32_t h = (uint32_t)__double2hiint(x) | (__double2loint(x) != 0);
+    return (h + 0xffffu + ((h >> 17) & 1u)) >> 17;
 }
 
-// The value of a code, without its block's scale: its bits are those of a double (or
-// float) with another bias, but for the codes below 8, which have no leading bit.
+// The value of a code without its block's scale, the other way round: the code's bits (of a
+// sign at bit 31 and exponent and mantissa from bit 17 on) are those of a double's high word.
 template <int BIAS>
-__device__ __forceinline__ double value_of(uint32_t c, bool some_small)
+__device__ __forceinline__ double value_of(uint32_t high)
 {
-    if (some_small) {   // of this warp
-        const bool small = c < 8;
-        const double v = __hiloint2double((int)((c + (small ? 8u : 0u) + (1023u - BIAS) * 8) << 17), 0);
-        return small ? v - pow2(1 - BIAS) : v;
-    }
-    return __hiloint2double((int)((c + (1023u - BIAS) * 8) << 17), 0);
+    return __hiloint2double((int)high, 0) * pow2(1023 - BIAS);
 }
 
 template <int BIAS>
@@ -172,26 +169,40 @@ __device__ __forceinline__ float next_param(float p, float m, float v, const Fac
     return fmaf(p, f.decay, __fdividef(-f.lr * m, fmaf(root, f.root2, f.eps)));
 }
 
+__device__ __forceinline__ void store_param(const semicrf_adamw_tensor &t, long long i, int cnt, bool vec,
+                                            const float (&p)[kPer])
+{
+    if (t.param_dtype == SEMICRF_F32)
+        store8<float>(t.param, i, cnt, vec, p);
+    else if (t.param_dtype == SEMICRF_BF16)
+        store8<__nv_bfloat16>(t.param, i, cnt, vec, p);
+    else
+        store8<__half>(t.param, i, cnt, vec, p);
+}
+
 // One call of a warp: 256 consecutive values, which is one block of scales.
 __device__ __forceinline__ void step8(const semicrf_adamw_tensor &t, const semicrf_adamw_config &c, const Factors &f,
-                                      long long i, int cnt, bool vec, float (&p)[kPer])
+                                      long long i, int cnt, bool vec)
 {
+    float p[kPer];
+    load_as<float>(t.param, t.param_dtype, i, cnt, vec, p);
     double g[kPer];
     load_as<double>(t.grad, t.grad_dtype, i, cnt, vec, g);
     const int lane = threadIdx.x & 31;
     const long long blk = (i - lane * kPer) / kBlock;
     const bool any = cnt > 0;
     uint8_t *mc = static_cast<uint8_t *>(t.exp_avg) + i, *vc = static_cast<uint8_t *>(t.exp_avg_sq) + i;
-    Pack<uint8_t, 8> cm, cv;
+    uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};   // the codes, four to a word
     const bool wide = vec && reinterpret_cast<uintptr_t>(mc) % 8 == 0 && reinterpret_cast<uintptr_t>(vc) % 8 == 0;
     if (wide) {
-        cm = *reinterpret_cast<const Pack<uint8_t, 8> *>(mc);
-        cv = *reinterpret_cast<const Pack<uint8_t, 8> *>(vc);
+        const uint2 wm = *reinterpret_cast<const uint2 *>(mc), wv = *reinterpret_cast<const uint2 *>(vc);
+        cm[0] = wm.x, cm[1] = wm.y;
+        cv[0] = wv.x, cv[1] = wv.y;
     } else {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            cm.v[j] = j < cnt ? mc[j] : 0;
-            cv.v[j] = j < cnt ? vc[j] : 0;
+            cm[j / 4] |= (uint32_t)(j < cnt ? mc[j] : 0) << (j % 4 * 8);
+            cv[j / 4] |= (uint32_t)(j < cnt ? vc[j] : 0) << (j % 4 * 8);
         }
     }
     // a warp enters with its first lane inside the tensor, so the block's scale exists
@@ -199,48 +210,41 @@ __device__ __forceinline__ void step8(const semicrf_adamw_tensor &t, const semic
     const double n1 = 1.0 - c.beta1, n2 = 1.0 - c.beta2;
     double m[kPer], v[kPer];
     float mm = 0.f, mv = 0.f;
-    bool small_m = false, small_v = false;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        small_m |= (cm.v[j] & 127u) < 8;
-        small_v |= cv.v[j] < 8;
-    }
-    small_m = __any_sync(0xffffffffu, small_m);
-    small_v = __any_sync(0xffffffffu, small_v);
     const bool scaled = c.grad_scale != 1.0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const double gj = scaled ? g[j] * c.grad_scale : g[j];
-        const double mag = value_of<15>(cm.v[j] & 127u, small_m);
-        const double old = __hiloint2double(__double2hiint(mag) | (int)((uint32_t)(cm.v[j] & 128u) << 24), __double2loint(mag));
+        const double old = value_of<15>((uint32_t)((int32_t)(cm[j / 4] << (24 - j % 4 * 8)) >> 7) & 0x80fe0000u);
         // (rounded operation by operation: what the formula gives on any machine, ties included)
         m[j] = __dadd_rn(__dmul_rn(c.beta1, __dmul_rn(old, sm)), __dmul_rn(n1, gj));
-        v[j] = __dadd_rn(__dmul_rn(c.beta2, __dmul_rn(value_of<31>(cv.v[j], small_v), sv)), __dmul_rn(__dmul_rn(n2, gj), gj));
+        v[j] = __dadd_rn(__dmul_rn(c.beta2, __dmul_rn(value_of<31>((cv[j / 4] << (24 - j % 4 * 8)) >> 7 & 0x1fe0000u), sv)), __dmul_rn(__dmul_rn(n2, gj), gj));
         const float fm = (float)m[j], fv = (float)v[j];
         p[j] = next_param(p[j], fm, fv, f);
         mm = __uint_as_float(max(__float_as_uint(mm), __float_as_uint(fabsf(fm))));   // NaN above infinity
-        mv = __uint_as_float(max(__float_as_uint(mv), __float_as_uint(fabsf(fv))));
+        mv = __uint_as_float(max(__float_as_uint(mv), __float_as_uint(fv)));
     }
+    store_param(t, i, cnt, vec, p);   // (now: its registers are wanted)
     const float scm = block_scale(mm), scv = block_scale(mv);
     const double im = scm > 0.f ? 1.0 / (double)scm : scm == 0.f ? 0.0 : (double)scm;
     const double iv = scv > 0.f ? 1.0 / (double)scv : scv == 0.f ? 0.0 : (double)scv;
+    cm[0] = cm[1] = cv[0] = cv[1] = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const uint32_t a = min(code_of<15>(fabs(m[j]) * im), 127u);
         uint32_t b = min(code_of<31>(v[j] * iv), 255u);
         if (v[j] > 0.0 && scv > 0.f) b = max(b, 1u);
-        cm.v[j] = (uint8_t)(a | (m[j] < 0.0 ? 128u : 0u));
-        cv.v[j] = (uint8_t)b;
+        cm[j / 4] |= (a | (m[j] < 0.0 ? 128u : 0u)) << (j % 4 * 8);
+        cv[j / 4] |= b << (j % 4 * 8);
     }
     if (wide) {
-        *reinterpret_cast<Pack<uint8_t, 8> *>(mc) = cm;
-        *reinterpret_cast<Pack<uint8_t, 8> *>(vc) = cv;
+        *reinterpret_cast<uint2 *>(mc) = make_uint2(cm[0], cm[1]);
+        *reinterpret_cast<uint2 *>(vc) = make_uint2(cv[0], cv[1]);
     } else if (any) {
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
             if (j < cnt) {
-                mc[j] = cm.v[j];
-                vc[j] = cv.v[j];
+                mc[j] = (uint8_t)(cm[j / 4] >> (j % 4 * 8));
+                vc[j] = (uint8_t)(cv[j / 4] >> (j % 4 * 8));
             }
     }
     __syncwarp();
@@ -251,9 +255,10 @@ __device__ __forceinline__ void step8(const semicrf_adamw_tensor &t, const semic
 }
 
 __device__ __forceinline__ void step32(const semicrf_adamw_tensor &t, const semicrf_adamw_config &c, const Factors &f,
-                                       long long i, int cnt, bool vec, float (&p)[kPer])
+                                       long long i, int cnt, bool vec)
 {
-    float g[kPer], m[kPer], v[kPer];
+    float p[kPer], g[kPer], m[kPer], v[kPer];
+    load_as<float>(t.param, t.param_dtype, i, cnt, vec, p);
     load_as<float>(t.grad, t.grad_dtype, i, cnt, vec, g);
     load8<float, float>(t.exp_avg, i, cnt, vec, m);
     load8<float, float>(t.exp_avg_sq, i, cnt, vec, v);
@@ -267,6 +272,7 @@ __device__ __forceinline__ void step32(const semicrf_adamw_tensor &t, const semi
     }
     store8<float>(t.exp_avg, i, cnt, vec, m);
     store8<float>(t.exp_avg_sq, i, cnt, vec, v);
+    store_param(t, i, cnt, vec, p);
 }
 
 template <int N>
@@ -283,8 +289,10 @@ __device__ __forceinline__ int entry_of(const AdamArgs<N> &a, long long block)
     return lo;
 }
 
+// Blocks of a multiprocessor: 8 bits with 4 (64 registers, 20 bytes of them in memory) 113 us,
+// with 3 (74 registers) 125; 32 bits with 5 (48 registers) 90 us, with 3 (74) 107.
 template <int N, bool EIGHT>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(const __grid_constant__ AdamArgs<N> a)
+__global__ __launch_bounds__(kThreads, EIGHT ? 4 : 5) void adamw_kernel(const __grid_constant__ AdamArgs<N> a)
 {
     const Entry &en = a.e[entry_of<N>(a, blockIdx.x)];
     const semicrf_adamw_tensor &t = en.t;
@@ -307,18 +315,10 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const __grid_constant__
         if (i - (threadIdx.x & 31) * kPer >= t.n) break;
         const int cnt = (int)max(0LL, min((long long)kPer, t.n - i));
         const bool vec = all && cnt == kPer;
-        float p[kPer];
-        load_as<float>(t.param, t.param_dtype, i, cnt, vec, p);
         if (EIGHT)
-            step8(t, c, f, i, cnt, vec, p);
+            step8(t, c, f, i, cnt, vec);
         else
-            step32(t, c, f, i, cnt, vec, p);
-        if (t.param_dtype == SEMICRF_F32)
-            store8<float>(t.param, i, cnt, vec, p);
-        else if (t.param_dtype == SEMICRF_BF16)
-            store8<__nv_bfloat16>(t.param, i, cnt, vec, p);
-        else
-            store8<__half>(t.param, i, cnt, vec, p);
+            step32(t, c, f, i, cnt, vec);
     }
 }
 
