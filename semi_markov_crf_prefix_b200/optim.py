@@ -15,6 +15,7 @@ from __future__ import annotations
 import array
 import ctypes
 import itertools
+import operator
 
 import torch
 
@@ -22,6 +23,10 @@ from . import _lib
 from .encoder import _call
 
 BLOCK = 256   # values that share a scale
+_PARAMS = frozenset((torch.float32, torch.bfloat16, torch.float16))
+_GRADS = _PARAMS | {torch.float64}
+_SINGLE, _CODES = frozenset((torch.float32,)), frozenset((torch.uint8,))
+_dtype, _shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
 _TYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16, torch.float64: _lib.F64}
 
 
@@ -46,12 +51,15 @@ def _same_length(lists):
 
 
 def _check(ts, name, sizes, dtypes, device):
-    """Types, sizes, device and layout of a list's tensors; one pass where all is well."""
+    """Types, sizes, device and layout of a list's tensors: all together, then one by one for the error."""
+    if (set(map(_dtype, ts)) <= dtypes and list(map(torch.Tensor.numel, ts)) == sizes
+            and set(map(torch.Tensor.get_device, ts)) <= {device.index} and all(map(torch.Tensor.is_contiguous, ts))):
+        return
     for t, n in zip(ts, sizes):
         if t.dtype in dtypes and t.numel() == n and t.device == device and t.is_contiguous():
             continue
         if t.dtype not in dtypes:
-            raise TypeError(f"{name} has type {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+            raise TypeError(f"{name} has type {t.dtype}, expected {' or '.join(sorted(map(str, dtypes)))}")
         if t.numel() != n:
             raise ValueError(f"{name} has a tensor of {t.numel()} values, expected {n}")
         if t.device != device:
@@ -60,7 +68,7 @@ def _check(ts, name, sizes, dtypes, device):
 
 
 def _pointers(ts, n):
-    return [0] * n if ts is None else [t.data_ptr() for t in ts]
+    return [0] * n if ts is None else list(map(torch.Tensor.data_ptr, ts))
 
 
 def _table(params, grads, m, v, ms, vs, sizes):
@@ -71,7 +79,7 @@ def _table(params, grads, m, v, ms, vs, sizes):
         kinds = [k | _TYPES[g.dtype] << 32 for k, g in zip(kinds, grads)]
     rows = zip(_pointers(params, n), _pointers(grads, n), _pointers(m, n), _pointers(v, n), _pointers(ms, n),
                _pointers(vs, n), sizes, kinds)
-    return array.array("q", [word for row in rows for word in row])
+    return array.array("q", list(itertools.chain.from_iterable(rows)))
 
 
 def _scalar(x, name, dtype, device):
@@ -80,7 +88,6 @@ def _scalar(x, name, dtype, device):
     return x.data_ptr()
 
 
-@torch.no_grad()
 def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
                grad_scale=1.0, exp_avg_scale=None, exp_avg_sq_scale=None):
     """One step over lists of tensors, in place; `step` counts from 1.
@@ -100,19 +107,19 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     device = params[0].device
     if not params[0].is_cuda:
         raise TypeError("params must be CUDA tensors")
-    kind = (torch.uint8,) if eight else (torch.float32,)
-    sizes = [p.numel() for p in params]
-    _check(params, "params", sizes, (torch.float32, torch.bfloat16, torch.float16), device)
-    _check(grads, "grads", sizes, tuple(_TYPES), device)
-    for p, g in zip(params, grads):
-        if g.shape != p.shape:
-            raise ValueError(f"a gradient of shape {tuple(g.shape)} for a tensor of shape {tuple(p.shape)}")
+    kind = _CODES if eight else _SINGLE
+    sizes = list(map(torch.Tensor.numel, params))
+    _check(params, "params", sizes, _PARAMS, device)
+    _check(grads, "grads", sizes, _GRADS, device)
+    if list(map(_shape, grads)) != list(map(_shape, params)):
+        p, g = next((p, g) for p, g in zip(params, grads) if g.shape != p.shape)
+        raise ValueError(f"a gradient of shape {tuple(g.shape)} for a tensor of shape {tuple(p.shape)}")
     _check(exp_avg, "exp_avg", sizes, kind, device)
     _check(exp_avg_sq, "exp_avg_sq", sizes, kind, device)
     if eight:
         blocks = [-(-n // BLOCK) for n in sizes]
-        _check(exp_avg_scale, "exp_avg_scale", blocks, (torch.float32,), device)
-        _check(exp_avg_sq_scale, "exp_avg_sq_scale", blocks, (torch.float32,), device)
+        _check(exp_avg_scale, "exp_avg_scale", blocks, _SINGLE, device)
+        _check(exp_avg_sq_scale, "exp_avg_sq_scale", blocks, _SINGLE, device)
     c = _lib.AdamWConfig(0.0, betas[0], betas[1], eps, weight_decay, grad_scale, 0)
     if isinstance(step, torch.Tensor):
         c.step_ptr = _scalar(step, "step", torch.int64, device)
@@ -131,7 +138,6 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     torch.autograd.graph.increment_version([*params, *exp_avg, *exp_avg_sq])
 
 
-@torch.no_grad()
 def adamw_state_values(codes, scales, which):
     """The float32 values that 8-bit states stand for; which: "exp_avg" or "exp_avg_sq"."""
     if which not in ("exp_avg", "exp_avg_sq"):
@@ -142,11 +148,11 @@ def adamw_state_values(codes, scales, which):
     device = codes[0].device
     if not codes[0].is_cuda:
         raise TypeError("codes must be CUDA tensors")
-    sizes = [c.numel() for c in codes]
-    _check(codes, "codes", sizes, (torch.uint8,), device)
-    _check(scales, "scales", [-(-n // BLOCK) for n in sizes], (torch.float32,), device)
+    sizes = list(map(torch.Tensor.numel, codes))
+    _check(codes, "codes", sizes, _CODES, device)
+    _check(scales, "scales", [-(-n // BLOCK) for n in sizes], _SINGLE, device)
     # one allocation, each tensor at a multiple of 256 bytes
-    starts = list(itertools.accumulate((-(-n // 64) * 64 for n in sizes), initial=0))
+    starts = list(itertools.accumulate([n + 63 & -64 for n in sizes], initial=0))
     flat = torch.empty(starts[-1], dtype=torch.float32, device=device)
     out = [flat.as_strided(c.shape, c.stride(), at) for c, at in zip(codes, starts)]
     second = which == "exp_avg_sq"
