@@ -180,6 +180,15 @@ def linear_attention_backward(grad_o, q, k, v, log_decay, lengths=None, scale=No
     return dq, dk_, dv_, ds
 
 
+def _first_order(backward):
+    """once_differentiable, whose wrapper is left out where nothing records the backward pass."""
+    once = torch.autograd.function.once_differentiable(backward)
+
+    def run(ctx, *grads):
+        return once(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+    return run
+
+
 class LinearAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, initial_state, log_decay, lengths, scale, reverse, return_state):
@@ -190,7 +199,7 @@ class LinearAttention(torch.autograd.Function):
         return (o, state) if return_state else o
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_first_order
     def backward(ctx, grad_o, grad_state=None):
         q, k, v, initial_state, log_decay, lengths = ctx.saved_tensors
         scale, reverse = ctx.how
@@ -317,7 +326,10 @@ def _norm_backward(dy, x, stats, weight, bias, lengths, shape, d, want_params, w
     device = x.device
     ws = _workspace(ws, _norm_ws(shape, d, True), device)
     dx = torch.empty_like(x)
-    dw, db = torch.empty((2, shape[2]), dtype=torch.float32, device=device) if want_params else (None, None)
+    dw = db = None
+    if want_params:
+        dw = torch.empty(shape[2], dtype=torch.float32, device=device)
+        db = torch.empty(shape[2], dtype=torch.float32, device=device)
     _call("group_norm_backward", device, d, dy.data_ptr(), x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(lengths),
           stats.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db), ws.data_ptr(), ws.numel())
     return dx, dw, db
@@ -332,13 +344,18 @@ class GroupNorm(torch.autograd.Function):
         return y
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_first_order
     def backward(ctx, dy):
         x, weight, bias, lengths, stats = ctx.saved_tensors
         _, want_w, want_b = ctx.needs_input_grad[:3]
-        dx, dw, db = _norm_backward(dy.contiguous(), x, stats, weight, bias, lengths, ctx.shape, ctx.dims, want_w or want_b)
-        return (dx, dw.to(weight.dtype) if want_w else None, db.to(bias.dtype) if want_b else None, None, None, None,
-                None)
+        if not dy.is_contiguous():
+            dy = dy.contiguous()
+        dx, dw, db = _norm_backward(dy, x, stats, weight, bias, lengths, ctx.shape, ctx.dims, want_w or want_b)
+        if want_w and weight.dtype != torch.float32:
+            dw = dw.to(weight.dtype)
+        if want_b and bias.dtype != torch.float32:
+            db = db.to(bias.dtype)
+        return dx, dw if want_w else None, db if want_b else None, None, None, None, None
 
 
 def group_norm(x, groups, weight=None, bias=None, lengths=None, eps=1e-5, activation="none"):
