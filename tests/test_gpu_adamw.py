@@ -200,6 +200,18 @@ def test_overwritten_parameters_are_noticed():
         y.backward()
 
 
+def test_leaves_stay_leaves():
+    # parameters as a model holds them, with gradients recorded around the call
+    w = torch.randn(300, device="cuda", requires_grad=True)
+    for bits in (32, 8):
+        m, v, ms, vs = sc.new_adamw_state([w], bits)
+        old = w.detach().clone()
+        sc.adamw_step([w], [torch.ones_like(w)], m, v, 1, exp_avg_scale=ms, exp_avg_sq_scale=vs)
+        assert w.is_leaf and w.requires_grad and not torch.equal(w, old)
+        if bits == 8:
+            assert not sc.adamw_state_values(m, ms, "exp_avg")[0].requires_grad
+
+
 def test_refusals():
     p, g = make([(8, 4), (5,)], KINDS[:1])
     m, v, _, _ = sc.new_adamw_state(p)

@@ -158,6 +158,31 @@ def test_segments(dtype, d, reverse):
     check(q[:1], k[:1], v[:1], ld, None, reverse=reverse)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_segments_without_a_state(d, reverse):
+    # no state leaves (fewer terms); a segment's end, one more, one less, and NaN behind the ends
+    T = 4000
+    q, k, v, ld, s0 = inputs(4, T, 1, d, d, torch.bfloat16, state=True, decay=-0.002)
+    lengths = torch.tensor([T, 1024, 1025, 1023], dtype=torch.int32, device="cuda")
+    for b, n in enumerate(lengths.tolist()):
+        for x in (q, k, v):
+            x[b, n:] = float("nan")
+    o = sc.linear_attention(q, k, v, ld, lengths=lengths, initial_state=s0, reverse=reverse)
+    args = [torch.nan_to_num(x.double(), nan=0.0) for x in (q, k, v)]
+    want, _ = definition(*args, ld, lengths, d ** -0.5, s0.double(), reverse)
+    M, _ = definition(*[x.abs() for x in args], ld, lengths, d ** -0.5, s0.double().abs(), reverse)
+    assert torch.all((o.double() - want).abs() <= tol(want, M, torch.bfloat16))
+
+
+def test_second_derivatives_are_refused():
+    q, k, v, ld, _ = inputs(1, 9, 1, 16, 16, torch.float32)
+    q.requires_grad_(True)
+    first = torch.autograd.grad(sc.linear_attention(q, k, v, ld).square().sum(), q, create_graph=True)[0]
+    with pytest.raises(RuntimeError):
+        first.sum().backward()
+
+
 def test_pieces_equal_the_whole():
     # a sequence read in pieces with the state handed on, then position by position
     q, k, v, ld, _ = inputs(2, 400, 2, 64, 64, torch.float32)

@@ -234,6 +234,14 @@ def test_bad_lengths_are_reported():
     assert torch.equal(y[0], sc.group_norm(x[:1], 2, w, b)[0]) and torch.all(y[1] == 0)
 
 
+def test_second_derivatives_are_refused():
+    x, w, b = inputs(2, 9, 8, torch.float32)
+    x.requires_grad_(True)
+    first = torch.autograd.grad(sc.group_norm(x, 2, w, b).square().sum(), x, create_graph=True)[0]
+    with pytest.raises(RuntimeError):
+        first.sum().backward()
+
+
 def test_refusals():
     x, w, b = inputs(3, 40, 8, torch.bfloat16)
     f = sc.group_norm
