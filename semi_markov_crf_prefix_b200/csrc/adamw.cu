@@ -131,8 +131,8 @@ __device__ __forceinline__ void store8(void *p, long long i, int cnt, bool vec, 
 __device__ __forceinline__ bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // Code of y >= 0: y 2^(BIAS - 1023), whose bits are the code's with 49 more behind it, small
-// codes included (those are a double's own small values); nearest even, the low word only
-// decides ties.
+// codes included (those are a double's own small values, which the product rounds 49 bits
+// below a code's last); nearest even, the low word only decides ties.
 template <int BIAS>
 __device__ __forceinline__ uint32_t code_of(double y)
 {

@@ -313,6 +313,17 @@ def _norm_forward(x, weight, bias, lengths, shape, d, ws=None):
     return y, stats
 
 
+def _norm_alone(x, weight, bias, lengths, shape, d):
+    """y, with the statistics behind the workspace (whose size is a multiple of 256)."""
+    need = _norm_ws(shape, d, False)
+    ws = torch.empty(need + 8 * shape[0] * shape[3], dtype=torch.uint8, device=x.device)
+    y = torch.empty_like(x)
+    at = ws.data_ptr()
+    _call("group_norm", x.device, d, x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(lengths), y.data_ptr(), at + need, at,
+          need)
+    return y
+
+
 def group_norm_backward(dy, x, stats, groups, weight=None, bias=None, lengths=None, eps=1e-5, activation="none",
                         want_params=True, ws=None):
     """(dx like x, dweight [C] float32, dbias [C] float32); the last two None without want_params."""
@@ -364,4 +375,5 @@ def group_norm(x, groups, weight=None, bias=None, lengths=None, eps=1e-5, activa
     x [N,S,C], zero behind them); activation "none", "silu" or "gelu".  Differentiable with
     respect to x, weight and bias."""
     return _differentiable(GroupNorm, (x, weight, bias), (x, weight, bias, groups, lengths, eps, activation),
-                           lambda: group_norm_forward(x, groups, weight, bias, lengths, eps, activation)[0])
+                           lambda: _norm_alone(x, weight, bias, lengths,
+                                               *_norm_dims(x, groups, weight, bias, lengths, eps, activation)))
