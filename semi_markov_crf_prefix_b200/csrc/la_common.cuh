@@ -102,7 +102,10 @@ __device__ __forceinline__ StateAt state_from(const LaWalk &w, const LaArgs &a, 
 }
 
 // Products of operands in NA and NB terms: go(x, y, accumulate) for the pairs of terms
-// with x + y < N, the smallest first.
+// with x + y < N, the smallest first.  What is left out: 2^-23 of each product of three
+// terms, 2^-16 (both second terms) of two; for float16 that fourth product costs 8 % of a
+// call and takes the outputs' distance from 64 bits from 4.2e-5 to 3.5e-5, most of which is
+// their own rounding.
 template <int NA, int NB, int N, typename F>
 __device__ __forceinline__ void mma_terms(F &&go)
 {

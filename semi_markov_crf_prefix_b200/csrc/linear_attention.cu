@@ -35,8 +35,8 @@ struct LaHot {
 // launch each, and slices of the values' columns, which are independent.  Operands
 // enter the matrix unit as sums of bf16 terms: NI for the inputs (exact), NM for the
 // products P and for the state as an operand of q S (2: 2^-17 relative, far inside the
-// rounding of a 16-bit output; 3 for float32), NK = 3 for the decayed keys, whose
-// products make the float32 state.
+// rounding of a 16-bit output, 2^-11 at best; 3 for float32), NK = 3 for the decayed keys,
+// whose products make the float32 state.
 constexpr int D = 64;
 
 template <typename T>

@@ -195,21 +195,22 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t mbar, uint32_t parity
     }
 }
 
-// Two floats as sums of NT bf16 terms, packed (a low, b high).  Each term but the last
-// is the upper half of what is left (8 bits, cut off: no conversion), the last one
-// rounds to nearest.  Three terms hold a float exactly; two leave 2^-17 of it.
+// Two floats as sums of NT bf16 terms, packed (a low, b high), each the nearest to what is
+// left.  Three terms hold a float exactly; two leave 2^-17 of the value at most, one 2^-9.
+// (First terms that are cut off instead, which needs no conversion, leave twice as much of
+// one sign, and the calls take the same time.)
 template <int NT>
 __device__ __forceinline__ void split2(float a, float b, uint32_t (&t)[NT])
 {
 #pragma unroll
-    for (int i = 0; i + 1 < NT; ++i) {
-        const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-        t[i] = __byte_perm(ua, ub, 0x7632);
-        a -= __uint_as_float(ua & 0xffff0000u);
-        b -= __uint_as_float(ub & 0xffff0000u);
+    for (int i = 0; i < NT; ++i) {
+        const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+        t[i] = *reinterpret_cast<const uint32_t *>(&r);
+        if (i + 1 < NT) {
+            a -= __uint_as_float(t[i] << 16);
+            b -= __uint_as_float(t[i] & 0xffff0000u);
+        }
     }
-    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-    t[NT - 1] = *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // The floats that NT packed terms stand for.

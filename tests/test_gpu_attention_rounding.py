@@ -1,0 +1,79 @@
+"""What linear attention rounds inside a call, at sizes where nothing averages out.
+
+For 16-bit operands the scores times their decays and the state as q's operand enter the
+matrix unit in two bf16 terms, each nearest: 2^-17 of the value at most.  float16 operands
+are two terms themselves, exactly, and the product of both second terms (2^-8 of each
+operand) is left out: 2^-16 of a product, of q and k and of P and v.  Everything else is
+float32: a few roundings of 2^-24 and accumulators that cut at 2^-23, below 2^-20 of the
+absolute sum M at these lengths.  The state's keys are held to 24 bits where a state is
+returned.
+"""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+import torch  # noqa: E402
+
+import semi_markov_crf_prefix_b200 as sc  # noqa: E402
+
+
+def half_step(t):
+    return torch.finfo(t).eps / 2
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("state", [False, True])
+def test_products_to_their_bits(dtype, d, state):
+    # values of opposite sign, so that o is far smaller than the two terms it is made of and
+    # what those lost shows behind o's own rounding; q has few components, so that little is
+    # lost in the scores themselves
+    B, H = 64, 8
+    g = torch.Generator(device="cuda").manual_seed(11)
+    q, k, v = (torch.randn(B, 2, H, d, generator=g, device="cuda").to(dtype) for _ in range(3))
+    q[..., 2:] = 0
+    v[:, 1] = -v[:, 0]
+    k[:, 1] = k[:, 0]
+    k[:, 1, :, 0] += 0.25 * k[:, 0, :, 1]
+    ld = torch.linspace(-0.01, -0.0001, H, device="cuda")
+    s0 = None
+    if state:
+        q[:, 0, :, 1:] = 0      # o of the first position: one row of the state against one product
+        s0 = torch.randn(B, H, d, d, generator=g, device="cuda")
+        s0[:, :, 0] = -(k[:, 0, :, :1].float() * v[:, 0].float()) * (1 + 0.01 * torch.rand(B, H, d, generator=g, device="cuda"))
+    o = sc.linear_attention(q, k, v, ld, scale=1.0, initial_state=s0)
+    lam = torch.exp(ld.double())[:, None]
+    q, k, v = q.double(), k.double(), v.double()
+    sum_of = lambda x, y: (x * y).sum(-1, keepdim=True)  # noqa: E731
+    size = lambda x, y: sum_of(x.abs(), y.abs())  # noqa: E731
+    lead = lambda x: torch.exp2(torch.floor(torch.log2(x.abs())))  # noqa: E731  (2^-17 of this is half a step of two terms)
+    if state:
+        s0 = s0[:, :, 0].double()
+        row, p = q[:, 0, :, :1] * lam, sum_of(q[:, 0], k[:, 0])
+        want, M, got = row * s0 + p * v[:, 0], (row * s0).abs() + (p * v[:, 0]).abs(), o[:, 0]
+        held = row.abs() * lead(s0) + lead(p) * v[:, 0].abs()
+    else:
+        a, b = sum_of(q[:, 1], k[:, 0]) * lam, sum_of(q[:, 1], k[:, 1])
+        want, got = a * v[:, 0] + b * v[:, 1], o[:, 1]
+        M = (size(q[:, 1], k[:, 0]) + size(q[:, 1], k[:, 1])) * v[:, 0].abs()
+        held = (lead(a) + lead(b)) * v[:, 0].abs()
+    tiny = torch.finfo(dtype).smallest_normal * half_step(dtype)
+    off = (got.double() - want).abs() - half_step(dtype) * want.abs() * 1.001 - tiny
+    lost = 2.0 ** -20 + (2.0 ** -15 if dtype == torch.float16 else 0.0)
+    assert torch.all(off <= 2.0 ** -17 * held + lost * M)
+    assert (want.abs() < M / 32).float().mean() > 0.05          # there are such values
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T", [2, 16, 128])
+@pytest.mark.parametrize("d", [64, 128])
+def test_state_is_held_to_24_bits(dtype, T, d):
+    # one-signed products of few positions; 128 positions: 24 cut sums of 2^-23 are 2^-18.4
+    B, H = 32, 4
+    g = torch.Generator(device="cuda").manual_seed(12)
+    q, k, v = (torch.rand(B, T, H, d, generator=g, device="cuda").to(dtype) for _ in range(3))
+    ld = torch.tensor([-0.3, -0.05, -0.007, -0.001], device="cuda")
+    _, s = sc.linear_attention(q, k, v, ld, return_state=True)
+    left = torch.exp(ld.double()[None, :] * (T - 1 - torch.arange(T, device="cuda"))[:, None])[None, :, :, None]
+    want = torch.einsum("bthk,bthv->bhkv", k.double() * left, v.double())
+    assert torch.all((s.double() - want).abs() <= (2.0 ** -20 if T <= 16 else 2.0 ** -18) * want)
