@@ -298,10 +298,11 @@ semicrf_status semicrf_nll_backward(const semicrf_dims *dims, const double *S, c
  *   state_out  float32 [B, H, dk, dv], S behind the last position, or NULL
  * Sums and the state are held in float32, whatever dtype, and each output is rounded to
  * dtype once.  The products run on sums of bf16 terms: bfloat16 inputs are one, the decayed
- * keys that make a returned state three (24 bits); the scores times their decays, and the state
+ * keys that make the state three (24 bits); the scores times their decays, and the state
  * where q multiplies it, are held to 2^-17 of each value for 16-bit dtypes and to 24 bits
  * for float32.  Of products of several terms the smallest are left out: 2^-23 of a product
- * for float32, 2^-16 for float16, none for bfloat16.  A value that is not finite may spread to every position
+ * for float32, 2^-16 for float16, none for bfloat16.  The results do not depend
+ * on which outputs are asked for.  A value that is not finite may spread to every position
  * of its sequence and head.
  */
 typedef struct {

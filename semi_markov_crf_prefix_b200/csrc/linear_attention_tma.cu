@@ -48,7 +48,7 @@ struct LaTables {
 
 template <int D>
 struct TmaCfg {
-    static constexpr int NM = 2;                    // terms of P and S (see the register form)
+    static constexpr int NM = 2, NK = 3;            // terms of P and S, and of K~
     static constexpr int kTile = D / 64 * 16384;    // 128 rows
     static constexpr int kSTile = D * D * 2;
     static constexpr bool kApart = D == 64;         // K has a tile of its own beside K~, or becomes K~'s first term
@@ -58,22 +58,22 @@ struct TmaCfg {
                          kSmem = kBars + 64;
     static constexpr int kO = 128, kKV = kO + D, kCols = D == 64 ? 256 : 512;
     static constexpr int kState = kKV + (kStateTmem ? D : 0);
-    static constexpr int kOut = kKt + 2 * kTile;    // outputs on their way, where K~'s third term is if there is one
+    static constexpr int kOut = kKt + 2 * kTile;    // outputs on their way, where K~'s third term is
     static constexpr int NP = kChunk * (D / 8) / kWorkers, kRows = kWorkers / (D / 8);
     static constexpr int kBlocks = D == 64 ? 2 : 1;
     static_assert(kSmem <= (kBlocks == 2 ? 113 : 227) * 1024, "shared memory");
 };
 
-// NK: terms of K~.  Three (24 bits) where a float32 state leaves the call; two leave 2^-17,
-// which 16-bit outputs do not show, and cost a third less of the shared memory's traffic,
-// the first bound of this kernel (2.9 of 4.2 thousand cycles a chunk at width 64).
-template <int D, int NK>
+// K~ has three terms (24 bits), as the float32 state wants.  Where no state leaves the call
+// two would do for 16-bit outputs and take 6 % (width 64) to 14 % (width 128) less time, but
+// then outputs would differ in their last bits with whether the state is asked for.
+template <int D>
 __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(const __grid_constant__ LaArgs args,
                                                                                 const __grid_constant__ LaMaps maps)
 {
     using G = TmaCfg<D>;
     using T = __nv_bfloat16;
-    constexpr int NM = G::NM, NP = G::NP;
+    constexpr int NM = G::NM, NK = G::NK, NP = G::NP;
     constexpr int kUnroll = D == 128 ? 8 : 1;   // of the matrix instructions: no registers for it at width 64
     constexpr uint64_t kTileD = G::kTile >> 4, kSTileD = G::kSTile >> 4, kRow16 = 2048 >> 4;
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -177,17 +177,11 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
                 }
                 mma_commit(done_qs);
                 tma_store_read();   // the last outputs have left
-                if (NK == 2 && next) {
-                    await(done_qs, parity);
-                    fetch(map.q, G::kQ, full_q, n + 1);
-                }
             }
-            if (NK == 3) {
-                if (!meet()) break;   // K~'s third term may be written
-                if (next && elect_lane()) {
-                    await(done_qs, parity);
-                    fetch(map.q, G::kQ, full_q, n + 1);
-                }
+            if (!meet()) break;   // K~'s third term may be written
+            if (next && elect_lane()) {
+                await(done_qs, parity);
+                fetch(map.q, G::kQ, full_q, n + 1);
             }
             if (!meet()) break;   // K~ is there
             if (elect_lane()) {
@@ -345,7 +339,7 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
             const int lead = s.p0 + n == 0 ? w.lead : 1;
             if (is_whole) await(full_k, parity);
             if (!G::kApart) await(done_qk, parity);   // K~ replaces K
-            uint4 third[NK == 3 ? NP : 1];   // K~'s third term, whose tile the last outputs may still be leaving
+            uint4 third[NP];   // K~'s third term, whose tile the last outputs may still be leaving
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 const unsigned char *at = sm + G::kK + at0 + i * G::kRows * 128;
@@ -368,17 +362,15 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
                 for (int x = 0; x < NK; ++x) {
                     const uint4 v = make_uint4(o[x][0], o[x][1], o[x][2], o[x][3]);
                     if (x == 2)
-                        third[NK == 3 ? i : 0] = v;
+                        third[i] = v;
                     else
                         *reinterpret_cast<uint4 *>(sm + G::kKt + x * G::kTile + at0 + i * G::kRows * 128) = v;
                 }
             }
-            if (NK == 3) {
-                if (__syncthreads_or(!alive)) break;
+            if (__syncthreads_or(!alive)) break;
 #pragma unroll
-                for (int i = 0; i < NP; ++i)
-                    *reinterpret_cast<uint4 *>(sm + G::kKt + 2 * G::kTile + at0 + i * G::kRows * 128) = third[NK == 3 ? i : 0];
-            }
+            for (int i = 0; i < NP; ++i)
+                *reinterpret_cast<uint4 *>(sm + G::kKt + 2 * G::kTile + at0 + i * G::kRows * 128) = third[i];
             smem_to_mma();
             if (__syncthreads_or(!alive)) break;
 
@@ -549,30 +541,31 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
 }
 
 // What a whole segment adds to the state: KV of each chunk as above, S = lam^128 S + KV.
-// K~ and KV are double (K~ where two terms are enough), so that a chunk's products run
-// while the next one's keys are weighted and the last one's sums are taken up.
+// V's tile is double, so that the next one travels while a chunk's products run; the sums of
+// a chunk are taken up before the next keys are weighted into K~'s only tiles (three of
+// 32 KB at width 128).
 // Segments that end inside the sequence's last chunk are not asked for.
 //
 // Measured: 32 walks of 40 chunks at width 128 in 90 us, 2.2 us a chunk (two terms at the
 // matrix unit 0.8), the call of 4 x 20000 positions and 8 heads 309 us; 334 with the outputs'
 // kernel less its outputs, one tile of each kind.  At width 64 two blocks share an SM and the
 // second tiles change nothing (52 us for 288 segments of 22 chunks).
-template <int D, int NK>
+template <int D>
 struct StateCfg {
-    static constexpr int kTile = D / 64 * 16384, NB = NK == 2 ? 2 : 1;
-    static constexpr int kK = 0, kV = kK + kTile, kKt = kV + 2 * kTile, kBars = kKt + NB * NK * kTile, kSmem = kBars + 64;
+    static constexpr int kTile = D / 64 * 16384, NK = 3;   // (terms of K~)
+    static constexpr int kK = 0, kV = kK + kTile, kKt = kV + 2 * kTile, kBars = kKt + NK * kTile, kSmem = kBars + 64;
     static constexpr int kKV = 0, kState = 2 * D, kCols = D == 64 ? 128 : 512;
     static constexpr int NP = kChunk * (D / 8) / kWorkers, kRows = kWorkers / (D / 8);
     static constexpr int kBlocks = D == 64 ? 2 : 1;
     static_assert(kSmem <= (kBlocks == 2 ? 113 : 227) * 1024, "shared memory");
 };
 
-template <int D, int NK>
-__global__ __launch_bounds__(kThreads, (StateCfg<D, NK>::kBlocks)) void la_state_kernel(const __grid_constant__ LaArgs args,
-                                                                                    const __grid_constant__ LaMaps maps)
+template <int D>
+__global__ __launch_bounds__(kThreads, (StateCfg<D>::kBlocks)) void la_state_kernel(const __grid_constant__ LaArgs args,
+                                                                                  const __grid_constant__ LaMaps maps)
 {
-    using G = StateCfg<D, NK>;
-    constexpr int NB = G::NB, NP = G::NP;
+    using G = StateCfg<D>;
+    constexpr int NK = G::NK, NP = G::NP;
     constexpr uint64_t kTileD = G::kTile >> 4, kRow16 = 2048 >> 4;
     extern __shared__ __align__(1024) unsigned char sm[];
     const LaWalk &w = args.w[blockIdx.y];
@@ -624,7 +617,7 @@ __global__ __launch_bounds__(kThreads, (StateCfg<D, NK>::kBlocks)) void la_state
                 await(full_v + 8 * odd, n >> 1 & 1);
                 tc_after_sync();
                 const uint32_t id = mma_idesc(D, nv, true, true);
-                const uint64_t dk = desc_swz(smem + G::kKt + (NB == 2 ? odd * NK * G::kTile : 0), 16384);
+                const uint64_t dk = desc_swz(smem + G::kKt, 16384);
                 const uint64_t dv = desc_swz(smem + G::kV + odd * G::kTile, 16384);
 #pragma unroll
                 for (int x = NK - 1; x >= 0; --x)
@@ -709,9 +702,9 @@ __global__ __launch_bounds__(kThreads, (StateCfg<D, NK>::kBlocks)) void la_state
         };
         bool broken = false;
         for (int n = 0; n < chunks && !broken; ++n) {
-            if (NB == 1 && n > 0) take_up(n - 1);   // K~'s only tiles are read
+            if (n > 0) take_up(n - 1);   // K~'s tiles are read
             await(full_k, n & 1);
-            unsigned char *to = sm + G::kKt + (NB == 2 ? (n & 1) * NK * G::kTile : 0) + at0;
+            unsigned char *to = sm + G::kKt + at0;
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 const uint4 u = *reinterpret_cast<const uint4 *>(sm + G::kK + at0 + i * G::kRows * 128);
@@ -731,7 +724,6 @@ __global__ __launch_bounds__(kThreads, (StateCfg<D, NK>::kBlocks)) void la_state
             }
             smem_to_mma();
             broken = __syncthreads_or(!alive);
-            if (NB == 2 && n > 0 && !broken) take_up(n - 1);
         }
         if (!broken) take_up(chunks - 1);
         float *to = segment_at(w, args, s);
@@ -793,20 +785,15 @@ bool make_map(CUtensorMap *m, const void *p, const long long (&st)[3], int d, co
 
 using Kernel = void (*)(LaArgs, LaMaps);
 
-// The kernel for a width, a pass and the terms of K~, and its shared memory.
-Kernel kernel_of(int width, bool state_only, bool keeps, int *smem)
+// The kernel for a width and a pass, and its shared memory.
+Kernel kernel_of(int width, bool state_only, int *smem)
 {
     if (state_only) {
-        if (width == 64) {
-            *smem = keeps ? StateCfg<64, 3>::kSmem : StateCfg<64, 2>::kSmem;
-            return keeps ? la_state_kernel<64, 3> : la_state_kernel<64, 2>;
-        }
-        *smem = keeps ? StateCfg<128, 3>::kSmem : StateCfg<128, 2>::kSmem;
-        return keeps ? la_state_kernel<128, 3> : la_state_kernel<128, 2>;
+        *smem = width == 64 ? StateCfg<64>::kSmem : StateCfg<128>::kSmem;
+        return width == 64 ? la_state_kernel<64> : la_state_kernel<128>;
     }
     *smem = width == 64 ? TmaCfg<64>::kSmem : TmaCfg<128>::kSmem;
-    if (width == 64) return keeps ? la_tma_kernel<64, 3> : la_tma_kernel<64, 2>;
-    return keeps ? la_tma_kernel<128, 3> : la_tma_kernel<128, 2>;
+    return width == 64 ? la_tma_kernel<64> : la_tma_kernel<128>;
 }
 
 }  // namespace
@@ -828,10 +815,8 @@ bool la_tma_ok(const LaArgs &a, int dtype)
 
 cudaError_t launch_la_tma(const LaArgs &a, bool state_only, cudaStream_t st, int *n)
 {
-    bool keeps = false;   // some walk's state leaves the call
-    for (int i = 0; i < a.nwalk; ++i) keeps |= a.w[i].s_out != nullptr;
     int smem;
-    const Kernel k = kernel_of(a.width, state_only, keeps, &smem);
+    const Kernel k = kernel_of(a.width, state_only, &smem);
     // (also binds the device's context to a thread that makes its first call, which the
     // driver's encoder wants: the backward pass runs in a thread of its own)
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -5,8 +5,8 @@ matrix unit in two bf16 terms, each nearest: 2^-17 of the value at most.  float1
 are two terms themselves, exactly, and the product of both second terms (2^-8 of each
 operand) is left out: 2^-16 of a product, of q and k and of P and v.  Everything else is
 float32: a few roundings of 2^-24 and accumulators that cut at 2^-23, below 2^-20 of the
-absolute sum M at these lengths.  The state's keys are held to 24 bits where a state is
-returned.
+absolute sum M at these lengths.  The state's keys are held to 24 bits.  All outputs are
+independent of which of them are asked for.
 """
 import pytest
 
@@ -77,3 +77,21 @@ def test_state_is_held_to_24_bits(dtype, T, d):
     left = torch.exp(ld.double()[None, :] * (T - 1 - torch.arange(T, device="cuda"))[:, None])[None, :, :, None]
     want = torch.einsum("bthk,bthv->bhkv", k.double() * left, v.double())
     assert torch.all((s.double() - want).abs() <= (2.0 ** -20 if T <= 16 else 2.0 ** -18) * want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [300, 4000])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_outputs_do_not_depend_on_what_is_asked_for(d, T, reverse):
+    g = torch.Generator(device="cuda").manual_seed(13)
+    q, k, v, do = (torch.randn(2, T, 2, d, generator=g, device="cuda").bfloat16() for _ in range(4))
+    s0 = torch.randn(2, 2, d, d, generator=g, device="cuda")
+    ld = torch.tensor([-0.02, -0.0005], device="cuda")
+    for initial in (None, s0):
+        how = dict(initial_state=initial, reverse=reverse)
+        a, none = sc.linear_attention_forward(q, k, v, ld, **how)
+        b, _ = sc.linear_attention_forward(q, k, v, ld, return_state=True, **how)
+        assert none is None and torch.equal(a, b)
+        ga = sc.linear_attention_backward(do, q, k, v, ld, **how)
+        gb = sc.linear_attention_backward(do, q, k, v, ld, want_initial_state=True, **how)
+        assert all(torch.equal(x, y) for x, y in zip(ga[:3], gb[:3]))
