@@ -392,7 +392,8 @@ semicrf_status semicrf_group_norm_backward(const semicrf_norm_dims *dims, const 
  * A code's value is scale times a small float of 3 mantissa bits: m has a sign bit
  * and 4 exponent bits (bias 15), v 5 exponent bits (bias 31); a block's scale is its
  * largest magnitude / 1.875, codes are nearest even, and a v above 0 has a code above 0.
- * A block with a value that is not finite reads as NaN from then on.
+ * A block in which a moment is not finite (or passes float32, as the square of a gradient
+ * above 1e20 does) reads as NaN from then on, all 256 values of it.
  * step counts from 1; step_ptr (int64) and lr_ptr (float32), where not NULL, are
  * device scalars read by the kernel instead of step and lr, so that a captured step
  * follows them.  Tensors must not overlap.

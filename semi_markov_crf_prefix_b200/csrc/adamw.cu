@@ -155,9 +155,12 @@ __device__ __forceinline__ float float_value_of(uint32_t c)
     return __uint_as_float(c << 20) * __uint_as_float((127u + 127u - BIAS) << 23);   // (a float's own small values)
 }
 
+// NaN where the largest is not finite: an infinite scale would give codes of 0 that read as
+// NaN and others that read as infinity, which a second moment's root turns into no update.
 __device__ __forceinline__ float block_scale(float most)
 {
     const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+    if (bits >= 0x7f800000u) return __uint_as_float(0x7fffffffu);
     return (float)((double)__uint_as_float(bits) / 1.875);
 }
 

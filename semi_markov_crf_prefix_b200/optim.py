@@ -8,7 +8,9 @@ floating types) into new parameters.
 Everything is updated in place on the current CUDA stream.  In 8 bits a moment moves
 only when an update passes half of its code's spacing (1/16 of its value at most), so
 beta2 near 1 makes the second moment follow slowly growing or shrinking gradients in
-steps; 32 bits are the exact form.
+steps; 32 bits are the exact form.  Where a moment of a block of 256 values is not finite, or
+passes float32, the whole block's moments read as NaN, and its parameters are NaN after the
+next step: gradients that may overflow are to be checked before the call.
 """
 from __future__ import annotations
 

@@ -1,0 +1,63 @@
+"""AdamW's states where they leave the ordinary range: blocks of 8-bit codes with values that
+are not finite or pass float32."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+import torch  # noqa: E402
+
+import semi_markov_crf_prefix_b200 as sc  # noqa: E402
+
+
+@pytest.mark.parametrize("dtype,value", [(torch.float32, 1e21), (torch.bfloat16, 1e21), (torch.float64, 1e25),
+                                         (torch.float32, float("inf")), (torch.float32, -float("inf")),
+                                         (torch.float32, float("nan")), (torch.float64, 1e300)])
+def test_a_block_that_overflows_reads_as_nan(dtype, value):
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    p = [torch.randn(1000, generator=gen, device="cuda")]
+    g = (torch.randn(1000, generator=gen, device="cuda") * 1e-2).to(dtype)
+    g[300] = value                     # in the second block of 256
+    m, v, ms, vs = sc.new_adamw_state(p, 8)
+    inside = torch.zeros(1000, dtype=torch.bool, device="cuda")
+    inside[256:512] = True
+    sc.adamw_step(p, [g], m, v, 1, exp_avg_scale=ms, exp_avg_sq_scale=vs)
+    second = sc.adamw_state_values(v, vs, "exp_avg_sq")[0]
+    assert torch.equal(torch.isnan(second), inside) and torch.isfinite(second[~inside]).all()
+    first = sc.adamw_state_values(m, ms, "exp_avg")[0]
+    # the first moment passes float32 only where 0.1 of the gradient does
+    if abs(0.1 * value) < torch.finfo(torch.float32).max:
+        assert torch.isfinite(first).all()
+    else:
+        assert torch.equal(torch.isnan(first), inside) and torch.isfinite(first[~inside]).all()
+    # ordinary gradients afterwards: the block's parameters say so, the others go on
+    g.fill_(1e-2)
+    before = p[0].clone()
+    sc.adamw_step(p, [g], m, v, 2, exp_avg_scale=ms, exp_avg_sq_scale=vs)
+    assert torch.equal(torch.isnan(p[0]), inside)
+    assert torch.all(p[0][~inside] != before[~inside])
+    second = sc.adamw_state_values(v, vs, "exp_avg_sq")[0]
+    assert torch.equal(torch.isnan(second), inside)
+
+
+def test_a_moment_that_is_infinite_already():
+    # float32 states allow it; here a code's scale does
+    p = [torch.ones(512, device="cuda")]
+    m, v, ms, vs = sc.new_adamw_state(p, 8)
+    m[0].fill_(100)
+    ms[0].fill_(1.0)
+    ms[0][1] = float("inf")
+    sc.adamw_step(p, [torch.full((512,), 1e-2, device="cuda")], m, v, 1, exp_avg_scale=ms, exp_avg_sq_scale=vs)
+    first = sc.adamw_state_values(m, ms, "exp_avg")[0]
+    assert torch.isfinite(first[:256]).all() and torch.isnan(first[256:]).all()
+
+
+def test_the_largest_moments_that_float32_holds():
+    # a block's largest value at float32's end is no overflow
+    top = 1.8e19
+    p = [torch.zeros(256, device="cuda")]
+    g = torch.full((256,), top, device="cuda")
+    m, v, ms, vs = sc.new_adamw_state(p, 8)
+    sc.adamw_step(p, [g], m, v, 1, betas=(0.9, 0.0), exp_avg_scale=ms, exp_avg_sq_scale=vs)
+    second = sc.adamw_state_values(v, vs, "exp_avg_sq")[0]
+    assert torch.allclose(second, torch.full_like(second, top ** 2), rtol=2.0 ** -4)
+    assert torch.allclose(p[0], torch.full_like(p[0], -1e-3), rtol=1e-5)
