@@ -394,6 +394,8 @@ semicrf_status semicrf_group_norm_backward(const semicrf_norm_dims *dims, const 
  * largest magnitude / 1.875, codes are nearest even, and a v above 0 has a code above 0.
  * A block in which a moment is not finite (or passes float32, as the square of a gradient
  * above 1e20 does) reads as NaN from then on, all 256 values of it.
+ * A float64 gradient is scaled before it is rounded.  eps, and with float32 states the
+ * grad_scale of other gradients, are 0 or within float32's normal range.
  * step counts from 1; step_ptr (int64) and lr_ptr (float32), where not NULL, are
  * device scalars read by the kernel instead of step and lr, so that a captured step
  * follows them.  Tensors must not overlap.

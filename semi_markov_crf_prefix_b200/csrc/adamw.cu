@@ -17,6 +17,7 @@
 // instead of correctly rounded and powers of beta on the host took it from 178 to 143;
 // codes read and written as the high words of doubles 2^1008 (2^992) times too small, a
 // multiplication for a change of the bias and a case for small codes, to 125.
+#include <float.h>
 #include <math.h>
 
 #include "device_util.cuh"
@@ -70,10 +71,17 @@ __device__ __forceinline__ R cvt(T v)
         return (R)v;
 }
 
-// 8 values from index i on (cnt of them exist); vec: whole and 16-byte aligned.
+// 8 values from index i on (cnt of them exist); vec: whole and 16-byte aligned; float64 ones
+// to float times `by`.
 template <typename R, typename T>
-__device__ __forceinline__ void load8(const void *p, long long i, int cnt, bool vec, R (&o)[kPer])
+__device__ __forceinline__ void load8(const void *p, long long i, int cnt, bool vec, R (&o)[kPer], double by = 1.0)
 {
+    auto cast = [&](T v) {
+        if constexpr (sizeof(T) == 8 && sizeof(R) == 4)
+            return (R)(v * by);
+        else
+            return cvt<R, T>(v);
+    };
     const T *s = static_cast<const T *>(p) + i;
     constexpr int n = 16 / sizeof(T);
     if (vec) {
@@ -87,11 +95,11 @@ __device__ __forceinline__ void load8(const void *p, long long i, int cnt, bool 
             for (int j = 0; j < kPer; ++j) o[j] = (R)f[j];
         } else {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) o[j] = (R)h[j / n].v[j % n];
+            for (int j = 0; j < kPer; ++j) o[j] = cast(h[j / n].v[j % n]);
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) o[j] = j < cnt ? cvt<R, T>(s[j]) : (R)0;
+        for (int j = 0; j < kPer; ++j) o[j] = j < cnt ? cast(s[j]) : (R)0;
     }
 }
 
@@ -262,10 +270,13 @@ __device__ __forceinline__ void step32(const semicrf_adamw_tensor &t, const semi
 {
     float p[kPer], g[kPer], m[kPer], v[kPer];
     load_as<float>(t.param, t.param_dtype, i, cnt, vec, p);
-    load_as<float>(t.grad, t.grad_dtype, i, cnt, vec, g);
+    if (t.grad_dtype == SEMICRF_F64)   // scaled before it is rounded: the product may fit where the gradient does not
+        load8<float, double>(t.grad, i, cnt, vec, g, c.grad_scale);
+    else
+        load_as<float>(t.grad, t.grad_dtype, i, cnt, vec, g);
     load8<float, float>(t.exp_avg, i, cnt, vec, m);
     load8<float, float>(t.exp_avg_sq, i, cnt, vec, v);
-    const float gs = (float)c.grad_scale;
+    const float gs = t.grad_dtype == SEMICRF_F64 ? 1.f : (float)c.grad_scale;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const float gj = g[j] * gs;
@@ -434,6 +445,10 @@ extern "C" semicrf_status semicrf_adamw(const semicrf_adamw_tensor *tensors, int
         !(c.weight_decay >= 0.0) || !isfinite(c.grad_scale) || (!c.lr_ptr && !(c.lr >= 0.0)) ||
         (!c.step_ptr && c.step < 1))
         return SEMICRF_ERR_INVALID_ARG;
+    // eps enters the quotient as float32, grad_scale a gradient that is not float64
+    if (c.eps > 0.0 && c.eps < FLT_MIN) return SEMICRF_ERR_INVALID_ARG;
+    const double scale = fabs(c.grad_scale);
+    const bool scale_fits = scale == 0.0 || (scale >= FLT_MIN && scale <= FLT_MAX);
     int eight = 0, filled = 0;
     for (int i = 0; i < count; ++i) {
         const semicrf_adamw_tensor &t = tensors[i];
@@ -445,6 +460,7 @@ extern "C" semicrf_status semicrf_adamw(const semicrf_adamw_tensor *tensors, int
             return SEMICRF_ERR_INVALID_ARG;
         ++filled;
         eight += t.exp_avg_scale != nullptr;
+        if (!scale_fits && !t.exp_avg_scale && t.grad_dtype != SEMICRF_F64) return SEMICRF_ERR_INVALID_ARG;
     }
     if (eight && eight != filled) return SEMICRF_ERR_INVALID_ARG;   // one kind of state a call
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -61,3 +61,18 @@ def test_the_largest_moments_that_float32_holds():
     second = sc.adamw_state_values(v, vs, "exp_avg_sq")[0]
     assert torch.allclose(second, torch.full_like(second, top ** 2), rtol=2.0 ** -4)
     assert torch.allclose(p[0], torch.full_like(p[0], -1e-3), rtol=1e-5)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_large_float64_gradients_are_scaled_before_they_are_rounded(bits):
+    # the gradients pass float32, scaled ones do not
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    g = torch.randn(777, generator=gen, device="cuda", dtype=torch.float64)
+    p = [torch.randn(777, generator=gen, device="cuda")]
+    q = [p[0].clone()]
+    a, b = sc.new_adamw_state(p, bits), sc.new_adamw_state(q, bits)
+    scale = 2.0 ** -120
+    sc.adamw_step(p, [g * 2.0 ** 130], a[0], a[1], 1, grad_scale=scale, exp_avg_scale=a[2], exp_avg_sq_scale=a[3])
+    sc.adamw_step(q, [g * 2.0 ** 10], b[0], b[1], 1, exp_avg_scale=b[2], exp_avg_sq_scale=b[3])
+    assert torch.isfinite(p[0]).all() and torch.equal(p[0], q[0])
+    assert all(torch.equal(x, y) for x, y in zip(a[0] + a[1], b[0] + b[1]))

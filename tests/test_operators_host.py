@@ -1,0 +1,31 @@
+"""The operators around the loss without a GPU, beside test_encoder_host.py: arguments that are
+refused, and what needs no device."""
+import ctypes
+
+import pytest
+
+from semi_markov_crf_prefix_b200 import _lib
+from semi_markov_crf_prefix_b200 import build as build_mod
+
+ARG = _lib.SEMICRF_ERR_INVALID_ARG
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build_mod.build()
+    return _lib.load()
+
+
+class Entry(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("ms", ctypes.c_void_p), ("vs", ctypes.c_void_p), ("n", ctypes.c_int64), ("pt", ctypes.c_int32),
+                ("gt", ctypes.c_int32)]
+
+
+@pytest.mark.parametrize("grad_scale,eps", [(1e39, 1e-8), (-1e39, 1e-8), (1e-39, 1e-8), (1e-300, 1e-8), (1.0, 1e-39),
+                                            (1.0, 1e-60), (float("nan"), 1e-8)])
+def test_what_float32_cannot_hold_is_refused(lib, grad_scale, eps):
+    # nothing is launched: the addresses are never used
+    e = (Entry * 1)(Entry(8, 8, 8, 8, None, None, 10, _lib.F32, _lib.BF16))
+    c = _lib.AdamWConfig(1e-3, 0.9, 0.999, eps, 0.01, grad_scale, 1, None, None)
+    assert lib.semicrf_adamw(e, 1, ctypes.byref(c), None) == ARG
