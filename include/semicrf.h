@@ -398,7 +398,8 @@ semicrf_status semicrf_group_norm_backward(const semicrf_norm_dims *dims, const 
  * grad_scale of other gradients, are 0 or within float32's normal range.
  * step counts from 1; step_ptr (int64) and lr_ptr (float32), where not NULL, are
  * device scalars read by the kernel instead of step and lr, so that a captured step
- * follows them.  Tensors must not overlap.
+ * follows them.  What is written overlaps nothing else of the call (checked); gradients,
+ * which are read, may be shared.
  */
 typedef struct {
     void *param;

@@ -20,6 +20,10 @@
 #include <float.h>
 #include <math.h>
 
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "device_util.cuh"
 #include "encoder_internal.h"
 
@@ -421,6 +425,43 @@ semicrf_status ended(cudaError_t e, int launches)
     return SEMICRF_OK;
 }
 
+// Whether what a step writes overlaps anything else that it touches (the thread blocks of one
+// tensor would race with another's); gradients are only read and may be shared.
+struct Range {
+    uintptr_t from, to;
+    bool written;
+};
+
+semicrf_status apart(const semicrf_adamw_tensor *t, int count)
+{
+    const std::unique_ptr<Range[]> all(new (std::nothrow) Range[(size_t)count * 6]);
+    if (!all) return SEMICRF_ERR_INVALID_ARG;
+    size_t n = 0;
+    auto add = [&](const void *p, long long bytes, bool written) {
+        const uintptr_t from = reinterpret_cast<uintptr_t>(p);
+        if (p) all[n++] = {from, from + bytes, written};
+    };
+    for (int i = 0; i < count; ++i) {
+        if (t[i].n == 0) continue;
+        const bool eight = t[i].exp_avg_scale;
+        const long long state = t[i].n * (eight ? 1 : 4), scales = (t[i].n + kBlock - 1) / kBlock * 4;
+        add(t[i].param, t[i].n * (t[i].param_dtype == SEMICRF_F32 ? 4 : 2), true);
+        add(t[i].grad, t[i].n * (t[i].grad_dtype == SEMICRF_F64 ? 8 : t[i].grad_dtype == SEMICRF_F32 ? 4 : 2), false);
+        add(t[i].exp_avg, state, true);
+        add(t[i].exp_avg_sq, state, true);
+        add(t[i].exp_avg_scale, scales, true);
+        add(t[i].exp_avg_sq_scale, scales, true);
+    }
+    std::sort(all.get(), all.get() + n, [](const Range &a, const Range &b) { return a.from < b.from; });
+    uintptr_t end = 0, written = 0;   // of all ranges so far, of those that are written
+    for (size_t i = 0; i < n; ++i) {
+        if (all[i].from < (all[i].written ? end : written)) return SEMICRF_ERR_INVALID_ARG;
+        end = std::max(end, all[i].to);
+        if (all[i].written) written = std::max(written, all[i].to);
+    }
+    return SEMICRF_OK;
+}
+
 bool tensors_ok(const semicrf_adamw_tensor *t, int count)
 {
     if (count < 0 || (count > 0 && !t)) return false;
@@ -463,6 +504,7 @@ extern "C" semicrf_status semicrf_adamw(const semicrf_adamw_tensor *tensors, int
         if (!scale_fits && !t.exp_avg_scale && t.grad_dtype != SEMICRF_F64) return SEMICRF_ERR_INVALID_ARG;
     }
     if (eight && eight != filled) return SEMICRF_ERR_INVALID_ARG;   // one kind of state a call
+    if (const semicrf_status s = apart(tensors, count)) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int n = 0;
     cudaError_t e = launch_all(tensors, count, c, st, &n, [&](const auto &a, unsigned blocks) {

@@ -84,6 +84,20 @@ def _table(params, grads, m, v, ms, vs, sizes):
     return array.array("q", list(itertools.chain.from_iterable(rows)))
 
 
+def _refuse_overlaps(written, grads):
+    """Says which tensors of a refused call overlap, if any do."""
+    span = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())  # noqa: E731
+    spans = sorted((*span(t), name) for name, ts in [*written, ("grads", grads)] for t in ts or [] if t.numel())
+    end, last, wrote, writer = 0, None, 0, None   # of all so far, of those that are written
+    for a, b, name in spans:
+        if a < (wrote if name == "grads" else end):
+            raise ValueError(f"the same tensor is given twice, or one overlaps another: {name} and {writer if name == 'grads' else last}")
+        if b > end:
+            end, last = b, name
+        if name != "grads" and b > wrote:
+            wrote, writer = b, name
+
+
 def _scalar(x, name, dtype, device):
     if x.dtype != dtype or x.numel() != 1 or x.device != device:
         raise TypeError(f"{name} must be a number or one {dtype} value on {device}")
@@ -132,10 +146,12 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     else:
         c.lr = lr
     words = _table(params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, sizes)
-    full = [p for p, n in zip(words[0::8], sizes) if n]
-    if len(set(full)) != len(full):
-        raise ValueError("the same tensor is given twice")
-    _call("adamw", device, words.buffer_info()[0], len(params), ctypes.byref(c))
+    try:
+        _call("adamw", device, words.buffer_info()[0], len(params), ctypes.byref(c))
+    except _lib.SemiCRFError:
+        _refuse_overlaps([("params", params), ("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq),
+                          ("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)], grads)
+        raise
     # autograd refuses a graph that saved what was just overwritten
     torch.autograd.graph.increment_version([*params, *exp_avg, *exp_avg_sq])
 

@@ -76,3 +76,24 @@ def test_large_float64_gradients_are_scaled_before_they_are_rounded(bits):
     sc.adamw_step(q, [g * 2.0 ** 10], b[0], b[1], 1, exp_avg_scale=b[2], exp_avg_sq_scale=b[3])
     assert torch.isfinite(p[0]).all() and torch.equal(p[0], q[0])
     assert all(torch.equal(x, y) for x, y in zip(a[0] + a[1], b[0] + b[1]))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_overlaps_are_refused_and_neighbours_are_not(bits):
+    flat, g = torch.randn(1024, device="cuda"), torch.randn(512, device="cuda")
+    p = [flat[:512], flat[512:]]
+    m, v, ms, vs = sc.new_adamw_state(p, bits)
+    how = dict(exp_avg_scale=ms, exp_avg_sq_scale=vs)
+    sc.adamw_step(p, [g, g], m, v, 1, **how)                # one gradient for both
+    want = flat.clone()
+    bad = [lambda: sc.adamw_step([flat[:512], flat[511:1023]], [g, g], m, v, 2, **how),
+           lambda: sc.adamw_step([p[0], p[0]], [g, g], m, v, 2, **how),
+           lambda: sc.adamw_step(p, [g, g], [m[0], m[0]], v, 2, **how),
+           lambda: sc.adamw_step(p, [g, g], m, [v[0], m[1]], 2, **how),
+           lambda: sc.adamw_step(p, [g, flat[:512]], m, v, 2, **how)]
+    if bits == 8:
+        bad.append(lambda: sc.adamw_step(p, [g, g], m, v, 2, exp_avg_scale=[ms[0], ms[0]], exp_avg_sq_scale=vs))
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    assert torch.equal(flat, want)

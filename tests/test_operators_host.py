@@ -29,3 +29,25 @@ def test_what_float32_cannot_hold_is_refused(lib, grad_scale, eps):
     e = (Entry * 1)(Entry(8, 8, 8, 8, None, None, 10, _lib.F32, _lib.BF16))
     c = _lib.AdamWConfig(1e-3, 0.9, 0.999, eps, 0.01, grad_scale, 1, None, None)
     assert lib.semicrf_adamw(e, 1, ctypes.byref(c), None) == ARG
+
+
+def test_overlapping_tensors_are_refused(lib):
+    # what a step writes against everything else; fake addresses, and every call is refused
+    base, n, cfg = 1 << 30, 300, _lib.AdamWConfig(1e-3, 0.9, 0.999, 1e-8, 0.01, 1.0, 1, None, None)
+    at = lambda i: base + (i << 16)  # noqa: E731
+    good = [at(i) for i in range(6)]
+    for eight in (False, True):
+        row = lambda ptrs, k=0: Entry(*[p + (k << 24) for p in ptrs[:4]],  # noqa: E731
+                                      *([p + (k << 24) for p in ptrs[4:]] if eight else [None, None]), n, _lib.F32, _lib.F32)
+        for i in range(6 if eight else 4):
+            for j in range(6 if eight else 4):
+                size = [4 * n, 4 * n, n if eight else 4 * n, n if eight else 4 * n, 8, 8][j]
+                if i == j:
+                    continue
+                bad = list(good)
+                bad[i] = good[j] + size - 1                # the last byte of the other one
+                assert lib.semicrf_adamw((Entry * 1)(row(bad)), 1, ctypes.byref(cfg), None) == ARG, (i, j)
+                two = (Entry * 2)(row(good), row(good, 1))
+                if i != 1:
+                    setattr(two[1], Entry._fields_[i][0], good[i] + 4)     # another tensor's own kind
+                    assert lib.semicrf_adamw(two, 2, ctypes.byref(cfg), None) == ARG, i
