@@ -153,7 +153,8 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
                           ("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)], grads)
         raise
     # autograd refuses a graph that saved what was just overwritten
-    torch.autograd.graph.increment_version([*params, *exp_avg, *exp_avg_sq])
+    torch.autograd.graph.increment_version([*params, *exp_avg, *exp_avg_sq, *(exp_avg_scale or ()),
+                                            *(exp_avg_sq_scale or ())])
 
 
 def adamw_state_values(codes, scales, which):

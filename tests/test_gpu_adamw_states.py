@@ -97,3 +97,14 @@ def test_overlaps_are_refused_and_neighbours_are_not(bits):
         with pytest.raises(ValueError):
             call()
     assert torch.equal(flat, want)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_everything_written_is_reported_to_autograd(bits):
+    p = [torch.randn(300, device="cuda"), torch.randn(5, device="cuda")]
+    m, v, ms, vs = sc.new_adamw_state(p, bits)
+    g = [torch.ones_like(t) for t in p]
+    written = [*p, *m, *v, *(ms or ()), *(vs or ())]
+    before = [t._version for t in written]
+    sc.adamw_step(p, g, m, v, 1, exp_avg_scale=ms, exp_avg_sq_scale=vs)
+    assert all(t._version > n for t, n in zip(written, before)) and all(t._version == 0 for t in g)
