@@ -108,7 +108,8 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
                grad_scale=1.0, exp_avg_scale=None, exp_avg_sq_scale=None):
     """One step over lists of tensors, in place; `step` counts from 1.
 
-    params: float32, bfloat16 or float16; grads: those or float64, of the params' shapes;
+    params: float32, bfloat16 or float16; grads: those or float64, of the params' shapes
+    (None: the parameter had no part in the loss and stays as it is, its states too);
     exp_avg, exp_avg_sq: float32, or uint8 with the lists exp_avg_scale and
     exp_avg_sq_scale (new_adamw_state).  step and lr may be CUDA scalars (int64 and
     float32), which the kernel reads: a captured step then follows them.
@@ -118,6 +119,10 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
         raise ValueError("exp_avg_scale and exp_avg_sq_scale come together")
     _same_length([("params", params), ("grads", grads), ("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq),
                   ("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)])
+    if any(g is None for g in grads):
+        at = [i for i, g in enumerate(grads) if g is not None]
+        params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale = (
+            ts and [ts[i] for i in at] for ts in (params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale))
     if not params:
         return
     device = params[0].device

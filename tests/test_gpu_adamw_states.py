@@ -108,3 +108,21 @@ def test_everything_written_is_reported_to_autograd(bits):
     before = [t._version for t in written]
     sc.adamw_step(p, g, m, v, 1, exp_avg_scale=ms, exp_avg_sq_scale=vs)
     assert all(t._version > n for t, n in zip(written, before)) and all(t._version == 0 for t in g)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_parameters_without_a_gradient_stay(bits):
+    # as torch.autograd.grad(..., allow_unused=True) gives them
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    p = [torch.randn(n, generator=gen, device="cuda") for n in (300, 5, 700)]
+    q = [t.clone() for t in p]
+    a, b = sc.new_adamw_state(p, bits), sc.new_adamw_state(q, bits)
+    g = [torch.randn(300, generator=gen, device="cuda"), None, torch.randn(700, generator=gen, device="cuda")]
+    sc.adamw_step(p, g, a[0], a[1], 1, exp_avg_scale=a[2], exp_avg_sq_scale=a[3])
+    some = lambda ts: ts and [ts[0], ts[2]]  # noqa: E731
+    sc.adamw_step(some(q), some(g), some(b[0]), some(b[1]), 1, exp_avg_scale=some(b[2]), exp_avg_sq_scale=some(b[3]))
+    for x, y in zip((p, *a), (q, *b)):
+        assert x is None or all(torch.equal(s, t) for s, t in zip(x, y))
+    assert not torch.equal(p[0], torch.zeros(300, device="cuda")) and not a[0][1].any()
+    assert sc.adamw_step(p, [None] * 3, a[0], a[1], 2, exp_avg_scale=a[2], exp_avg_sq_scale=a[3]) is None
+    assert all(torch.equal(s, t) for s, t in zip(p, q))
