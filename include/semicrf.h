@@ -272,11 +272,21 @@ semicrf_status semicrf_nll_backward(const semicrf_dims *dims, const double *S, c
  * each head, group norm with an activation) and what turns gradients into new
  * parameters (AdamW).  The pages have no counterpart to them.  Ownership, streams
  * and errors as above: caller-owned device memory, asynchronous, arguments checked
- * on the host before any launch.  Device findings (a length outside its range) go
- * to the status word at the start of the call's workspace; such a length is taken
- * as the nearest one in range.  A workspace serves one call at a time: calls that
- * may overlap on the GPU (two streams, two graphs) need one each.
+ * on the host before any launch.  Device findings (a length outside its range, a wait
+ * that ran out) go to the status word at the start of the call's workspace, which its
+ * owner clears before the first call (semicrf_clear_device_status), and to a word of the
+ * library on each device (semicrf_get_operators_status).  A length outside its range is
+ * taken as the nearest one in range; where a wait ran out, outputs are unspecified.  A
+ * workspace serves one call at a time: calls that may overlap on the GPU (two streams, two
+ * graphs) need one each.
  */
+
+/* Synchronise `stream` and return the first finding of linear attention or group norm on
+ * the current device since it was cleared, whatever the workspaces; clear it (asynchronous
+ * on stream).  Calls on other streams are seen once they are done. */
+semicrf_status semicrf_get_operators_status(void *stream);
+semicrf_status semicrf_clear_operators_status(void *stream);
+
 
 /* Element types. */
 #define SEMICRF_F32 0

@@ -77,6 +77,7 @@ def _need_ws(ws):
     torch = _torch()
     if not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise TypeError("ws must be a contiguous CUDA uint8 tensor (new_workspace)")
+    return ws.device
 
 
 def _same_device(ref, **others):
@@ -446,17 +447,25 @@ def logz_and_grads(x, A, D, lengths, grad_logZ=None, ckpt_interval=0, ws=None):
     return logZ, dX, dA, dD, ws
 
 
-def clear_device_status(ws):
-    _need_ws(ws)
-    with _torch().cuda.device(ws.device):
-        _lib.check(_lib.load().semicrf_clear_device_status(_ptr(ws), _stream(ws.device)), "clear_device_status")
+def clear_device_status(ws=None, device=None) -> None:
+    """Zero the workspace's device status word on the current stream; without a workspace, the
+    findings of linear_attention and group_norm on `device` (the current one)."""
+    with _torch().cuda.device(device if ws is None else _need_ws(ws)):
+        if ws is None:
+            _lib.check(_lib.load().semicrf_clear_operators_status(_stream()), "clear_device_status")
+        else:
+            _lib.check(_lib.load().semicrf_clear_device_status(_ptr(ws), _stream()), "clear_device_status")
 
 
-def device_status(ws) -> int:
-    """Synchronise the current stream and return the workspace's device status code."""
-    _need_ws(ws)
-    with _torch().cuda.device(ws.device):
-        return int(_lib.load().semicrf_get_device_status(_ptr(ws), _stream(ws.device)))
+def device_status(ws=None, device=None) -> int:
+    """Synchronise the current stream and return the workspace's device status code; without a
+    workspace, the first finding since it was cleared of any linear_attention or group_norm on
+    `device` (the current one): a length out of range, or a wait that ran out, whose outputs
+    are unspecified."""
+    with _torch().cuda.device(device if ws is None else _need_ws(ws)):
+        if ws is None:
+            return int(_lib.load().semicrf_get_operators_status(_stream()))
+        return int(_lib.load().semicrf_get_device_status(_ptr(ws), _stream()))
 
 
 def last_launch_count() -> int:

@@ -88,6 +88,8 @@ SIGNATURES = {
     "semicrf_group_norm_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
     "semicrf_adamw": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.POINTER(AdamWConfig), _P]),
     "semicrf_adamw_state_values": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32, _P]),
+    "semicrf_get_operators_status": (ctypes.c_int, [_P]),
+    "semicrf_clear_operators_status": (ctypes.c_int, [_P]),
     "semicrf_clear_device_status": (ctypes.c_int, [_P, _P]),
     "semicrf_get_device_status": (ctypes.c_int, [_P, _P]),
     "semicrf_status_string": (ctypes.c_char_p, [ctypes.c_int]),

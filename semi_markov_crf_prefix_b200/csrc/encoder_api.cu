@@ -333,4 +333,23 @@ semicrf_status semicrf_group_norm_backward(const semicrf_norm_dims *dims, const 
     return ended(e, n);
 }
 
+semicrf_status semicrf_get_operators_status(void *stream)
+{
+    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return SEMICRF_ERR_CUDA;
+    int32_t found[3] = {0, 0, 0};
+    if (la_found(found) != cudaSuccess || la_tma_found(found + 1) != cudaSuccess || norm_found(found + 2) != cudaSuccess)
+        return SEMICRF_ERR_CUDA;
+    for (int32_t f : found)
+        if (f) return static_cast<semicrf_status>(f);
+    return SEMICRF_OK;
+}
+
+semicrf_status semicrf_clear_operators_status(void *stream)
+{
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool ok = la_clear_found(st) == cudaSuccess && la_tma_clear_found(st) == cudaSuccess &&
+                    norm_clear_found(st) == cudaSuccess;
+    return ok ? SEMICRF_OK : SEMICRF_ERR_CUDA;
+}
+
 }  // extern "C"

@@ -90,6 +90,14 @@ __device__ __forceinline__ Pack<T, N> pack(const float (&f)[N])
     return p;
 }
 
+// Findings of each source's kernels on the current device, read and cleared (findings.cuh).
+cudaError_t la_found(int32_t *to);
+cudaError_t la_tma_found(int32_t *to);
+cudaError_t norm_found(int32_t *to);
+cudaError_t la_clear_found(cudaStream_t st);
+cudaError_t la_tma_clear_found(cudaStream_t st);
+cudaError_t norm_clear_found(cudaStream_t st);
+
 // ---- linear attention ----
 
 // One walk over all sequences and heads: S_p = lam S_{p-1} + c k_p v_p^T, o_p = b q_p S_p.  The forward is

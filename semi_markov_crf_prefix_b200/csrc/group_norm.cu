@@ -13,8 +13,8 @@
 // rate (22 operations a value) as to the memory's.
 #include <math.h>
 
-#include "device_util.cuh"
 #include "encoder_internal.h"
+#include "findings.cuh"
 
 namespace semicrf {
 namespace {
@@ -103,7 +103,7 @@ __device__ __forceinline__ int norm_length(const NormArgs &a, int n)
     if (!a.lengths) return a.S;
     const int L = a.lengths[n];
     if (L < 0 || L > a.S) {
-        set_status(a.status, SEMICRF_ERR_INVALID_LENGTH);
+        report(a.status, SEMICRF_ERR_INVALID_LENGTH);
         return max(0, min(L, a.S));
     }
     return L;
@@ -877,5 +877,8 @@ cudaError_t launch_norm(const NormArgs &a, int dtype, bool backward, cudaStream_
                         : norm_type<__nv_bfloat16, false>(a, vec, st, launches);
     return backward ? norm_type<__half, true>(a, vec, st, launches) : norm_type<__half, false>(a, vec, st, launches);
 }
+
+cudaError_t norm_found(int32_t *to) { return read_found(to); }
+cudaError_t norm_clear_found(cudaStream_t st) { return clear_found(st); }
 
 }  // namespace semicrf

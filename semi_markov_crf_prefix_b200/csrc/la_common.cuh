@@ -4,8 +4,8 @@
 
 #include <math.h>
 
-#include "device_util.cuh"
 #include "encoder_internal.h"
+#include "findings.cuh"
 
 namespace semicrf {
 namespace {
@@ -42,7 +42,7 @@ __device__ __forceinline__ LaSpan la_span(const LaArgs &a, const LaWalk &w, int 
     if (a.lengths) {
         L = a.lengths[s.b];
         if (L < 0 || L > a.T) {
-            if (threadIdx.x == 0) set_status(a.status, SEMICRF_ERR_INVALID_LENGTH);
+            if (threadIdx.x == 0) report(a.status, SEMICRF_ERR_INVALID_LENGTH);
             L = max(0, min(L, a.T));
         }
     }

@@ -537,7 +537,7 @@ __global__ __launch_bounds__(256, (LaCfg<T>::kBlocks)) void la_chunk_kernel(cons
         for (int i = 0; i < 16; ++i) S[i] = fmaf(S[i], hi, fmaf(S[i], lo, __uint_as_float(r[i])));
         if (!STATE_ONLY) put_pairs();
     }
-    if (!alive && tid == 0) set_status(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
+    if (!alive && tid == 0) report(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
 
     // the state behind the last position (or behind this segment)
     float *to = STATE_ONLY ? segment_at(w, args, s) : s.last && w.s_out ? w.s_out + state_at(w, args, s) : nullptr;
@@ -770,5 +770,8 @@ cudaError_t launch_la_step(const LaStepArgs &a, int dtype, cudaStream_t st, int 
     if (dtype == SEMICRF_BF16) return step_type<__nv_bfloat16>(a, st, launches);
     return step_type<__half>(a, st, launches);
 }
+
+cudaError_t la_found(int32_t *to) { return read_found(to); }
+cudaError_t la_clear_found(cudaStream_t st) { return clear_found(st); }
 
 }  // namespace semicrf

@@ -228,7 +228,7 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
         }
         if (elect_lane()) {
             tma_store_done();
-            if (!alive) set_status(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
+            if (!alive) report(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
             if (broken) {   // somebody's wait has run out: the copies under way end before the block does
 #pragma unroll
                 for (int i = 0; i < 3; ++i)
@@ -533,7 +533,7 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
                     keep(quad * 16 + (lane >> 2) + (i & 2) * 4, c0 + (i >> 2) * 8 + (lane & 3) * 2 + (i & 1), S[i]);
             }
         }
-        if (!alive && tid == 0) set_status(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
+        if (!alive && tid == 0) report(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
     }
     tc_before_sync();
     __syncthreads();
@@ -635,7 +635,7 @@ __global__ __launch_bounds__(kThreads, (StateCfg<D>::kBlocks)) void la_state_ker
             }
         }
         if (elect_lane()) {
-            if (!alive) set_status(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
+            if (!alive) report(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
             if (broken) {   // somebody's wait has run out: the copies under way end before the block does
 #pragma unroll
                 for (int i = 0; i < 3; ++i)
@@ -744,7 +744,7 @@ __global__ __launch_bounds__(kThreads, (StateCfg<D>::kBlocks)) void la_state_ker
                 for (int e = 0; e < 16; ++e) keep(row, c + e, __uint_as_float(r[e]));
             }
         }
-        if (!alive && tid == 0) set_status(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
+        if (!alive && tid == 0) report(args.status, SEMICRF_ERR_DEVICE_TIMEOUT);
     }
     tc_before_sync();
     __syncthreads();
@@ -831,5 +831,8 @@ cudaError_t launch_la_tma(const LaArgs &a, bool state_only, cudaStream_t st, int
     }
     return timed_launch(st, n, [&] { k<<<dim3(a.B * a.H * a.nseg, a.nwalk), kThreads, smem, st>>>(a, maps); });
 }
+
+cudaError_t la_tma_found(int32_t *to) { return read_found(to); }
+cudaError_t la_tma_clear_found(cudaStream_t st) { return clear_found(st); }
 
 }  // namespace semicrf

@@ -11,7 +11,10 @@ of the tensors' device.
 Layout: q, k [B,T,H,dk], v, o [B,T,H,dv] with a dense last axis and any strides
 before it; states float32 [B,H,dk,dv]; log_decay float32 [H]; x, y [N,...,C]
 contiguous; lengths int32, as everywhere in this package: what lies behind a
-sequence's end is not read, and is zero in outputs.
+sequence's end is not read, and is zero in outputs.  A length outside its range is found on
+the device: it is taken as the nearest one inside, and ``device_status()`` of this package
+returns the code, for any call until ``clear_device_status()``.  A workspace given as `ws` has
+a status word of its own, which its owner clears before the first call.
 """
 from __future__ import annotations
 
