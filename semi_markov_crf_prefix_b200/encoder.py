@@ -1,7 +1,8 @@
 """What makes emissions of long sequences: linear attention with a decay for each
 head, and group norm with an activation on channels-last rows.
 
-``linear_attention`` and ``group_norm`` are differentiable (torch.autograd); the
+``linear_attention`` and ``group_norm`` are differentiable (torch.autograd, once and in
+reverse mode; forward-mode tangents and second derivatives are refused); the
 ``*_forward`` / ``*_backward`` pairs are the library's calls, with the workspace in
 the caller's hands when given.  ``linear_attention_step`` is the form for single
 positions, with the state updated in place.  Argument marshalling only: every step
@@ -20,6 +21,7 @@ from __future__ import annotations
 
 import torch
 from torch._C import _cuda_getCurrentRawStream as _raw_stream
+from torch.autograd import forward_ad
 
 from . import _lib
 
@@ -224,6 +226,7 @@ def linear_attention(q, k, v, log_decay, lengths=None, scale=None, initial_state
                      reverse=False):
     """o [B,T,H,dv], or (o, state) with return_state; differentiable with respect to q, k, v
     and initial_state.  Arguments as for linear_attention_forward."""
+    _no_tangents((log_decay,))
     return _differentiable(LinearAttention, (q, k, v, initial_state), (q, k, v, initial_state, log_decay, lengths,
                                                                        scale, reverse, return_state),
                            lambda: _drop(linear_attention_forward(q, k, v, log_decay, lengths, scale, initial_state,
@@ -234,8 +237,16 @@ def _drop(pair, both):
     return pair if both else pair[0]
 
 
+def _no_tangents(inputs):
+    """Refuses forward-mode derivatives: the library's calls would drop the tangents without a word."""
+    if forward_ad._current_level >= 0 and any(isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None
+                                              for t in inputs):
+        raise NotImplementedError("linear attention and group norm have no forward-mode derivative")
+
+
 def _differentiable(function, inputs, args, plain):
     """function.apply where a gradient may be asked for, else the call alone."""
+    _no_tangents(inputs)
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
         return function.apply(*args)
     return plain()
@@ -244,6 +255,7 @@ def _differentiable(function, inputs, args, plain):
 def linear_attention_step(q, k, v, log_decay, state, scale=None):
     """One position: state [B,H,dk,dv] float32 becomes lam state + k v^T in place; returns
     o [B,H,dv] = scale q state.  q, k [B,H,dk], v [B,H,dv].  No gradient is recorded."""
+    _no_tangents((q, k, v, log_decay, state))
     device, kind, (B, H, dk), dv, qs, ks, vs = _attention(q, k, v, log_decay, 3)
     _want(state, "state", torch.float32, (B, H, dk, dv), device)
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or state.requires_grad):

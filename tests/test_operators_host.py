@@ -3,7 +3,10 @@ refused, and what needs no device."""
 import ctypes
 
 import pytest
+import torch
+import torch.autograd.forward_ad as forward_ad
 
+import semi_markov_crf_prefix_b200 as sc
 from semi_markov_crf_prefix_b200 import _lib
 from semi_markov_crf_prefix_b200 import build as build_mod
 
@@ -51,3 +54,24 @@ def test_overlapping_tensors_are_refused(lib):
                 if i != 1:
                     setattr(two[1], Entry._fields_[i][0], good[i] + 4)     # another tensor's own kind
                     assert lib.semicrf_adamw(two, 2, ctypes.byref(cfg), None) == ARG, i
+
+
+@pytest.mark.parametrize("which", range(5))
+def test_forward_mode_tangents_are_refused(lib, which):
+    # before anything else is looked at, so that no device is needed
+    args = [torch.ones(1, 3, 2, 8) for _ in range(3)] + [torch.zeros(2), torch.zeros(1, 2, 8, 8)]
+    norm = [torch.ones(2, 3, 8), torch.ones(8), torch.zeros(8)]
+    with forward_ad.dual_level():
+        dual = lambda t: forward_ad.make_dual(t, torch.ones_like(t))  # noqa: E731
+        given = [dual(t) if i == which else t for i, t in enumerate(args)]
+        with pytest.raises(NotImplementedError):
+            sc.linear_attention(*given[:4], initial_state=given[4])
+        with pytest.raises(NotImplementedError):
+            sc.linear_attention_step(*[t[:, 0] for t in given[:3]], *given[3:])
+        if which < 3:
+            with pytest.raises(NotImplementedError):
+                sc.group_norm(*[dual(t) if i == which else t for i, t in enumerate(norm[:1])] if which == 0 else norm[:1], 2,
+                              *[dual(t) if i + 1 == which else t for i, t in enumerate(norm[1:])])
+        # a level without tangents is no reason
+        with pytest.raises(TypeError):
+            sc.linear_attention(*args[:4])
