@@ -90,6 +90,11 @@ def _operand(t, name, q, shape):
     return strides
 
 
+def _constant(log_decay):
+    if isinstance(log_decay, torch.Tensor) and log_decay.requires_grad and torch.is_grad_enabled():
+        raise ValueError("log_decay is a constant: it has no gradient (detach it, or call under torch.no_grad())")
+
+
 def _attention(q, k, v, log_decay, axes):
     """(device, type, shape of q, width of v, strides of q, k and v) of checked operands."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
@@ -105,8 +110,7 @@ def _attention(q, k, v, log_decay, axes):
     ks = _operand(k, "k", q, shape)
     dv = v.shape[-1] if isinstance(v, torch.Tensor) and v.dim() else 0
     vs = _operand(v, "v", q, (*shape[:-1], dv))
-    if log_decay.requires_grad:
-        raise ValueError("log_decay is a constant: it has no gradient")
+    _constant(log_decay)
     _want(log_decay, "log_decay", torch.float32, shape[-2:-1], device)
     return device, kind, shape, dv, qs, ks, vs
 
@@ -227,6 +231,7 @@ def linear_attention(q, k, v, log_decay, lengths=None, scale=None, initial_state
     """o [B,T,H,dv], or (o, state) with return_state; differentiable with respect to q, k, v
     and initial_state.  Arguments as for linear_attention_forward."""
     _no_tangents((log_decay,))
+    _constant(log_decay)
     return _differentiable(LinearAttention, (q, k, v, initial_state), (q, k, v, initial_state, log_decay, lengths,
                                                                        scale, reverse, return_state),
                            lambda: _drop(linear_attention_forward(q, k, v, log_decay, lengths, scale, initial_state,
