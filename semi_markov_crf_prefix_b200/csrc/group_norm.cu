@@ -435,12 +435,17 @@ __global__ __launch_bounds__(512) void norm_params_kernel(const double *part, in
 
 // ---- long rows: two passes over the data ----
 //
-// Pass 1: per-channel sums of a strip of positions, part[n][strip][2][C] in float64
-// (forward: x and x^2; backward: dz xh and dz).  A thread sums a strip's values of a
-// channel, kRun at most, in float32 about the first of them, which no mean can spoil,
-// and takes the two sums about zero to float64.  Then the groups' statistics, then pass 2
-// writes y or dx, strips in the opposite order: the ones that pass 1 read last are
-// still in the L2 cache.
+// Pass 1: two numbers for each channel of a strip of positions, part[n][strip][2][C] in
+// float64: forward the mean and the sum of squares about it, backward the sums of dz xh and
+// dz.  A thread takes a strip's values of a channel, kRun at most, in float32 less the mean
+// of its first eight (so that a mean far from zero costs no bits), eight at a time: the sums
+// s of their distances d from the mean m of the n before them and t of the squares,
+//   m += s / (n + 8),   M2 += t - s^2 / (n + 8),
+// where at least half of t stays, whatever the values are.  (Sums about the first value
+// alone lost 2^-13 of the variance where that one was an outlier.)  Means and squares of row
+// lanes, strips and channels are joined about a common value in float64.  Then
+// the groups' statistics, then pass 2 writes y or dx, strips in the opposite order: the
+// ones that pass 1 read last are still in the L2 cache.
 constexpr int kLongThreads = 256, kRun = 128;
 
 struct LongShape {
@@ -463,26 +468,51 @@ __global__ __launch_bounds__(kLongThreads, 3) void norm_sums_kernel(const __grid
     if (mine && s0 + r < s1) {
         const T *px = static_cast<const T *>(a.x) + base, *pd = static_cast<const T *>(a.dy) + base;
         if constexpr (!BWD) {
-            auto add = [&](const Pack<T, VEC> &x) {
+            constexpr int U = 8;   // loads in flight
+            // the first m of x to the mean p (less about) and the squares q of the cnt before them
+            auto add = [&](const Pack<T, VEC> (&x)[U], auto whole, int m) {
                 float f[VEC];
-                unpack(x, f);
+                if (cnt == 0) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (whole.value || u < m) {
+                            unpack(x[u], f);
+#pragma unroll
+                            for (int e = 0; e < VEC; ++e) about[e] += f[e];
+                        }
+                    const float inv = 1.f / (float)m;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) about[e] *= inv;
+                }
+                float sum[VEC], sq[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) sum[e] = sq[e] = 0.f;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (whole.value || u < m) {
+                        unpack(x[u], f);
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) {
+                            const float d = f[e] - about[e] - p[e];
+                            sum[e] += d;
+                            sq[e] = fmaf(d, d, sq[e]);
+                        }
+                    }
+                const float inv = 1.f / (float)(cnt + m);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    const float d = f[e] - about[e];
-                    p[e] += d;
-                    q[e] = fmaf(d, d, q[e]);
+                    p[e] = fmaf(sum[e], inv, p[e]);
+                    q[e] += fmaf(-sum[e], sum[e] * inv, sq[e]);
                 }
+                cnt += m;
             };
-            constexpr int U = 8;   // loads in flight
             int s = s0 + r;
-            for (; s + (U - 1) * sh.R < s1; s += U * sh.R, cnt += U) {
+            for (; s + (U - 1) * sh.R < s1; s += U * sh.R) {
                 Pack<T, VEC> x[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     x[u] = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s + u * sh.R) * a.C);
-                if (cnt == 0) unpack(x[0], about);
-#pragma unroll
-                for (int u = 0; u < U; ++u) add(x[u]);
+                add(x, Int<1>(), U);
             }
             if (s < s1) {   // the strip's last rows, together as well
                 Pack<T, VEC> x[U];
@@ -490,13 +520,7 @@ __global__ __launch_bounds__(kLongThreads, 3) void norm_sums_kernel(const __grid
                 for (int u = 0; u < U - 1; ++u)
                     if (s + u * sh.R < s1)
                         x[u] = *reinterpret_cast<const Pack<T, VEC> *>(px + (long long)(s + u * sh.R) * a.C);
-                if (cnt == 0) unpack(x[0], about);
-#pragma unroll
-                for (int u = 0; u < U - 1; ++u)
-                    if (s + u * sh.R < s1) {
-                        add(x[u]);
-                        ++cnt;
-                    }
+                add(x, Int<0>(), (s1 - s + sh.R - 1) / sh.R);
             }
         } else {
             float wt[VEC], bs[VEC];
@@ -541,16 +565,29 @@ __global__ __launch_bounds__(kLongThreads, 3) void norm_sums_kernel(const __grid
     for (int e = 0; e < VEC; ++e) {
         __syncthreads();
         if (r < sh.R) {
-            const double m = about[e], dp = p[e];
-            dsm[tid] = BWD ? dp : dp + cnt * m;
-            dsm[kLongThreads + tid] = BWD ? (double)q[e] : (double)q[e] + m * (2.0 * dp + cnt * m);
+            dsm[tid] = (double)about[e] + (double)p[e];
+            dsm[kLongThreads + tid] = (double)q[e];
         }
         __syncthreads();
         if (r == 0 && mine) {
             double x = 0.0, y = 0.0;
-            for (int j = tid; j < sh.R * cols; j += cols) {
-                x += dsm[j];
-                y += dsm[kLongThreads + j];
+            if constexpr (BWD) {
+                for (int j = tid; j < sh.R * cols; j += cols) {
+                    x += dsm[j];
+                    y += dsm[kLongThreads + j];
+                }
+            } else if (s0 < s1) {
+                // row lane j took the strip's rows j, j + R, ..: about the first lane's mean
+                const double first = dsm[tid];
+                const int each = (s1 - s0) / sh.R, more = (s1 - s0) % sh.R;
+                for (int j = 0; j < sh.R && s0 + j < s1; ++j) {
+                    const double d = dsm[j * cols + tid] - first, all = (double)(each + (j < more)) * d;
+                    x += all;
+                    y += fma(all, d, dsm[kLongThreads + j * cols + tid]);
+                }
+                const double m = x / (double)(s1 - s0);
+                y -= x * m;
+                x = first + m;
             }
             out[e] = x;
             out[a.C + e] = y;
@@ -562,22 +599,34 @@ __global__ __launch_bounds__(kLongThreads, 3) void norm_sums_kernel(const __grid
 // [N,G,2]) and row block n's share of dw and db (to total [N][2][C]).  Thread (x, y): channel
 // x of the group (and x + X, ..), strand y of the strips.
 template <typename T, bool BWD>
-__global__ __launch_bounds__(256) void norm_group_kernel(const __grid_constant__ NormArgs a, int strips, float *gsum,
-                                                         double *total, int X)
+__global__ __launch_bounds__(256) void norm_group_kernel(const __grid_constant__ NormArgs a, int strips, int rows,
+                                                         float *gsum, double *total, int X)
 {
     const int n = blockIdx.x / a.G, g = blockIdx.x % a.G, Cg = a.C / a.G, Y = 256 / X;
     const int x = threadIdx.x % X, y = threadIdx.x / X;
     const double *part = a.part + (long long)n * strips * 2 * a.C + g * Cg;
     __shared__ double sa[256], sb[256];
     double A = 0.0, B = 0.0;   // the group's
+    // forward: sums about the first strip's mean of the first channel
+    const int L = norm_length(a, n);
+    const double about = BWD ? 0.0 : part[0];
     for (int c0 = 0; c0 < Cg; c0 += X) {
         const int c = c0 + x;
         double p = 0.0, q = 0.0;
         if (c < Cg) {
 #pragma unroll 4
             for (int i = y; i < strips; i += Y) {
-                p += part[(long long)i * 2 * a.C + c];
-                q += part[(long long)i * 2 * a.C + a.C + c];
+                const double u = part[(long long)i * 2 * a.C + c], v = part[(long long)i * 2 * a.C + a.C + c];
+                if constexpr (BWD) {
+                    p += u;
+                    q += v;
+                } else {
+                    const long long have = min((long long)rows, (long long)L - (long long)i * rows);
+                    if (have <= 0) break;
+                    const double d = u - about, all = (double)have * d;
+                    p += all;
+                    q += fma(all, d, v);
+                }
             }
         }
         if (!BWD) {
@@ -618,15 +667,15 @@ __global__ __launch_bounds__(256) void norm_group_kernel(const __grid_constant__
             A += sa[j];
             B += sb[j];
         }
-        const double cnt = fmax((double)norm_length(a, n) * Cg, 1.0);
+        const double cnt = fmax((double)L * Cg, 1.0);
         float *o = (BWD ? gsum : a.stats) + 2 * (long long)blockIdx.x;
         if (BWD) {
             o[0] = (float)(B / cnt);   // mean of w dz
             o[1] = (float)(A / cnt);   // mean of w dz xh
         } else {
-            const double m = A / cnt;
-            o[0] = (float)m;
-            o[1] = (float)(1.0 / sqrt(fmax(B / cnt - m * m, 0.0) + (double)a.eps));
+            const double m = A / cnt, variance = B / cnt - m * m;
+            o[0] = (float)(about + m);
+            o[1] = (float)(1.0 / sqrt(fmax(variance, 0.0) + (double)a.eps));
         }
     }
 }
@@ -813,7 +862,7 @@ cudaError_t norm_go(NormArgs a, cudaStream_t st, int *n)
             norm_sums_kernel<T, VEC, BWD><<<grid, kLongThreads, 2 * kLongThreads * sizeof(double), st>>>(a, sh);
         });
         if (e != cudaSuccess) return e;
-        e = timed_launch(st, n, [&] { norm_group_kernel<T, BWD><<<a.N * a.G, 256, 0, st>>>(a, sh.strips, gsum, total, X); });
+        e = timed_launch(st, n, [&] { norm_group_kernel<T, BWD><<<a.N * a.G, 256, 0, st>>>(a, sh.strips, sh.rows, gsum, total, X); });
         if (e != cudaSuccess) return e;
         e = timed_launch(st, n, [&] { norm_apply_kernel<T, VEC, BWD><<<grid, kLongThreads, 0, st>>>(a, sh, gsum); });
         if (e != cudaSuccess) return e;

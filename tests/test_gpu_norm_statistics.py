@@ -1,0 +1,60 @@
+"""The statistics of group norm on values that are hard for them.
+
+Where rows do not fit a thread block's registers, means and squares about them come from
+runs of at most 128 values in float32, eight at a time: of a batch's squares, about the mean
+of the values before it, at least half stays in the sum, so its ten roundings of 2^-24 count
+twice, and sixteen batches are added: 36 roundings, below 2^-18.8 of the sum of squares;
+behind that float64.  So 1/std is right to 2^-19.8 and its rounding, and a mean to 2^-20 of a
+run's range.  y takes four roundings of 2^-24 more.
+"""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+import torch  # noqa: E402
+
+import semi_markov_crf_prefix_b200 as sc  # noqa: E402
+
+
+def rnd(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+def exact(x, G, w, b, eps=1e-5):
+    N, S, C = x.shape
+    u = x.double().view(N, S, G, C // G)
+    mean = u.mean((1, 3), keepdim=True)
+    d = u - mean
+    rstd = torch.rsqrt((d * d).mean((1, 3), keepdim=True) + eps)
+    xh = (d * rstd).view(N, S, C)
+    return xh * w.double() + b.double(), xh, mean.view(N, G), rstd.view(N, G)
+
+
+# (the last one: 128 values a run)
+@pytest.mark.parametrize("shape,groups", [((2, 20000, 32), 4), ((1, 5000, 64), 64), ((3, 9000, 6), 1), ((1, 3001, 20), 4),
+                                          ((1184, 128, 520), 2)])
+@pytest.mark.parametrize("outlier", [10.0, -1e3, 1e5])
+@pytest.mark.parametrize("rows", [1, 4, 8])
+def test_outliers_at_the_start(shape, groups, outlier, rows):
+    x, w, b = rnd(1, *shape), 1 + 0.2 * rnd(2, shape[2]), 0.2 * rnd(3, shape[2])
+    x[:, :rows] = outlier
+    y, stats = sc.group_norm_forward(x, groups, w, b)
+    want, xh, mean, rstd = exact(x, groups, w, b)
+    assert torch.all((stats[..., 1].double() / rstd - 1).abs() <= 2.0 ** -19.8 + 2.0 ** -23)
+    # a run's range is |outlier| + 10 and at most 128 of S values are in it
+    run = 2.0 ** -20 * (abs(outlier) + 10) * min(1.0, 128 * max(1, 256 // shape[2]) / shape[1])
+    assert torch.all((stats[..., 0].double() - mean).abs() <= run + 2.0 ** -23 * mean.abs())
+    off = (run * rstd.amax() + (2.0 ** -19.8 + 2.0 ** -23) * xh.abs() + 4 * 2.0 ** -24 * xh.abs()) * w.double().abs() + 2.0 ** -24 * want.abs()
+    off = off + 2.0 ** -23 * (mean.abs() * rstd).amax() * w.double().abs()
+    assert torch.all((y.double() - want).abs() <= off)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("shape,groups", [((2, 20000, 32), 4), ((1, 7001, 33), 3)])
+def test_deviations_of_shifted_values(shape, groups, dtype):
+    # a mean of 1e6 deviations
+    x = (rnd(4, *shape) + (1e6 if dtype == torch.float32 else 100.0)).to(dtype)
+    _, stats = sc.group_norm_forward(x, groups)
+    _, _, mean, rstd = exact(x, groups, torch.ones(shape[2], device="cuda"), torch.zeros(shape[2], device="cuda"))
+    assert torch.all((stats[..., 1].double() / rstd - 1).abs() <= 2.0 ** -19.8 + 2.0 ** -23)
+    assert torch.all((stats[..., 0].double() / mean - 1).abs() <= 2.0 ** -23)
