@@ -675,7 +675,7 @@ __global__ __launch_bounds__(256) void norm_group_kernel(const __grid_constant__
         } else {
             const double m = A / cnt, variance = B / cnt - m * m;
             o[0] = (float)(about + m);
-            o[1] = (float)(1.0 / sqrt(fmax(variance, 0.0) + (double)a.eps));
+            o[1] = (float)(1.0 / sqrt((variance < 0.0 ? 0.0 : variance) + (double)a.eps));   // (NaN stays NaN)
         }
     }
 }

@@ -58,3 +58,17 @@ def test_deviations_of_shifted_values(shape, groups, dtype):
     _, _, mean, rstd = exact(x, groups, torch.ones(shape[2], device="cuda"), torch.zeros(shape[2], device="cuda"))
     assert torch.all((stats[..., 1].double() / rstd - 1).abs() <= 2.0 ** -19.8 + 2.0 ** -23)
     assert torch.all((stats[..., 0].double() / mean - 1).abs() <= 2.0 ** -23)
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("shape,groups", [((2, 9000, 16), 4), ((2, 30, 16), 4), ((2, 1, 16), 4)])
+def test_values_that_are_not_finite(shape, groups, value):
+    # the statistics of their row block and group are NaN, and so is all of it
+    x = rnd(5, *shape)
+    for at in (0, shape[1] // 2, shape[1] - 1):
+        t = x.clone()
+        t[1, at, 5] = value
+        y = sc.group_norm(t, groups)
+        assert torch.isnan(y[1, :, 4:8]).all()
+        y[1, :, 4:8] = 0
+        assert torch.isfinite(y).all()
