@@ -114,9 +114,11 @@ __device__ __forceinline__ int norm_length(const NormArgs &a, int n)
 // Thread (r, col) holds U vectors of VEC channels: rows rl, rl + RL, ... of row block n.
 // NB row blocks lie side by side in a thread block, RL lanes of rows in each.  One read of
 // x (and dy), the statistics from registers in two exact passes (mean, then squares about
-// it), one write.
+// it), one write.  Rows of more vectors than threads are cut into slices of whole groups
+// (blockIdx.y), which have nothing to do with one another.
 struct RegShape {
-    int CV, RL, NB, W;   // vectors a row; row lanes a block; row blocks a thread block; lanes that sum one group
+    int CV, G, slices;   // vectors and groups of a slice's row (the last slice may have fewer); slices
+    int RL, NB, W;       // row lanes a block; row blocks a thread block; lanes that sum one group
 };
 
 constexpr int kRegThreads = 512;
@@ -148,10 +150,10 @@ template <typename T, int VEC, int U, bool BWD>
 __global__ __launch_bounds__(kRegThreads, U == 1 ? (BWD ? 2 : 3) : 1) void norm_reg_kernel(const __grid_constant__ NormArgs a, const RegShape sh)
 {
     extern __shared__ float shm[];
-    float *red = shm, *red2 = red + kRegThreads, *mean = red2 + kRegThreads, *aux = mean + sh.NB * a.G;
+    float *red = shm, *red2 = red + kRegThreads, *mean = red2 + kRegThreads, *aux = mean + sh.NB * sh.G;
     const int tid = threadIdx.x, col = tid % sh.CV, r = tid / sh.CV, nb = r / sh.RL, rl = r % sh.RL;
-    const bool mine = nb < sh.NB;
-    const int Cg = a.C / a.G, CgV = Cg / VEC, c0 = col * VEC, g = c0 / Cg;
+    const int Cg = a.C / a.G, CgV = Cg / VEC, c0 = (blockIdx.y * sh.CV + col) * VEC, g = col / CgV;
+    const bool mine = nb < sh.NB && c0 < a.C;
     float wt[VEC], bs[VEC], dw[VEC], db[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
@@ -163,9 +165,9 @@ __global__ __launch_bounds__(kRegThreads, U == 1 ? (BWD ? 2 : 3) : 1) void norm_
     auto total = [&](float share, float *red, float *out) {
         red[tid] = share;
         __syncthreads();
-        group_sums(red, out, sh, a.G, CgV);
+        group_sums(red, out, sh, sh.G, CgV);
         __syncthreads();
-        return mine ? out[nb * a.G + g] : 0.f;
+        return mine ? out[nb * sh.G + g] : 0.f;
     };
     auto fetch = [&](int n0, Pack<T, VEC>(&x)[U], Pack<T, VEC>(&dy)[BWD ? U : 1]) {
         const int n = n0 + nb;
@@ -211,7 +213,7 @@ __global__ __launch_bounds__(kRegThreads, U == 1 ? (BWD ? 2 : 3) : 1) void norm_
                 }
             rs = rsqrtf(fmaf(total(sum, red2, aux), inv, a.eps));
             if (on && a.stats && rl == 0 && c0 % Cg == 0) {
-                float *st = a.stats + 2 * ((long long)n * a.G + g);
+                float *st = a.stats + 2 * ((long long)n * a.G + blockIdx.y * sh.G + g);
                 st[0] = mu;
                 st[1] = rs;
             }
@@ -229,7 +231,7 @@ __global__ __launch_bounds__(kRegThreads, U == 1 ? (BWD ? 2 : 3) : 1) void norm_
                 }
             });
         } else {
-            const float *st = a.stats + 2 * ((long long)(on ? n : 0) * a.G + (mine ? g : 0));
+            const float *st = a.stats + 2 * ((long long)(on ? n : 0) * a.G + (mine ? blockIdx.y * sh.G + g : 0));
             mu = st[0];
             rs = st[1];
             float s1 = 0.f, s2 = 0.f;
@@ -277,7 +279,7 @@ __global__ __launch_bounds__(kRegThreads, U == 1 ? (BWD ? 2 : 3) : 1) void norm_
             acc[tid] = mine ? dw[e] : 0.f;
             acc[kRegThreads + tid] = mine ? db[e] : 0.f;
             __syncthreads();
-            if (r == 0) {
+            if (r == 0 && mine) {
                 double sw = 0.0, sb = 0.0;
                 for (int j = col; j < sh.NB * sh.RL * sh.CV; j += sh.CV) {
                     sw += (double)acc[j];
@@ -406,7 +408,9 @@ __global__ __launch_bounds__(256) void norm_row_kernel(const __grid_constant__ N
 }
 
 // dw[c], db[c] from P rows of partial sums [P][2][C]: 8 channels and 64 strands of rows a block.
-__global__ __launch_bounds__(512) void norm_params_kernel(const double *part, int P, int C, float *dw, float *db)
+// Row blocks that come in pieces: sums so far in acc [2][C], dw and db with the last piece.
+__global__ __launch_bounds__(512) void norm_params_kernel(const double *part, int P, int C, float *dw, float *db,
+                                                          double *acc, bool first, bool last)
 {
     __shared__ double sh[2][64][8];
     const int c = blockIdx.x * 8 + threadIdx.x, j = threadIdx.y;
@@ -428,8 +432,15 @@ __global__ __launch_bounds__(512) void norm_params_kernel(const double *part, in
         }
     }
     if (j == 0 && c < C) {
-        if (dw) dw[c] = (float)sh[0][0][threadIdx.x];
-        if (db) db[c] = (float)sh[1][0][threadIdx.x];
+        w = sh[0][0][threadIdx.x] + (first ? 0.0 : acc[c]);
+        b = sh[1][0][threadIdx.x] + (first ? 0.0 : acc[C + c]);
+        if (!last) {
+            acc[c] = w;
+            acc[C + c] = b;
+        } else {
+            if (dw) dw[c] = (float)w;
+            if (db) db[c] = (float)b;
+        }
     }
 }
 
@@ -561,6 +572,15 @@ __global__ __launch_bounds__(kLongThreads, 3) void norm_sums_kernel(const __grid
         }
     }
     double *out = a.part + ((long long)n * sh.strips + strip) * 2 * a.C + c0;
+    if (sh.R == 1) {   // nothing to join
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (mine) {
+                out[e] = (double)about[e] + (double)p[e];
+                out[a.C + e] = (double)q[e];
+            }
+        return;
+    }
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
         __syncthreads();
@@ -772,8 +792,12 @@ int narrower(int vec, int dtype) { return vec == 1 ? 0 : vec > 2 && dtype != SEM
 // Registers hold a row block where its rows take at most 32 values a thread.
 bool reg_shape(int S, int C, int G, int vec, RegShape *sh)
 {
-    sh->CV = C / vec;
-    if (sh->CV > kRegThreads) return false;
+    const int CgV = C / G / vec;
+    if (CgV > kRegThreads) return false;
+    sh->slices = (G + kRegThreads / CgV - 1) / (kRegThreads / CgV);
+    sh->G = (G + sh->slices - 1) / sh->slices;
+    sh->slices = (G + sh->G - 1) / sh->G;
+    sh->CV = sh->G * CgV;
     const int R = kRegThreads / sh->CV;
     sh->RL = R < S ? R : S;
     sh->NB = R / sh->RL;
@@ -800,10 +824,37 @@ LongShape long_shape(int N, int S, int C, int vec)
     return sh;
 }
 
+// The long form's scratch is 16 bytes for each channel, strip and row block (and as much again
+// for a row block's dw and db), which for many short row blocks of wide rows is several
+// times x.  Row blocks are taken in pieces whose scratch stays within 64 MB, half of the L2
+// cache: a piece has 2048 thread blocks at least, so the GPU stays full.
+struct LongPlan {
+    LongShape sh;
+    int rows;                        // row blocks of a piece
+    size_t total, acc, gsum, bytes;  // offsets behind the strips' sums, and the whole
+};
+
+constexpr size_t kLongScratch = (size_t)64 << 20;
+
+LongPlan long_plan(int N, int S, int C, int G, int vec, bool backward)
+{
+    LongPlan p;
+    p.sh = long_shape(N, S, C, vec);
+    const size_t strips = (size_t)p.sh.strips * 2 * C * sizeof(double), row = 2 * (size_t)C * sizeof(double),
+                 group = 2 * (size_t)G * sizeof(float), each = strips + (backward ? row + group : 0);
+    const size_t most = kLongScratch / each;
+    p.rows = most < 1 ? 1 : most < (size_t)N ? (int)most : N;
+    p.total = p.rows * strips;
+    p.acc = p.total + (backward ? p.rows * row : 0);
+    p.gsum = p.acc + (backward ? row : 0);
+    p.bytes = p.gsum + (backward ? p.rows * group : 0);
+    return p;
+}
+
 int reg_blocks(int N, const RegShape &sh)
 {
-    const int blocks = (N + sh.NB - 1) / sh.NB, most = 6 * device_sm_count();
-    return blocks < most ? blocks : most;
+    const int blocks = (N + sh.NB - 1) / sh.NB, most = 6 * device_sm_count() / sh.slices;
+    return blocks < most ? blocks : most > 1 ? most : 1;
 }
 
 // Lanes of a group in norm_row_kernel, 0 where it does not apply.
@@ -843,35 +894,55 @@ cudaError_t norm_go(NormArgs a, cudaStream_t st, int *n)
         prows = blocks;
     } else if (reg_shape(a.S, a.C, a.G, VEC, &rsh)) {
         const int blocks = reg_blocks(a.N, rsh);
-        const size_t smem = (2 * kRegThreads + 2 * (size_t)rsh.NB * a.G) * sizeof(float);
+        const dim3 grid(blocks, rsh.slices);
+        const size_t smem = (2 * kRegThreads + 2 * (size_t)rsh.NB * rsh.G) * sizeof(float);
         e = timed_launch(st, n, [&] {
             if ((a.S + rsh.RL - 1) / rsh.RL == 1)
-                norm_reg_kernel<T, VEC, 1, BWD><<<blocks, kRegThreads, smem, st>>>(a, rsh);
+                norm_reg_kernel<T, VEC, 1, BWD><<<grid, kRegThreads, smem, st>>>(a, rsh);
             else
-                norm_reg_kernel<T, VEC, 32 / VEC, BWD><<<blocks, kRegThreads, smem, st>>>(a, rsh);
+                norm_reg_kernel<T, VEC, 32 / VEC, BWD><<<grid, kRegThreads, smem, st>>>(a, rsh);
         });
         if (e != cudaSuccess) return e;
         prows = blocks;
     } else {
-        const LongShape sh = long_shape(a.N, a.S, a.C, VEC);
-        const dim3 grid((unsigned)(a.N * sh.strips), sh.tiles);
-        double *total = a.part + (size_t)a.N * sh.strips * 2 * a.C;
-        float *gsum = reinterpret_cast<float *>(total + (BWD ? (size_t)a.N * 2 * a.C : 0));
+        const LongPlan p = long_plan(a.N, a.S, a.C, a.G, VEC, BWD);
+        const LongShape &sh = p.sh;
+        unsigned char *scratch = reinterpret_cast<unsigned char *>(a.part);
+        double *total = reinterpret_cast<double *>(scratch + p.total), *acc = reinterpret_cast<double *>(scratch + p.acc);
+        float *gsum = reinterpret_cast<float *>(scratch + p.gsum);
         const int X = pow2_at_least(a.C / a.G, 256);
-        e = timed_launch(st, n, [&] {
-            norm_sums_kernel<T, VEC, BWD><<<grid, kLongThreads, 2 * kLongThreads * sizeof(double), st>>>(a, sh);
-        });
-        if (e != cudaSuccess) return e;
-        e = timed_launch(st, n, [&] { norm_group_kernel<T, BWD><<<a.N * a.G, 256, 0, st>>>(a, sh.strips, sh.rows, gsum, total, X); });
-        if (e != cudaSuccess) return e;
-        e = timed_launch(st, n, [&] { norm_apply_kernel<T, VEC, BWD><<<grid, kLongThreads, 0, st>>>(a, sh, gsum); });
-        if (e != cudaSuccess) return e;
-        prows = a.N;
-        a.part = total;
+        for (int n0 = 0; n0 < a.N; n0 += p.rows) {
+            NormArgs b = a;
+            b.N = a.N - n0 < p.rows ? a.N - n0 : p.rows;
+            const size_t at = (size_t)n0 * a.S * a.C;
+            b.x = static_cast<const T *>(a.x) + at;
+            if (BWD) b.dy = static_cast<const T *>(a.dy) + at;
+            b.y = static_cast<T *>(a.y) + at;
+            b.stats = a.stats + (size_t)n0 * a.G * 2;
+            if (a.lengths) b.lengths = a.lengths + n0;
+            const dim3 grid((unsigned)(b.N * sh.strips), sh.tiles);
+            e = timed_launch(st, n, [&] {
+                norm_sums_kernel<T, VEC, BWD><<<grid, kLongThreads, 2 * kLongThreads * sizeof(double), st>>>(b, sh);
+            });
+            if (e != cudaSuccess) return e;
+            e = timed_launch(st, n, [&] {
+                norm_group_kernel<T, BWD><<<b.N * a.G, 256, 0, st>>>(b, sh.strips, sh.rows, gsum, total, X);
+            });
+            if (e != cudaSuccess) return e;
+            e = timed_launch(st, n, [&] { norm_apply_kernel<T, VEC, BWD><<<grid, kLongThreads, 0, st>>>(b, sh, gsum); });
+            if (e != cudaSuccess) return e;
+            if (!BWD || (!a.dw && !a.db)) continue;
+            e = timed_launch(st, n, [&] {
+                norm_params_kernel<<<(a.C + 7) / 8, dim3(8, 64), 0, st>>>(total, b.N, a.C, a.dw, a.db, acc, n0 == 0,
+                                                                        n0 + b.N == a.N);
+            });
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
     }
     if (!BWD || (!a.dw && !a.db)) return cudaSuccess;
     return timed_launch(st, n, [&] {
-        norm_params_kernel<<<(a.C + 7) / 8, dim3(8, 64), 0, st>>>(a.part, prows, a.C, a.dw, a.db);
+        norm_params_kernel<<<(a.C + 7) / 8, dim3(8, 64), 0, st>>>(a.part, prows, a.C, a.dw, a.db, nullptr, true, true);
     });
 }
 
@@ -901,9 +972,7 @@ size_t norm_scratch(int N, int S, int C, int G, int dtype, bool backward)
         } else if (reg_shape(S, C, G, vec, &rsh)) {
             n = backward ? (size_t)reg_blocks(N, rsh) * 2 * C * sizeof(double) : 0;
         } else {
-            const LongShape sh = long_shape(N, S, C, vec);
-            n = (size_t)N * sh.strips * 2 * C * sizeof(double) +
-                (backward ? (size_t)N * 2 * C * sizeof(double) + (size_t)N * G * 2 * sizeof(float) : 0);
+            n = long_plan(N, S, C, G, vec, backward).bytes;
         }
         if (n > most) most = n;
     }

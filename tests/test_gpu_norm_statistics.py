@@ -14,6 +14,7 @@ pytestmark = pytest.mark.gpu
 import torch  # noqa: E402
 
 import semi_markov_crf_prefix_b200 as sc  # noqa: E402
+from test_gpu_norm import check  # noqa: E402
 
 
 def rnd(seed, *shape):
@@ -72,3 +73,26 @@ def test_values_that_are_not_finite(shape, groups, value):
         assert torch.isnan(y[1, :, 4:8]).all()
         y[1, :, 4:8] = 0
         assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("shape,groups", [((9001, 1, 520), 8), ((9000, 2, 1030), 2), ((300, 3, 40000), 4), ((1000, 2, 8200), 1),
+                                          ((700, 1, 8001), 9), ((90, 30, 2400), 400)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_many_wide_row_blocks(shape, groups, dtype, ragged):
+    # rows in slices of groups, and more row blocks than one piece of scratch holds; against 64
+    # bits, and some of them alone
+    N, S, C = shape
+    x, w, b, dy = rnd(6, *shape).add_(0.3).to(dtype), 1 + 0.2 * rnd(7, C), 0.2 * rnd(8, C), rnd(9, *shape).to(dtype)
+    lengths = torch.arange(N, device="cuda", dtype=torch.int32).remainder_(S + 1) if ragged else None
+    check(x, groups, w, b, lengths=lengths, kind="silu", dy=dy)
+    y, stats = sc.group_norm_forward(x, groups, w, b, lengths=lengths, activation="silu")
+    dx, dw, db = sc.group_norm_backward(dy, x, stats, groups, w, b, lengths=lengths, activation="silu")
+    for at in (slice(0, 100), slice(N // 2 - 7, N // 2 + 93), slice(N - 100, N)):
+        some = None if lengths is None else lengths[at].clone()
+        t, st = sc.group_norm_forward(x[at].clone(), groups, w, b, lengths=some, activation="silu")
+        assert torch.all((t.double() - y[at].double()).abs() <= 2.0 ** -7 * t.double().abs() + 1e-5)
+        u, _, _ = sc.group_norm_backward(dy[at].clone(), x[at].clone(), st, groups, w, b, lengths=some, activation="silu")
+        assert torch.all((u.double() - dx[at].double()).abs() <= 2.0 ** -7 * u.double().abs() + 1e-5 * u.abs().max())
+    again = sc.group_norm_backward(dy, x, stats, groups, w, b, lengths=lengths, activation="silu")
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw) and torch.equal(again[2], db)

@@ -75,3 +75,13 @@ def test_forward_mode_tangents_are_refused(lib, which):
         # a level without tangents is no reason
         with pytest.raises(TypeError):
             sc.linear_attention(*args[:4])
+
+
+@pytest.mark.parametrize("N,S,C,G", [(64_000, 1, 520, 8), (64_000, 1, 8192, 8), (1 << 20, 1, 8192, 8), (1 << 20, 4, 1000, 8),
+                                     (1 << 30, 1, 8, 1), (3, 1 << 30, 513, 1)])
+def test_workspace_of_many_row_blocks_stays_small(lib, N, S, C, G):
+    # (sizes of calls that nobody makes are still numbers)
+    for dtype in (_lib.F32, _lib.BF16):
+        for backward in (0, 1):
+            need = lib.semicrf_group_norm_workspace_bytes(_lib.NORM_DIMS.pack(N, S, C, G, dtype, _lib.F32, 0, 1e-5), backward)
+            assert 0 < need <= max(72 << 20, N * S * C // 8)
