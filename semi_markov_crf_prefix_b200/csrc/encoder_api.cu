@@ -169,8 +169,10 @@ semicrf_status semicrf_linear_attention(const semicrf_attention_dims *dims, cons
     w.lead = 1;
     finish_walk(w, a, d.dtype);
     int n = 0;
-    cudaError_t e = launch_la(a, d.dtype, static_cast<unsigned char *>(ws) + kStatusBytes, static_cast<cudaStream_t>(stream), &n);
-    return ended(e, n);
+    bool small;
+    cudaError_t e = launch_la(a, d.dtype, static_cast<unsigned char *>(ws) + kStatusBytes, ws_bytes - kStatusBytes,
+                              static_cast<cudaStream_t>(stream), &n, &small);
+    return small ? SEMICRF_ERR_WORKSPACE_TOO_SMALL : ended(e, n);
 }
 
 semicrf_status semicrf_linear_attention_backward(const semicrf_attention_dims *dims, const void *q, const void *k,
@@ -248,8 +250,10 @@ semicrf_status semicrf_linear_attention_backward(const semicrf_attention_dims *d
     z.lead = 0;
     for (LaWalk &w : a.w) finish_walk(w, a, d.dtype);
     int n = 0;
-    cudaError_t e = launch_la(a, d.dtype, static_cast<unsigned char *>(ws) + kStatusBytes, static_cast<cudaStream_t>(stream), &n);
-    return ended(e, n);
+    bool small;
+    cudaError_t e = launch_la(a, d.dtype, static_cast<unsigned char *>(ws) + kStatusBytes, ws_bytes - kStatusBytes,
+                              static_cast<cudaStream_t>(stream), &n, &small);
+    return small ? SEMICRF_ERR_WORKSPACE_TOO_SMALL : ended(e, n);
 }
 
 semicrf_status semicrf_linear_attention_step(const semicrf_attention_dims *dims, const void *q, const void *k,

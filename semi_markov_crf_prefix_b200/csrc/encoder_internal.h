@@ -140,10 +140,16 @@ struct LaStepArgs {
     float scale;
 };
 
+struct LaMaps;
+
+// Workspace of these operands, and the most that any operands of these sizes need.
+size_t la_need(const LaArgs &a, int dtype);
 size_t la_workspace(int B, int T, int H, int dk, int dv, int dtype, int nwalk);
-cudaError_t launch_la(LaArgs a, int dtype, unsigned char *ws, cudaStream_t st, int *launches);
+// *small: the workspace does not hold the plan that the operands turned out to need.
+cudaError_t launch_la(LaArgs a, int dtype, unsigned char *ws, size_t ws_bytes, cudaStream_t st, int *launches, bool *small);
 bool la_tma_ok(const LaArgs &a, int dtype);
-cudaError_t launch_la_tma(const LaArgs &a, bool state_only, cudaStream_t st, int *launches);
+bool la_tma_maps(const LaArgs &a, LaMaps *maps);
+cudaError_t launch_la_tma(const LaArgs &a, const LaMaps &maps, bool state_only, cudaStream_t st, int *launches);
 cudaError_t launch_la_step(const LaStepArgs &a, int dtype, cudaStream_t st, int *launches);
 
 // ---- group norm ----

@@ -2,12 +2,21 @@
 // block does, powers of the decay, states.
 #pragma once
 
+#include <cuda.h>
 #include <math.h>
 
 #include "encoder_internal.h"
 #include "findings.cuh"
 
 namespace semicrf {
+
+// What the copy engine knows of each walk's operands.
+struct LaMaps {
+    struct {
+        CUtensorMap q, k, v, o;
+    } w[3];
+};
+
 namespace {
 
 constexpr int kChunk = 128;     // positions of one step of the chunked walk

@@ -656,9 +656,8 @@ cudaError_t go_chunk(const LaArgs &a, cudaStream_t st, int *n)
 }
 
 template <bool STATE_ONLY>
-cudaError_t go_walk(const LaArgs &a, int dtype, bool tma, cudaStream_t st, int *n)
+cudaError_t go_walk(const LaArgs &a, int dtype, cudaStream_t st, int *n)
 {
-    if (tma) return launch_la_tma(a, STATE_ONLY, st, n);
     if (dtype == SEMICRF_F32) return go_chunk<float, STATE_ONLY>(a, st, n);
     if (dtype == SEMICRF_BF16) return go_chunk<__nv_bfloat16, STATE_ONLY>(a, st, n);
     return go_chunk<__half, STATE_ONLY>(a, st, n);
@@ -720,6 +719,12 @@ LaPlan la_plan(int B, int T, int H, int dk, int dv, int dtype, int nwalk, bool t
 
 }  // namespace
 
+size_t la_need(const LaArgs &a, int dtype)
+{
+    const LaPlan p = la_plan(a.B, a.T, a.H, a.w[0].dk, a.w[0].dv, dtype, a.nwalk, la_tma_ok(a, dtype));
+    return a.nwalk * (p.seg_bytes + p.part_bytes);
+}
+
 size_t la_workspace(int B, int T, int H, int dk, int dv, int dtype, int nwalk)
 {
     size_t most = 0;   // operands that the copy engine cannot address take the other plan: room for either
@@ -732,15 +737,25 @@ size_t la_workspace(int B, int T, int H, int dk, int dv, int dtype, int nwalk)
     return most;
 }
 
-cudaError_t launch_la(LaArgs a, int dtype, unsigned char *ws, cudaStream_t st, int *launches)
+cudaError_t launch_la(LaArgs a, int dtype, unsigned char *ws, size_t ws_bytes, cudaStream_t st, int *launches, bool *small)
 {
     *launches = 0;
-    const bool tma = la_tma_ok(a, dtype);
-    const LaPlan p = la_plan(a.B, a.T, a.H, a.w[0].dk, a.w[0].dv, dtype, a.nwalk, tma);
-    a.width = p.width;
-    a.slices = p.slices;
-    a.nseg = p.nseg;
-    a.seg_len = p.seg_len;
+    *small = false;
+    LaPlan p;
+    LaMaps maps;
+    bool tma = la_tma_ok(a, dtype);
+    for (;;) {
+        p = la_plan(a.B, a.T, a.H, a.w[0].dk, a.w[0].dv, dtype, a.nwalk, tma);
+        a.width = p.width;
+        a.slices = p.slices;
+        a.nseg = p.nseg;
+        a.seg_len = p.seg_len;
+        if (!tma || la_tma_maps(a, &maps)) break;
+        cudaGetLastError();
+        tma = false;   // the kernel for any operands
+    }
+    *small = ws_bytes < a.nwalk * (p.seg_bytes + p.part_bytes);
+    if (*small) return cudaSuccess;
     for (int i = 0; i < a.nwalk; ++i) {
         a.w[i].seg = p.seg_bytes ? reinterpret_cast<float *>(ws) : nullptr;
         ws += p.seg_bytes;
@@ -750,14 +765,14 @@ cudaError_t launch_la(LaArgs a, int dtype, unsigned char *ws, cudaStream_t st, i
     for (a.kblock = 0; a.kblock < p.kblocks; ++a.kblock) {
         cudaError_t e;
         if (a.nseg > 1) {
-            e = go_walk<true>(a, dtype, tma, st, launches);
+            e = tma ? launch_la_tma(a, maps, true, st, launches) : go_walk<true>(a, dtype, st, launches);
             if (e != cudaSuccess) return e;
             e = timed_launch(st, launches, [&] {
                 la_join_kernel<<<dim3(a.B * a.H * a.slices, a.width * a.width / 256, a.nwalk), 256, 0, st>>>(a);
             });
             if (e != cudaSuccess) return e;
         }
-        e = go_walk<false>(a, dtype, tma, st, launches);
+        e = tma ? launch_la_tma(a, maps, false, st, launches) : go_walk<false>(a, dtype, st, launches);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

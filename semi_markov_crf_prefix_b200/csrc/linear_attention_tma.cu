@@ -23,8 +23,6 @@
 //
 // A walk against time takes a chunk's rows in memory order too: row r is position
 // 127 - r of the chunk, and the tables of decays are mirrored.
-#include <cuda.h>
-
 #include "la_common.cuh"
 #include "tensor_core.cuh"
 
@@ -32,12 +30,6 @@ namespace semicrf {
 namespace {
 
 constexpr int kWorkers = 256, kThreads = kWorkers + 32;
-
-struct LaMaps {
-    struct {
-        CUtensorMap q, k, v, o;
-    } w[3];
-};
 
 struct LaTables {
     float diag[64];   // b c lam^d by 31 + (row - column) inside a 32 x 32 block, 0 where the column lies ahead
@@ -798,8 +790,8 @@ Kernel kernel_of(int width, bool state_only, int *smem)
 
 }  // namespace
 
-// Whether the copy engine can address every operand of these widths: aligned, and no axis
-// repeated by a stride of 0 (an expanded tensor's).
+// Whether the copy engine should be able to address every operand of these widths: aligned,
+// and no axis repeated by a stride of 0 (an expanded tensor's).  la_tma_maps has the last word.
 bool la_tma_ok(const LaArgs &a, int dtype)
 {
     if (dtype != SEMICRF_BF16 || !encoder()) return false;
@@ -813,22 +805,31 @@ bool la_tma_ok(const LaArgs &a, int dtype)
     return true;
 }
 
-cudaError_t launch_la_tma(const LaArgs &a, bool state_only, cudaStream_t st, int *n)
+// The maps of all operands; false where the driver's encoder refuses one.
+bool la_tma_maps(const LaArgs &a, LaMaps *maps)
+{
+    for (int state = 0; state < (a.nseg > 1 ? 2 : 1); ++state) {
+        int smem;
+        const Kernel k = kernel_of(a.width, state, &smem);
+        // (also binds the device's context to a thread that makes its first call, which the
+        // encoder wants: the backward pass runs in a thread of its own)
+        if (cudaFuncSetAttribute(reinterpret_cast<const void *>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return false;
+    }
+    for (int i = 0; i < a.nwalk; ++i) {
+        const LaWalk &w = a.w[i];
+        auto &m = maps->w[i];
+        if (!make_map(&m.q, w.q, w.qs, w.dk, a) || !make_map(&m.k, w.k, w.ks, w.dk, a) ||
+            !make_map(&m.v, w.v, w.vs, w.dv, a) || !make_map(&m.o, w.o, w.os, w.dv, a))
+            return false;
+    }
+    return true;
+}
+
+cudaError_t launch_la_tma(const LaArgs &a, const LaMaps &maps, bool state_only, cudaStream_t st, int *n)
 {
     int smem;
     const Kernel k = kernel_of(a.width, state_only, &smem);
-    // (also binds the device's context to a thread that makes its first call, which the
-    // driver's encoder wants: the backward pass runs in a thread of its own)
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    LaMaps maps;
-    for (int i = 0; i < a.nwalk; ++i) {
-        const LaWalk &w = a.w[i];
-        auto &m = maps.w[i];
-        if (!make_map(&m.q, w.q, w.qs, w.dk, a) || !make_map(&m.k, w.k, w.ks, w.dk, a) ||
-            !make_map(&m.v, w.v, w.vs, w.dv, a) || !make_map(&m.o, w.o, w.os, w.dv, a))
-            return cudaErrorInvalidValue;
-    }
     return timed_launch(st, n, [&] { k<<<dim3(a.B * a.H * a.nseg, a.nwalk), kThreads, smem, st>>>(a, maps); });
 }
 

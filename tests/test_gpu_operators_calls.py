@@ -36,3 +36,22 @@ def test_decays_held_as_a_parameter():
         sc.linear_attention_step(q.detach()[:, 0], k[:, 0], v[:, 0], decay, torch.zeros(2, 2, 16, 16, device="cuda"))
     with pytest.raises(TypeError):
         sc.linear_attention(q.detach(), k, v, None)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("strides", ["sliding", "heads apart", "positions and heads out of proportion", "positions first"])
+def test_strides_of_any_order(strides, d, dtype):
+    B, T, H = 2, 300, 3
+    buf = rnd(7, 4 * B * T * H * d + 4096).to(dtype)
+    st = {"sliding": (T * 8 + 8 * H, 8, 16, 1),                    # windows of one row that overlap
+          "heads apart": (H * T * d, d, T * d, 1),
+          "positions and heads out of proportion": (T * (H * d + 24), H * d + 24, d + 8, 1),
+          "positions first": (H * d, B * H * d, d, 1)}[strides]
+    x = [buf.as_strided((B, T, H, d), st, i * 512) for i in range(3)]
+    ld = torch.tensor([-0.2, -0.02, -0.002], device="cuda")
+    dense = [t.contiguous() for t in x]
+    assert torch.equal(sc.linear_attention(*x, ld), sc.linear_attention(*dense, ld))
+    do = rnd(8, B, T, H, d).to(dtype)
+    for got, want in zip(sc.linear_attention_backward(do, *x, ld)[:3], sc.linear_attention_backward(do, *dense, ld)[:3]):
+        assert torch.equal(got, want)
