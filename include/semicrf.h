@@ -330,6 +330,13 @@ typedef struct {
  * backward call; 0 for invalid dims. */
 size_t semicrf_linear_attention_workspace_bytes(const semicrf_attention_dims *dims, int32_t backward);
 
+/* The same of a call with these operands (o: of the backward grad_o; dq, dk and dv 16-byte
+ * aligned), which may be far less: bfloat16 operands whose rows are 16-byte aligned need no
+ * partial sums at widths above 64.  The call has the last word: where it returns
+ * SEMICRF_ERR_WORKSPACE_TOO_SMALL all the same, the size above serves. */
+size_t semicrf_linear_attention_workspace_bytes_at(const semicrf_attention_dims *dims, int32_t backward, const void *q,
+                                                   const void *k, const void *v, const void *o);
+
 semicrf_status semicrf_linear_attention(const semicrf_attention_dims *dims, const void *q, const void *k,
                                         const void *v, const float *log_decay, const int32_t *lengths,
                                         const float *state_in, void *o, float *state_out, void *ws,

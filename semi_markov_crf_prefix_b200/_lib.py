@@ -79,6 +79,7 @@ SIGNATURES = {
     "semicrf_nll": (ctypes.c_int, [_DP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
     "semicrf_nll_backward": (ctypes.c_int, [_DP, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P, _P, _P, _P]),
     "semicrf_linear_attention_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int32]),
+    "semicrf_linear_attention_workspace_bytes_at": (ctypes.c_size_t, [_P, ctypes.c_int32, _P, _P, _P, _P]),
     "semicrf_linear_attention": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
     "semicrf_linear_attention_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S,
                                                          _P]),

@@ -94,59 +94,10 @@ void finish_walk(LaWalk &w, const LaArgs &a, int dtype)
     w.o_vec = vectors(w.o, w.os, a, w.dv, dtype);
 }
 
-semicrf_status norm_ok(const semicrf_norm_dims *d)
+// The walk of a forward call.
+LaArgs forward_args(const semicrf_attention_dims &d, const void *q, const void *k, const void *v, const float *log_decay,
+                    const int32_t *lengths, const float *state_in, void *o, float *state_out, void *ws)
 {
-    if (!d || d->N < 1 || d->S < 1 || d->C < 1 || d->G < 1 || d->C % d->G) return SEMICRF_ERR_INVALID_ARG;
-    if (d->dtype < SEMICRF_F32 || d->dtype > SEMICRF_F16 ||
-        (d->weight_dtype != SEMICRF_F32 && d->weight_dtype != d->dtype) || d->activation < SEMICRF_ACT_NONE ||
-        d->activation > SEMICRF_ACT_GELU || !(d->eps >= 0.f) || !isfinite(d->eps))
-        return SEMICRF_ERR_INVALID_ARG;
-    // thread blocks of one launch, and indices of one row block
-    if (d->S > (1 << 30) || (long long)d->N * d->G > (1LL << 30) || d->C > (1 << 22)) return SEMICRF_ERR_UNSUPPORTED_SHAPE;
-    return SEMICRF_OK;
-}
-
-NormArgs norm_args(const semicrf_norm_dims &d, const void *weight, const void *bias, const int32_t *lengths, void *ws)
-{
-    NormArgs a;
-    memset(&a, 0, sizeof(a));
-    a.N = d.N;
-    a.S = d.S;
-    a.C = d.C;
-    a.G = d.G;
-    a.act = d.activation;
-    a.wdtype = d.weight_dtype;
-    a.eps = d.eps;
-    a.weight = weight;
-    a.bias = bias;
-    a.lengths = lengths;
-    a.status = static_cast<int32_t *>(ws);
-    a.part = reinterpret_cast<double *>(static_cast<unsigned char *>(ws) + kStatusBytes);
-    return a;
-}
-
-}  // namespace
-
-extern "C" {
-
-size_t semicrf_linear_attention_workspace_bytes(const semicrf_attention_dims *dims, int32_t backward)
-{
-    if (attention_ok(dims) != SEMICRF_OK || (backward != 0 && backward != 1)) return 0;
-    return attention_ws(*dims, backward);
-}
-
-semicrf_status semicrf_linear_attention(const semicrf_attention_dims *dims, const void *q, const void *k,
-                                        const void *v, const float *log_decay, const int32_t *lengths,
-                                        const float *state_in, void *o, float *state_out, void *ws, size_t ws_bytes,
-                                        void *stream)
-{
-    prof_reset();
-    semicrf_status s = attention_ok(dims);
-    if (s != SEMICRF_OK) return s;
-    const semicrf_attention_dims &d = *dims;
-    if (!q || !k || !v || !log_decay || !o) return SEMICRF_ERR_INVALID_ARG;
-    s = ws_ok(ws, ws_bytes, attention_ws(d, false));
-    if (s != SEMICRF_OK) return s;
     LaArgs a = attention_args(d, log_decay, lengths, ws, 1);
     LaWalk &w = a.w[0];
     w.q = q;
@@ -168,26 +119,14 @@ semicrf_status semicrf_linear_attention(const semicrf_attention_dims *dims, cons
     w.reverse = d.reverse;
     w.lead = 1;
     finish_walk(w, a, d.dtype);
-    int n = 0;
-    bool small;
-    cudaError_t e = launch_la(a, d.dtype, static_cast<unsigned char *>(ws) + kStatusBytes, ws_bytes - kStatusBytes,
-                              static_cast<cudaStream_t>(stream), &n, &small);
-    return small ? SEMICRF_ERR_WORKSPACE_TOO_SMALL : ended(e, n);
+    return a;
 }
 
-semicrf_status semicrf_linear_attention_backward(const semicrf_attention_dims *dims, const void *q, const void *k,
-                                                 const void *v, const float *log_decay, const int32_t *lengths,
-                                                 const float *state_in, const void *grad_o, const float *grad_state,
-                                                 void *dq, void *dk, void *dv, float *grad_state_in, void *ws,
-                                                 size_t ws_bytes, void *stream)
+// The three walks of a backward call.
+LaArgs backward_args(const semicrf_attention_dims &d, const void *q, const void *k, const void *v, const float *log_decay,
+                     const int32_t *lengths, const float *state_in, const void *grad_o, const float *grad_state, void *dq,
+                     void *dk, void *dv, float *grad_state_in, void *ws)
 {
-    prof_reset();
-    semicrf_status s = attention_ok(dims);
-    if (s != SEMICRF_OK) return s;
-    const semicrf_attention_dims &d = *dims;
-    if (!q || !k || !v || !log_decay || !grad_o || !dq || !dk || !dv) return SEMICRF_ERR_INVALID_ARG;
-    s = ws_ok(ws, ws_bytes, attention_ws(d, true));
-    if (s != SEMICRF_OK) return s;
     LaArgs a = attention_args(d, log_decay, lengths, ws, 3);
     // dq_i = scale sum_j lam^{i-j} (do_i . v_j) k_j, and the given state transposed
     LaWalk &x = a.w[0];
@@ -249,11 +188,98 @@ semicrf_status semicrf_linear_attention_backward(const semicrf_attention_dims *d
     z.reverse = !d.reverse;
     z.lead = 0;
     for (LaWalk &w : a.w) finish_walk(w, a, d.dtype);
+    return a;
+}
+
+semicrf_status run_walks(const LaArgs &a, int dtype, void *ws, size_t ws_bytes, void *stream)
+{
+    const semicrf_status s = ws_ok(ws, ws_bytes, kStatusBytes + la_need(a, dtype));
+    if (s != SEMICRF_OK) return s;
     int n = 0;
     bool small;
-    cudaError_t e = launch_la(a, d.dtype, static_cast<unsigned char *>(ws) + kStatusBytes, ws_bytes - kStatusBytes,
-                              static_cast<cudaStream_t>(stream), &n, &small);
+    const cudaError_t e = launch_la(a, dtype, static_cast<unsigned char *>(ws) + kStatusBytes, ws_bytes - kStatusBytes,
+                                    static_cast<cudaStream_t>(stream), &n, &small);
     return small ? SEMICRF_ERR_WORKSPACE_TOO_SMALL : ended(e, n);
+}
+
+semicrf_status norm_ok(const semicrf_norm_dims *d)
+{
+    if (!d || d->N < 1 || d->S < 1 || d->C < 1 || d->G < 1 || d->C % d->G) return SEMICRF_ERR_INVALID_ARG;
+    if (d->dtype < SEMICRF_F32 || d->dtype > SEMICRF_F16 ||
+        (d->weight_dtype != SEMICRF_F32 && d->weight_dtype != d->dtype) || d->activation < SEMICRF_ACT_NONE ||
+        d->activation > SEMICRF_ACT_GELU || !(d->eps >= 0.f) || !isfinite(d->eps))
+        return SEMICRF_ERR_INVALID_ARG;
+    // thread blocks of one launch, and indices of one row block
+    if (d->S > (1 << 30) || (long long)d->N * d->G > (1LL << 30) || d->C > (1 << 22)) return SEMICRF_ERR_UNSUPPORTED_SHAPE;
+    return SEMICRF_OK;
+}
+
+NormArgs norm_args(const semicrf_norm_dims &d, const void *weight, const void *bias, const int32_t *lengths, void *ws)
+{
+    NormArgs a;
+    memset(&a, 0, sizeof(a));
+    a.N = d.N;
+    a.S = d.S;
+    a.C = d.C;
+    a.G = d.G;
+    a.act = d.activation;
+    a.wdtype = d.weight_dtype;
+    a.eps = d.eps;
+    a.weight = weight;
+    a.bias = bias;
+    a.lengths = lengths;
+    a.status = static_cast<int32_t *>(ws);
+    a.part = reinterpret_cast<double *>(static_cast<unsigned char *>(ws) + kStatusBytes);
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t semicrf_linear_attention_workspace_bytes(const semicrf_attention_dims *dims, int32_t backward)
+{
+    if (attention_ok(dims) != SEMICRF_OK || (backward != 0 && backward != 1)) return 0;
+    return attention_ws(*dims, backward);
+}
+
+size_t semicrf_linear_attention_workspace_bytes_at(const semicrf_attention_dims *dims, int32_t backward, const void *q,
+                                                   const void *k, const void *v, const void *o)
+{
+    if (attention_ok(dims) != SEMICRF_OK || (backward != 0 && backward != 1)) return 0;
+    const semicrf_attention_dims &d = *dims;
+    const LaArgs a = backward ? backward_args(d, q, k, v, nullptr, nullptr, nullptr, o, nullptr, nullptr, nullptr, nullptr,
+                                              nullptr, nullptr)
+                              : forward_args(d, q, k, v, nullptr, nullptr, nullptr, const_cast<void *>(o), nullptr, nullptr);
+    return kStatusBytes + la_need(a, d.dtype);
+}
+
+semicrf_status semicrf_linear_attention(const semicrf_attention_dims *dims, const void *q, const void *k,
+                                        const void *v, const float *log_decay, const int32_t *lengths,
+                                        const float *state_in, void *o, float *state_out, void *ws, size_t ws_bytes,
+                                        void *stream)
+{
+    prof_reset();
+    semicrf_status s = attention_ok(dims);
+    if (s != SEMICRF_OK) return s;
+    const semicrf_attention_dims &d = *dims;
+    if (!q || !k || !v || !log_decay || !o) return SEMICRF_ERR_INVALID_ARG;
+    return run_walks(forward_args(d, q, k, v, log_decay, lengths, state_in, o, state_out, ws), d.dtype, ws, ws_bytes, stream);
+}
+
+semicrf_status semicrf_linear_attention_backward(const semicrf_attention_dims *dims, const void *q, const void *k,
+                                                 const void *v, const float *log_decay, const int32_t *lengths,
+                                                 const float *state_in, const void *grad_o, const float *grad_state,
+                                                 void *dq, void *dk, void *dv, float *grad_state_in, void *ws,
+                                                 size_t ws_bytes, void *stream)
+{
+    prof_reset();
+    semicrf_status s = attention_ok(dims);
+    if (s != SEMICRF_OK) return s;
+    const semicrf_attention_dims &d = *dims;
+    if (!q || !k || !v || !log_decay || !grad_o || !dq || !dk || !dv) return SEMICRF_ERR_INVALID_ARG;
+    return run_walks(backward_args(d, q, k, v, log_decay, lengths, state_in, grad_o, grad_state, dq, dk, dv, grad_state_in, ws),
+                     d.dtype, ws, ws_bytes, stream);
 }
 
 semicrf_status semicrf_linear_attention_step(const semicrf_attention_dims *dims, const void *q, const void *k,

@@ -129,19 +129,38 @@ def _extras(shape, dv, device, lengths, state, state_name):
 
 
 def linear_attention_workspace_bytes(q, v, backward=False) -> int:
-    """Bytes of workspace of a call with operands like q [B,T,H,dk] and v [B,T,H,dv]."""
+    """Bytes of workspace that serve any call with operands like q [B,T,H,dk] and v [B,T,H,dv],
+    whatever their strides and addresses (the calls themselves make what theirs need)."""
     none = (0, 0, 0)
-    return _attention_ws(_dims(_TYPES[q.dtype], q.shape, v.shape[3], 1.0, False, none, none, none, none), q.shape,
-                         v.shape[3], backward)
+    d = _dims(_TYPES[q.dtype], q.shape, v.shape[3], 1.0, False, none, none, none, none)
+    return _supported(_lib.load().semicrf_linear_attention_workspace_bytes(d, 1 if backward else 0), q.shape, v.shape[3])
 
 
-def _attention_ws(dims, shape, dv, backward):
-    n = _lib.load().semicrf_linear_attention_workspace_bytes(dims, 1 if backward else 0)
+def _supported(n, shape, dv):
     if n == 0:
         bad = max(shape[3], dv) > _lib.MAX_HEAD
         raise ValueError(f"unsupported arguments: q {tuple(shape)}, width of v {dv}"
                          + (f" (at most {_lib.MAX_HEAD} wide)" if bad else ""))
     return n
+
+
+def _attention_ws_at(dims, shape, dv, backward, q, k, v, o):
+    return _supported(_lib.load().semicrf_linear_attention_workspace_bytes_at(dims, backward, q, k, v, o), shape, dv)
+
+
+def _walk(name, dims, shape, dv, backward, q, k, v, o, device, ws, *args):
+    """A call with the workspace given, or with one of the operands' size: args, ws and its bytes."""
+    own = ws is None
+    need = _attention_ws_at(dims, shape, dv, backward, q, k, v, o)
+    ws = _workspace(ws, need, device)
+    try:
+        _call(name, device, *args, ws.data_ptr(), ws.numel())
+    except _lib.SemiCRFError as e:
+        if not own or e.status != _lib.SEMICRF_ERR_WORKSPACE_TOO_SMALL:
+            raise
+        # the copy engine's maps were refused: the size for any operands
+        ws = _workspace(None, _lib.load().semicrf_linear_attention_workspace_bytes(dims, backward), device)
+        _call(name, device, *args, ws.data_ptr(), ws.numel())
 
 
 def _dense(shape, width):
@@ -160,12 +179,14 @@ def linear_attention_forward(q, k, v, log_decay, lengths=None, scale=None, initi
 
 
 def _attention_run(q, k, v, log_decay, lengths, initial_state, return_state, d, shape, dv, device, ws):
-    ws = _workspace(ws, _attention_ws(d, shape, dv, False), device)
     B, T, H, dk = shape
+    qp, kp, vp = q.data_ptr(), k.data_ptr(), v.data_ptr()
+    _supported(B * T * H * dk * dv, shape, dv)
     o = torch.empty((B, T, H, dv), dtype=q.dtype, device=device)
     state = torch.empty((B, H, dk, dv), dtype=torch.float32, device=device) if return_state else None
-    _call("linear_attention", device, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lengths),
-          _ptr(initial_state), o.data_ptr(), _ptr(state), ws.data_ptr(), ws.numel())
+    op = o.data_ptr()
+    _walk("linear_attention", d, shape, dv, 0, qp, kp, vp, op, device, ws, d, qp, kp, vp, log_decay.data_ptr(),
+          _ptr(lengths), _ptr(initial_state), op, _ptr(state))
     return o, state
 
 
@@ -178,14 +199,14 @@ def linear_attention_backward(grad_o, q, k, v, log_decay, lengths=None, scale=No
     _extras(shape, dv, device, lengths, initial_state, "initial_state")
     _extras(shape, dv, device, None, grad_state, "grad_state")
     d = _dims(kind, shape, dv, scale, reverse, qs, ks, vs, os)
-    ws = _workspace(ws, _attention_ws(d, shape, dv, True), device)
     B, T, H, dk = shape
+    qp, kp, vp, gp = q.data_ptr(), k.data_ptr(), v.data_ptr(), grad_o.data_ptr()
+    _supported(B * T * H * dk * dv, shape, dv)
     new = lambda width: torch.empty((B, T, H, width), dtype=q.dtype, device=device)  # noqa: E731
     dq, dk_, dv_ = new(dk), new(dk), new(dv)
     ds = torch.empty((B, H, dk, dv), dtype=torch.float32, device=device) if want_initial_state else None
-    _call("linear_attention_backward", device, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-          _ptr(lengths), _ptr(initial_state), grad_o.data_ptr(), _ptr(grad_state), dq.data_ptr(), dk_.data_ptr(),
-          dv_.data_ptr(), _ptr(ds), ws.data_ptr(), ws.numel())
+    _walk("linear_attention_backward", d, shape, dv, 1, qp, kp, vp, gp, device, ws, d, qp, kp, vp, log_decay.data_ptr(),
+          _ptr(lengths), _ptr(initial_state), gp, _ptr(grad_state), dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(), _ptr(ds))
     return dq, dk_, dv_, ds
 
 

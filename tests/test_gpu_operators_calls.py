@@ -38,6 +38,48 @@ def test_decays_held_as_a_parameter():
         sc.linear_attention(q.detach(), k, v, None)
 
 
+def test_workspace_follows_the_operands():
+    # widths over 64 in bf16: partial sums only where the copy engine cannot address the operands
+    from semi_markov_crf_prefix_b200 import encoder
+    B, T, H, d = 4, 20000, 4, 128
+    q = torch.zeros(B, T, H, d, dtype=torch.bfloat16, device="cuda")
+    ld = torch.full((H,), -0.01, device="cuda")
+    size = q.numel() * 2
+
+    def used(f):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        f()
+        return torch.cuda.max_memory_allocated() - before
+
+    assert used(lambda: sc.linear_attention_forward(q, q, q, ld)) < size + (64 << 20)
+    assert used(lambda: sc.linear_attention_backward(q, q, q, q, ld)) < 3 * size + (64 << 20)
+    # the size for any operands is what it was, and serves
+    need = encoder.linear_attention_workspace_bytes(q, q)
+    assert need > 2 * size
+    odd = torch.zeros(q.numel() + 1, dtype=torch.bfloat16, device="cuda")[1:].view_as(q)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    sc.linear_attention_forward(odd, q, q, ld, ws=ws)
+    with pytest.raises(sc.SemiCRFError):
+        sc.linear_attention_forward(odd, q, q, ld, ws=ws[:need // 2])
+    sc.linear_attention_forward(q, q, q, ld, ws=ws[:need // 2])
+
+
+def test_a_workspace_that_turns_out_too_small(monkeypatch):
+    # the library's call has the last word on its plan
+    from semi_markov_crf_prefix_b200 import encoder
+    q, k, v, do = (rnd(i, 1, 4000, 2, 64).bfloat16() for i in range(4))
+    ld = torch.tensor([-0.1, -0.001], device="cuda")
+    want = sc.linear_attention_forward(q, k, v, ld)[0]
+    grads = sc.linear_attention_backward(do, q, k, v, ld)
+    monkeypatch.setattr(encoder, "_attention_ws_at", lambda *a: 256)
+    assert torch.equal(sc.linear_attention_forward(q, k, v, ld)[0], want)
+    assert all(torch.equal(a, b) for a, b in zip(sc.linear_attention_backward(do, q, k, v, ld)[:3], grads))
+    with pytest.raises(sc.SemiCRFError):
+        sc.linear_attention_forward(q, k, v, ld, ws=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("strides", ["sliding", "heads apart", "positions and heads out of proportion", "positions first"])
