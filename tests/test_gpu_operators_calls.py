@@ -7,6 +7,7 @@ pytestmark = pytest.mark.gpu
 import torch  # noqa: E402
 
 import semi_markov_crf_prefix_b200 as sc  # noqa: E402
+from test_gpu_attention import check as attention_check, inputs as attention_inputs  # noqa: E402
 
 
 def rnd(seed, *shape):
@@ -97,3 +98,32 @@ def test_strides_of_any_order(strides, d, dtype):
     do = rnd(8, B, T, H, d).to(dtype)
     for got, want in zip(sc.linear_attention_backward(do, *x, ld)[:3], sc.linear_attention_backward(do, *dense, ld)[:3]):
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [(torch.float16, 128, 128), (torch.float16, 200, 130), (torch.bfloat16, 200, 130),
+                                         (torch.bfloat16, 130, 200), (torch.float32, 130, 70), (torch.float16, 64, 65)])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_wide_heads_in_segments(dtype, dk, dv, reverse):
+    # blocks of the contraction, slices of the values and joined segments in one call
+    T = 2500
+    q, k, v, ld, s0 = attention_inputs(2, T, 1, dk, dv, dtype, state=True, decay=-0.003)
+    assert sc.linear_attention_workspace_bytes(q, v) > 256
+    attention_check(q, k, v, ld, s0, reverse=reverse, lengths=torch.tensor([T, 1300], dtype=torch.int32, device="cuda"))
+    attention_check(q[:1], k[:1], v[:1], ld, None, reverse=reverse)
+
+
+@pytest.mark.parametrize("d", [64, 100])
+def test_rows_off_the_copy_engine_in_segments(d):
+    # bf16 without 16-byte alignment
+    q, k, v, ld, s0 = attention_inputs(1, 3100, 1, d, d, torch.bfloat16, state=True, decay=-0.003, layout="off")
+    attention_check(q, k, v, ld, s0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 100, 128])
+@pytest.mark.parametrize("T", [1, 2, 300, 2500])
+def test_no_memory_at_all(dtype, d, T):
+    # log_decay of minus infinity: each position alone, gradients too
+    q, k, v, ld, s0 = attention_inputs(1, T, 2, d, d, dtype, state=True, decay=float("-inf"))
+    attention_check(q, k, v, ld, s0)
+    attention_check(q, k, v, ld, s0, reverse=True)
