@@ -96,3 +96,50 @@ def test_many_wide_row_blocks(shape, groups, dtype, ragged):
         assert torch.all((u.double() - dx[at].double()).abs() <= 2.0 ** -7 * u.double().abs() + 1e-5 * u.abs().max())
     again = sc.group_norm_backward(dy, x, stats, groups, w, b, lengths=lengths, activation="silu")
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw) and torch.equal(again[2], db)
+
+
+@pytest.mark.parametrize("shape,groups", [((2, 4000, 128), 8), ((1, 70000, 8), 1), ((2, 3001, 20), 4), ((1, 9000, 1040), 1),
+                                          ((3, 50, 16), 2), ((4, 9, 2000), 5), ((700, 1, 512), 8)])
+@pytest.mark.parametrize("kind", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_every_term_of_the_gradient(shape, groups, kind, dtype):
+    # an upstream gradient with a mean and a part along xh, so that both means that dx takes
+    # away are as large as what stays, against bounds made of dx's own terms: xh, z and the
+    # slopes to 2^-20 of their parts, means to 2^-17 of the absolute mean (float32 runs of 128)
+    N, S, C = shape
+    x, w, b = rnd(10, *shape).to(dtype), 1 + 0.2 * rnd(11, C), 0.2 * rnd(12, C)
+    grp = lambda t: t.view(N, S, groups, C // groups)  # noqa: E731
+    mean_of = lambda t: grp(t).mean((1, 3), keepdim=True).expand(N, S, groups, C // groups).reshape(N, S, C)  # noqa: E731
+    x64, w64, b64 = x.double(), w.double(), b.double()
+    d = x64 - mean_of(x64)
+    rstd = torch.rsqrt(mean_of(d * d) + 1e-5)
+    xh = d * rstd
+    z = xh * w64 + b64
+    dy = (1.0 + 0.8 * xh + 0.5 * rnd(13, *shape)).to(dtype)
+    if kind == "silu":
+        slope = torch.sigmoid(z) * (1 + z * (1 - torch.sigmoid(z)))
+    elif kind == "gelu":
+        slope = 0.5 * torch.special.erfc(-z * 0.5 ** 0.5) + z * torch.exp(-z * z / 2) * 0.3989422804014327
+    else:
+        slope = torch.ones_like(z)
+    dz = dy.double() * slope
+    g = dz * w64
+    m1, m2 = mean_of(g), mean_of(g * xh)
+    want = rstd * (g - m1 - xh * m2)
+    leaves = [t.clone().requires_grad_(True) for t in (x, w, b)]
+    y = sc.group_norm(leaves[0], groups, leaves[1], leaves[2], activation=kind)
+    dx, dw, db = torch.autograd.grad(y, leaves, dy)
+    u = 2.0 ** -20
+    ez = dy.double().abs() * u * (1 + (w64 * xh).abs() + w64.abs() + b64.abs())      # of dz
+    e1 = mean_of(w64.abs() * ez) + 2.0 ** -17 * mean_of(g.abs())
+    e2 = mean_of((w64 * xh).abs() * ez) + 2.0 ** -17 * mean_of((g * xh).abs())
+    step = torch.finfo(dtype).eps / 2 * 1.001
+    bound = rstd * (w64.abs() * ez + e1 + xh.abs() * e2 + u * (g.abs() + m1.abs() + (xh * m2).abs())) + step * want.abs()
+    assert torch.all((dx.double() - want).abs() <= bound)
+    # either mean left out would be far outside
+    if S * (C // groups) > 8:
+        assert ((rstd * m1).abs() > 2 * bound).double().mean() > 0.9
+        assert ((rstd * xh * m2).abs() > 2 * bound).double().mean() > 0.7
+    flat = lambda t: t.abs().sum((0, 1))  # noqa: E731
+    assert torch.all((dw.double() - (dz * xh).sum((0, 1))).abs() <= 2.0 ** -17 * flat(dz * xh) + flat(ez * (1 + xh.abs())))
+    assert torch.all((db.double() - dz.sum((0, 1))).abs() <= 2.0 ** -17 * flat(dz) + flat(ez))
