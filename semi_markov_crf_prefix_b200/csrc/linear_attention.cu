@@ -685,12 +685,16 @@ namespace {
 
 // How a call is walked: by the copy engine's kernel in one tile of 64 or 128, or in tiles of
 // 64; and its segments, which walk side by side.  A split walk first forms what each
-// segment adds to the state (K and V read twice), so it pays where the sequences and
-// heads leave most of the GPU idle.  Blocks that share an SM (two at width 64 in bf16)
-// take 4.6 us a chunk and 1.8 us for the state alone, one by itself 3.2 us: three
-// segments are the fewest that gain (100 000 positions of 8 heads: 151 us in 36 segments,
-// 209 us in 18; 4000 positions of 128 heads: 115 us in two, 102 us in one).  One block an
-// SM elsewhere (4.6 and 3.0 us a chunk at width 128): two gain.
+// segment adds to the state (K and V read twice) and joins the states, so it pays where the
+// sequences and heads leave most of the GPU idle.  Measured on forward calls, the rule's
+// choice against one walk (rows: sequences times heads):
+//   bf16, width 64   48 rows of 4096 positions 62 us in 6 segments, 105 in one; 98 rows 97 in
+//                    three, 107 in one, but of 2048 positions 66 and 60; two never gain (128
+//                    rows of 4096: 129 and 109), as two blocks share an SM and its rate
+//   bf16, width 128  48 rows of 4096 positions 130 us in three, 154 in one; 74 rows in two 171
+//                    and 156, of 20 000 positions 620 and 713, of 2048 115 and 86
+//   float32          74 rows of 2048 positions 109 us in two, 138 in one; 98 rows have one
+//   float16          74 rows of 2048 positions 86 us in two, 104 in one
 struct LaPlan {
     int width, slices, kblocks, nseg, seg_len;
     size_t seg_bytes, part_bytes;   // of one walk
@@ -708,6 +712,7 @@ LaPlan la_plan(int B, int T, int H, int dk, int dv, int dtype, int nwalk, bool t
     long long n = (shared ? 2LL : 1LL) * device_sm_count() / rows;
     if (n > T / 512) n = T / 512;
     if (n < (shared ? 3 : 2)) n = 1;
+    if (dtype == SEMICRF_BF16 && ((n == 2 && T < 8192) || (n == 3 && T < 3072))) n = 1;
     const long long len = ((T + n - 1) / n + kChunk - 1) / kChunk * kChunk;
     p.seg_len = (int)len;
     p.nseg = (int)((T + len - 1) / len);
