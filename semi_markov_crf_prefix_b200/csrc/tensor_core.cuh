@@ -195,22 +195,31 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t mbar, uint32_t parity
     }
 }
 
+// Two floats to bf16, nearest, a low and b high; what rounds past the largest finite value
+// becomes that value.
+__device__ __forceinline__ uint32_t bf16_pair_finite(float a, float b)
+{
+    uint32_t r;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
 // Two floats as sums of NT bf16 terms, packed (a low, b high), each the nearest to what is
 // left.  Three terms hold a float exactly; two leave 2^-17 of the value at most, one 2^-9.
 // (First terms that are cut off instead, which needs no conversion, leave twice as much of
-// one sign, and the calls take the same time.)
+// one sign, and the calls take the same time.)  All but the last term are finite: float32's
+// largest values, which bf16 rounds to infinity, are sums of finite terms too.
 template <int NT>
 __device__ __forceinline__ void split2(float a, float b, uint32_t (&t)[NT])
 {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-        t[i] = *reinterpret_cast<const uint32_t *>(&r);
-        if (i + 1 < NT) {
-            a -= __uint_as_float(t[i] << 16);
-            b -= __uint_as_float(t[i] & 0xffff0000u);
-        }
+    for (int i = 0; i + 1 < NT; ++i) {
+        t[i] = bf16_pair_finite(a, b);
+        a -= __uint_as_float(t[i] << 16);
+        b -= __uint_as_float(t[i] & 0xffff0000u);
     }
+    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+    t[NT - 1] = *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // The floats that NT packed terms stand for.

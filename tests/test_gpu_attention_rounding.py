@@ -95,3 +95,29 @@ def test_outputs_do_not_depend_on_what_is_asked_for(d, T, reverse):
         ga = sc.linear_attention_backward(do, q, k, v, ld, **how)
         gb = sc.linear_attention_backward(do, q, k, v, ld, want_initial_state=True, **how)
         assert all(torch.equal(x, y) for x, y in zip(ga[:3], gb[:3]))
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (16, 40), (130, 70)])
+@pytest.mark.parametrize("T", [2, 130])
+def test_the_largest_values_of_float32(dk, dv, T):
+    # finite operands at the type's end (what is infinite may spread, as documented)
+    top = torch.finfo(torch.float32).max
+    g = torch.Generator(device="cuda").manual_seed(14)
+    ld = torch.tensor([-0.5], device="cuda")
+    for value in (top, -top):
+        q, k = (torch.zeros(1, T, 1, dk, device="cuda") for _ in range(2))
+        v = torch.rand(1, T, 1, dv, generator=g, device="cuda")
+        q[..., 0], k[..., 0] = 0.5, 0.25
+        v[0, T - 1, 0, 3] = value
+        o, s = sc.linear_attention(q, k, v, ld, scale=1.0, return_state=True)
+        left = torch.exp(ld.double() * torch.arange(T - 1, -1, -1, device="cuda"))
+        want = 0.25 * (left[:, None] * v[0, :, 0].double()).sum(0)
+        assert torch.allclose(s[0, 0, 0].double(), want, rtol=2.0 ** -16)
+        assert torch.allclose(o[0, -1, 0].double(), 0.5 * want, rtol=2.0 ** -16)
+        # the same of a given state
+        s0 = torch.zeros(1, 1, dk, dv, device="cuda")
+        s0[0, 0, 0, 5] = value
+        v[0, T - 1, 0, 3] = 1.0
+        o, s = sc.linear_attention(q, k, v, ld, scale=1.0, initial_state=s0, return_state=True)
+        assert torch.allclose(s[0, 0, 0, 5].double(), s0[0, 0, 0, 5].double() * torch.exp(ld.double() * T)[0], rtol=2.0 ** -16)
+        assert torch.allclose(o[0, 0, 0, 5].double(), 0.5 * s0[0, 0, 0, 5].double() * torch.exp(ld.double())[0], rtol=2.0 ** -16)
