@@ -371,7 +371,8 @@ semicrf_status semicrf_linear_attention_step(const semicrf_attention_dims *dims,
  * Group norm with an activation, channels last:
  *   y[n,s,c] = act(xh w[c] + b[c]),   xh = (x[n,s,c] - mean[n,g]) rstd[n,g]
  * with mean and variance over the positions s < L_n and the C/G channels of c's
- * group g, rstd = 1 / sqrt(variance + eps).
+ * group g, rstd = 1 / sqrt(variance + eps).  Sums are float32 and float64: a variance that
+ * passes float32 (deviations above 1e19) is infinite, and y = act(b) there.
  *   x, y      dtype [N, S, C], contiguous
  *   weight, bias  [C] in float32 or in x's dtype (both the same), or NULL (1 and 0)
  *   lengths   int32 [N] in [0, S], or NULL (all S); y = 0 at s >= L_n, where nothing

@@ -143,3 +143,26 @@ def test_every_term_of_the_gradient(shape, groups, kind, dtype):
     flat = lambda t: t.abs().sum((0, 1))  # noqa: E731
     assert torch.all((dw.double() - (dz * xh).sum((0, 1))).abs() <= 2.0 ** -17 * flat(dz * xh) + flat(ez * (1 + xh.abs())))
     assert torch.all((db.double() - dz.sum((0, 1))).abs() <= 2.0 ** -17 * flat(dz) + flat(ez))
+
+
+@pytest.mark.parametrize("shape,groups", [((2, 9000, 16), 4), ((2, 30, 16), 4), ((3, 1, 512), 8), ((2, 2, 8200), 1), ((1184, 128, 520), 2)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_lowest_value_of_the_type(shape, groups, dtype):
+    # its square passes float32: an infinite variance, not a NaN
+    N, S, C = shape
+    per = C // groups
+    for at in {0, min(5, S - 1), S - 1}:
+        x, b = rnd(14, *shape).to(dtype), rnd(15, C)
+        x[-1, at, per + 1 if groups > 1 else 3] = torch.finfo(dtype).min
+        y = sc.group_norm(x, groups, None, b)
+        some = slice(per, 2 * per) if groups > 1 else slice(0, per)
+        assert torch.equal(y[-1, :, some], b.to(dtype)[some].expand(S, per))
+        assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("value", [3.0, -1e30, 1e-30, 2e38])
+@pytest.mark.parametrize("shape,groups", [((2, 9000, 16), 4), ((1184, 128, 520), 2)])
+def test_constants(shape, groups, value):
+    b = rnd(16, shape[2])
+    y = sc.group_norm(torch.full(shape, value, device="cuda"), groups, None, b)
+    assert torch.equal(y, b.expand(shape))
