@@ -390,11 +390,7 @@ cudaError_t launch_some(const semicrf_adamw_tensor *t, int count, const semicrf_
     }
     if (!blocks) return cudaSuccess;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    prof_before(st);
-    kernel(a, (unsigned)blocks);
-    prof_after(st);
-    ++*n;
-    return cudaGetLastError();
+    return timed_launch(st, n, [&] { kernel(a, (unsigned)blocks); });
 }
 
 template <typename F>
@@ -416,13 +412,6 @@ cudaError_t launch_all(const semicrf_adamw_tensor *t, int count, const semicrf_a
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
-}
-
-semicrf_status ended(cudaError_t e, int launches)
-{
-    if (e != cudaSuccess) return SEMICRF_ERR_CUDA;
-    record_launches(launches);
-    return SEMICRF_OK;
 }
 
 // Whether what a step writes overlaps anything else that it touches (the thread blocks of one

@@ -13,13 +13,6 @@ constexpr size_t kStatusBytes = 256;
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-semicrf_status ended(cudaError_t e, int launches)
-{
-    if (e != cudaSuccess) return SEMICRF_ERR_CUDA;
-    record_launches(launches);
-    return SEMICRF_OK;
-}
-
 semicrf_status ws_ok(const void *ws, size_t have, size_t need)
 {
     if (!ws || reinterpret_cast<uintptr_t>(ws) % 256) return SEMICRF_ERR_INVALID_ARG;

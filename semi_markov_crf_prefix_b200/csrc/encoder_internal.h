@@ -18,6 +18,25 @@ void prof_after(cudaStream_t st);
 void record_launches(int n);
 int device_sm_count();
 
+// One launch, counted in *n and between the profile's events.
+template <typename F>
+cudaError_t timed_launch(cudaStream_t st, int *n, F &&go)
+{
+    prof_before(st);
+    go();
+    prof_after(st);
+    ++*n;
+    return cudaGetLastError();
+}
+
+// How an entry point ends after its launches.
+inline semicrf_status ended(cudaError_t e, int launches)
+{
+    if (e != cudaSuccess) return SEMICRF_ERR_CUDA;
+    record_launches(launches);
+    return SEMICRF_OK;
+}
+
 template <typename T>
 __device__ __forceinline__ float to_f(T v);
 template <>

@@ -869,16 +869,6 @@ int row_blocks(int N, int rows, bool backward)
     return blocks < most ? blocks : most;
 }
 
-template <typename F>
-cudaError_t timed_launch(cudaStream_t st, int *n, F &&go)
-{
-    prof_before(st);
-    go();
-    prof_after(st);
-    ++*n;
-    return cudaGetLastError();
-}
-
 template <typename T, int VEC, bool BWD>
 cudaError_t norm_go(NormArgs a, cudaStream_t st, int *n)
 {

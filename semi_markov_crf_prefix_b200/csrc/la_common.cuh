@@ -129,15 +129,5 @@ __device__ __forceinline__ void mma_terms(F &&go)
             }
 }
 
-template <typename F>
-cudaError_t timed_launch(cudaStream_t st, int *n, F &&go)
-{
-    prof_before(st);
-    go();
-    prof_after(st);
-    ++*n;
-    return cudaGetLastError();
-}
-
 }  // namespace
 }  // namespace semicrf
