@@ -300,7 +300,7 @@ semicrf_status semicrf_clear_operators_status(void *stream);
  * (reverse: from the last valid position to the first),
  *   S_p = lam S_{p-1} + k_p v_p^T,     o_p = scale q_p S_p.
  *   q, k       dtype [B, T, H, dk], v, o dtype [B, T, H, dv]: strides of b, t and h
- *              in elements, the last axis dense
+ *              in elements, 0 for a repeated axis of an input, the last axis dense
  *   log_decay  float32 [H], at most 0 (not checked)
  *   lengths    int32 [B], in [0, T], or NULL (all T); o = 0 at t >= L_b, where
  *              nothing is read

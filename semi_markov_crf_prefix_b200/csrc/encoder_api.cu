@@ -35,6 +35,15 @@ semicrf_status attention_ok(const semicrf_attention_dims *d)
     return SEMICRF_OK;
 }
 
+// Outputs that are written twice would race: no axis longer than one is repeated.
+bool output_ok(const semicrf_attention_dims &d)
+{
+    const int length[3] = {d.B, d.T, d.H};
+    for (int i = 0; i < 3; ++i)
+        if (length[i] > 1 && d.o_stride[i] == 0) return false;
+    return true;
+}
+
 size_t attention_ws(const semicrf_attention_dims &d, bool backward)
 {
     return kStatusBytes + la_workspace(d.B, d.T, d.H, d.dk, d.dv, d.dtype, backward ? 3 : 1);
@@ -256,7 +265,7 @@ semicrf_status semicrf_linear_attention(const semicrf_attention_dims *dims, cons
     semicrf_status s = attention_ok(dims);
     if (s != SEMICRF_OK) return s;
     const semicrf_attention_dims &d = *dims;
-    if (!q || !k || !v || !log_decay || !o) return SEMICRF_ERR_INVALID_ARG;
+    if (!q || !k || !v || !log_decay || !o || !output_ok(d)) return SEMICRF_ERR_INVALID_ARG;
     return run_walks(forward_args(d, q, k, v, log_decay, lengths, state_in, o, state_out, ws), d.dtype, ws, ws_bytes, stream);
 }
 
@@ -283,7 +292,7 @@ semicrf_status semicrf_linear_attention_step(const semicrf_attention_dims *dims,
     semicrf_status s = attention_ok(dims);
     if (s != SEMICRF_OK) return s;
     const semicrf_attention_dims &d = *dims;
-    if (d.T != 1 || !q || !k || !v || !log_decay || !state || !o) return SEMICRF_ERR_INVALID_ARG;
+    if (d.T != 1 || !q || !k || !v || !log_decay || !state || !o || !output_ok(d)) return SEMICRF_ERR_INVALID_ARG;
     LaStepArgs a;
     memset(&a, 0, sizeof(a));
     a.q = q;

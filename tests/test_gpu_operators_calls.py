@@ -127,3 +127,40 @@ def test_no_memory_at_all(dtype, d, T):
     q, k, v, ld, s0 = attention_inputs(1, T, 2, d, d, dtype, state=True, decay=float("-inf"))
     attention_check(q, k, v, ld, s0)
     attention_check(q, k, v, ld, s0, reverse=True)
+
+
+def test_calls_from_several_threads():
+    # each with its own stream and tensors, at the same time
+    import threading
+    ld = torch.tensor([-0.1, -0.001], device="cuda")
+
+    def work(seed):
+        q, k, v, do = (rnd(4 * seed + i, 2, 1500, 2, 64).bfloat16() for i in range(4))
+        x = rnd(seed + 100, 4, 700, 32)
+        p, g = [rnd(seed + 200, 5000)], [rnd(seed + 300, 5000)]
+        m, w, ms, ws = sc.new_adamw_state(p, 8)
+        out = []
+        for i in range(1, 6):
+            leaves = [t.clone().requires_grad_(True) for t in (q, k, v)]
+            o = sc.linear_attention(*leaves, ld)
+            out += [o.detach(), *torch.autograd.grad(o, leaves, do)]
+            y = x.clone().requires_grad_(True)
+            z = sc.group_norm(y, 4, activation="silu")
+            out += [z.detach(), *torch.autograd.grad(z, y, x)]
+            sc.adamw_step(p, g, m, w, i, exp_avg_scale=ms, exp_avg_sq_scale=ws)
+        return out + [p[0].clone(), *sc.adamw_state_values(m, ms, "exp_avg")]
+
+    want = [work(s) for s in range(4)]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def run(s):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got[s] = work(s)
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=run, args=(s,)) for s in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))

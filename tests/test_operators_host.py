@@ -85,3 +85,18 @@ def test_workspace_of_many_row_blocks_stays_small(lib, N, S, C, G):
         for backward in (0, 1):
             need = lib.semicrf_group_norm_workspace_bytes(_lib.NORM_DIMS.pack(N, S, C, G, dtype, _lib.F32, 0, 1e-5), backward)
             assert 0 < need <= max(72 << 20, N * S * C // 8)
+
+
+def test_repeated_outputs_are_refused(lib):
+    # an output axis of stride 0 would be written many times; an input's may repeat
+    fake = ctypes.c_void_p(1 << 20)
+    for axis in range(3):
+        for B, T, H in ((2, 1, 2), (2, 5, 2)):
+            st = [[T * H * 8, H * 8, 8] for _ in range(4)]
+            if (B, T, H)[axis] == 1:
+                continue
+            st[3][axis] = 0
+            d = _lib.ATTENTION_DIMS.pack(B, T, H, 8, 8, _lib.F32, 0, 1.0, *[x for s in st for x in s])
+            assert lib.semicrf_linear_attention(d, fake, fake, fake, fake, None, None, fake, None, fake, 1 << 30, None) == ARG
+            if T == 1:
+                assert lib.semicrf_linear_attention_step(d, fake, fake, fake, fake, fake, fake, None) == ARG
