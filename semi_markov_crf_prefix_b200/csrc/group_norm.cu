@@ -569,47 +569,48 @@ __global__ __launch_bounds__(kLongThreads, 3) void norm_sums_kernel(const __grid
             });
         }
     }
-    double *out = a.part + ((long long)n * sh.strips + strip) * 2 * a.C + c0;
+    double *out = a.part + ((long long)n * sh.strips + strip) * 2 * a.C;
     if (sh.R == 1) {   // nothing to join
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
             if (mine) {
-                out[e] = (double)about[e] + (double)p[e];
-                out[a.C + e] = (double)q[e];
+                out[c0 + e] = (double)about[e] + (double)p[e];
+                out[a.C + c0 + e] = (double)q[e];
             }
         return;
     }
+    // dsm[e][2][thread]; then a thread joins the row lanes of one channel
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        __syncthreads();
-        if (r < sh.R) {
-            dsm[tid] = (double)about[e] + (double)p[e];
-            dsm[kLongThreads + tid] = (double)q[e];
-        }
-        __syncthreads();
-        if (r == 0 && mine) {
-            double x = 0.0, y = 0.0;
-            if constexpr (BWD) {
-                for (int j = tid; j < sh.R * cols; j += cols) {
-                    x += dsm[j];
-                    y += dsm[kLongThreads + j];
-                }
-            } else if (s0 < s1) {
-                // row lane j took the strip's rows j, j + R, ..: about the first lane's mean
-                const double first = dsm[tid];
-                const int each = (s1 - s0) / sh.R, more = (s1 - s0) % sh.R;
-                for (int j = 0; j < sh.R && s0 + j < s1; ++j) {
-                    const double d = dsm[j * cols + tid] - first, all = (double)(each + (j < more)) * d;
-                    x += all;
-                    y += fma(all, d, dsm[kLongThreads + j * cols + tid]);
-                }
-                const double m = x / (double)(s1 - s0);
-                y -= x * m;
-                x = first + m;
+        dsm[2 * e * kLongThreads + tid] = (double)about[e] + (double)p[e];
+        dsm[(2 * e + 1) * kLongThreads + tid] = (double)q[e];
+    }
+    __syncthreads();
+    for (int i = tid; i < cols * VEC; i += kLongThreads) {
+        const int col = i % cols, e = i / cols, c = (blockIdx.y * kLongThreads + col) * VEC + e;
+        if (c >= a.C) continue;
+        const double *u = dsm + 2 * e * kLongThreads + col, *v = u + kLongThreads;
+        double x = 0.0, y = 0.0;
+        if constexpr (BWD) {
+            for (int j = 0; j < sh.R; ++j) {
+                x += u[j * cols];
+                y += v[j * cols];
             }
-            out[e] = x;
-            out[a.C + e] = y;
+        } else if (s0 < s1) {
+            // row lane j took the strip's rows j, j + R, ..: about the first lane's mean
+            const double first = u[0];
+            const int each = (s1 - s0) / sh.R, more = (s1 - s0) % sh.R;
+            for (int j = 0; j < sh.R && s0 + j < s1; ++j) {
+                const double d = u[j * cols] - first, all = (double)(each + (j < more)) * d;
+                x += all;
+                y += fma(all, d, v[j * cols]);
+            }
+            const double m = x / (double)(s1 - s0);
+            y -= x * m;
+            x = first + m;
         }
+        out[c] = x;
+        out[a.C + c] = y;
     }
 }
 
@@ -910,7 +911,7 @@ cudaError_t norm_go(NormArgs a, cudaStream_t st, int *n)
             if (a.lengths) b.lengths = a.lengths + n0;
             const dim3 grid((unsigned)(b.N * sh.strips), sh.tiles);
             e = timed_launch(st, n, [&] {
-                norm_sums_kernel<T, VEC, BWD><<<grid, kLongThreads, 2 * kLongThreads * sizeof(double), st>>>(b, sh);
+                norm_sums_kernel<T, VEC, BWD><<<grid, kLongThreads, 2 * VEC * kLongThreads * sizeof(double), st>>>(b, sh);
             });
             if (e != cudaSuccess) return e;
             e = timed_launch(st, n, [&] {
