@@ -32,7 +32,8 @@
  * (except where a function says otherwise).  The library allocates nothing and
  * frees nothing.  Every call is asynchronous on the caller's CUDA stream, passed
  * as an opaque pointer (a cudaStream_t; NULL is the legacy default stream), and
- * returns after launching.  Only semicrf_get_device_status synchronises.
+ * returns after launching.  Only the two status calls (semicrf_get_device_status,
+ * semicrf_get_operators_status) synchronise.
  *
  * Workspace: the caller provides `ws` of at least semicrf_workspace_bytes(dims,
  * what) bytes, 256-byte aligned.  The same workspace must be passed unchanged
@@ -311,9 +312,9 @@ semicrf_status semicrf_clear_operators_status(void *stream);
  * keys that make the state three (24 bits); the scores times their decays, and the state
  * where q multiplies it, are held to 2^-17 of each value for 16-bit dtypes and to 24 bits
  * for float32.  Of products of several terms the smallest are left out: 2^-23 of a product
- * for float32, 2^-16 for float16, none for bfloat16.  The results do not depend
- * on which outputs are asked for.  A value that is not finite may spread to every position
- * of its sequence and head.
+ * for float32, 2^-16 for float16, none for bfloat16.  The results do not depend on which
+ * outputs are asked for.  A value that is not finite may spread to every position of its
+ * sequence and head.
  */
 typedef struct {
     int32_t B, T, H, dk, dv;
@@ -365,7 +366,7 @@ semicrf_status semicrf_linear_attention_step(const semicrf_attention_dims *dims,
 /* Activations of the group norm. */
 #define SEMICRF_ACT_NONE 0
 #define SEMICRF_ACT_SILU 1 /* z / (1 + exp(-z)) */
-#define SEMICRF_ACT_GELU 2 /* z Phi(z), Phi the normal distribution function */
+#define SEMICRF_ACT_GELU 2 /* z Phi(z), Phi the normal distribution function (to 1e-7) */
 
 /*
  * Group norm with an activation, channels last:

@@ -11,12 +11,12 @@
 // on the side the formula says.
 //
 // Measured on 26 million parameters.  float32 states: 90 us, which is 591 MB at the
-// measured copy rate, so what is left is the memory's.  8 bits: 113 us for 420 MB (64 us):
-// bound by issue (68 % of the cycles) and by the loads' latency, about 95 instructions a
+// measured copy rate, so what is left is the memory's.  8 bits: 111 us for 420 MB (64 us):
+// bound by issue (69 % of the cycles) and by the loads' latency, about 95 instructions a
 // value, of which 14 are float64.  Square root and quotient to two units of the last place
-// instead of correctly rounded and powers of beta on the host took it from 178 to 143;
-// codes read and written as the high words of doubles 2^1008 (2^992) times too small, a
-// multiplication for a change of the bias and a case for small codes, to 125.
+// instead of correctly rounded and powers of beta on the host saved a fifth; codes read and
+// written as the high words of doubles 2^1008 (2^992) times too small, a multiplication for
+// a change of the bias and a case for small codes, an eighth.
 #include <float.h>
 #include <math.h>
 
@@ -307,8 +307,8 @@ __device__ __forceinline__ int entry_of(const AdamArgs<N> &a, long long block)
     return lo;
 }
 
-// Blocks of a multiprocessor: 8 bits with 4 (64 registers, 20 bytes of them in memory) 113 us,
-// with 3 (74 registers) 125; 32 bits with 5 (48 registers) 90 us, with 3 (74) 107.
+// Blocks of a multiprocessor: 8 bits with 4 (64 registers, 20 bytes of them in memory) a tenth
+// faster than with 3 (74 registers); 32 bits with 5 (47 registers) 90 us, with 3 (74) 107.
 template <int N, bool EIGHT>
 __global__ __launch_bounds__(kThreads, EIGHT ? 4 : 5) void adamw_kernel(const __grid_constant__ AdamArgs<N> a)
 {

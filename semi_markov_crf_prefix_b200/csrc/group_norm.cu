@@ -7,10 +7,10 @@
 // Bound by memory: x once where a row block fits a thread block's registers
 // (norm_reg_kernel, norm_row_kernel), twice where it does not.  Measured, with the bytes
 // that each form moves against the copy rate: 64 000 positions of 512 channels in bf16
-// 38 us forward (131 MB, 53 %) and 65 us backward (197 MB, 46 %), with silu's two
-// transcendentals a value; 4 x 200 000 x 256 bf16 with gelu 75 + 9 + 154 us (410 MB read,
-// then 820 MB read and written: 83 % and 81 %).  The second pass is as near to the issue
-// rate (22 operations a value) as to the memory's.
+// 43 us forward (131 MB, 47 %) and 60 us backward (197 MB, 50 %), with silu's two
+// transcendentals a value; 4 x 200 000 x 256 bf16 with gelu 251 us in three kernels (410 MB
+// read, then 820 MB read and written: 188 us at the copy rate).  The second pass is as near
+// to the issue rate (22 operations a value) as to the memory's.
 #include <float.h>
 #include <math.h>
 
@@ -40,7 +40,8 @@ __device__ __forceinline__ float rcp_approx(float x)
 // and Stegun 7.1.26, erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2) with t = 1 / (1 + p x) and an
 // error below 1.5e-7, at x = |z| / sqrt 2 with the half and the root in the constants.
 // Eleven operations of which two are transcendental; with the library's erfcf the
-// two-pass kernel ran at a fifth of the memory's rate.
+// two-pass kernel ran at a fifth of the memory's rate.  The bound is absolute: of GELU's
+// value itself 5e-5 at z = -3, where that is -4e-3, and more further out.
 __device__ __forceinline__ float normal_tail(float z, float &e)
 {
     e = exp2_approx(z * z * -0.72134752044448170f);
@@ -147,6 +148,9 @@ __device__ __forceinline__ void group_sums(const float *red, float *out, const R
     }
 }
 
+// Two and three blocks an SM for one vector a thread spill 252 and 124 bytes at 16 bits and 8
+// values a vector, and are faster all the same: 16 000 row blocks of 8 x 512 forward 192 us
+// (205 with two blocks and no spill), forward and backward 467 (545 with one).
 template <typename T, int VEC, int U, bool BWD>
 __global__ __launch_bounds__(kRegThreads, U == 1 ? (BWD ? 2 : 3) : 1) void norm_reg_kernel(const __grid_constant__ NormArgs a, const RegShape sh)
 {

@@ -167,8 +167,8 @@ __device__ __forceinline__ void bring_pieces(const Track &g, unsigned char *to, 
 // each 8 steps of 16), which a state carried in them over thousands of chunks would
 // show; so they hold one chunk's sums only, small terms first, and the state is
 // advanced by float32 multiply-adds to nearest.
-// Measured (16 x 4000 positions, 8 heads of 64): float32 262 us of 80 at the copy rate,
-// float16 198 of 40.  One block an SM; bound by the six products a term pair asks for in
+// Measured (16 x 4000 positions, 8 heads of 64): float32 264 us of 80 at the copy rate,
+// float16 204 of 40; backward 768 and 591.  One block an SM; bound by the six products a term pair asks for in
 // float32 (144 matrix instructions a chunk, 5500 cycles at shared memory's rate of 128
 // bytes a cycle, issued from one of the computing warps) and by splitting and staging
 // between them.  32 sentences of 512 positions and 4 heads: 39 us, four chunks in a row.

@@ -16,10 +16,11 @@
 // width 128), must not.
 //
 // Measured: 512 sequences and heads of 1024 positions at width 64 (268 MB, 41 us at the copy
-// rate) 77 us; of 128 x 4000, which fill the SMs once, 100 us, the time of one block's 32
-// chunks in a row (3.1 us each).  Bounds, of some 4200 cycles a chunk and SM: shared
-// memory's traffic about 2600 (matrix operands 1400, K~ 400, tiles in and out 500, the
-// state 130), the matrix unit 1500 (`sm__pipe_tensor_cycles_active` 40 %), memory 2750.
+// rate) 79 us; of 128 x 4000, which fill the SMs once, 109 us, the time of one block's 32
+// chunks in a row (3.4 us each).  A chunk moves 368 KB through shared memory, 2900 cycles at
+// 128 bytes a cycle (matrix operands 208 KB, K~ 64, tiles in and out 80, the state 16); the
+// matrix unit is busy 42 % of the time.  The chain of a chunk's steps, each behind a meeting
+// of all warps, is what bounds it.
 //
 // A walk against time takes a chunk's rows in memory order too: row r is position
 // 127 - r of the chunk, and the tables of decays are mirrored.
@@ -538,10 +539,9 @@ __global__ __launch_bounds__(kThreads, (TmaCfg<D>::kBlocks)) void la_tma_kernel(
 // 32 KB at width 128).
 // Segments that end inside the sequence's last chunk are not asked for.
 //
-// Measured: 32 walks of 40 chunks at width 128 in 90 us, 2.2 us a chunk (two terms at the
-// matrix unit 0.8), the call of 4 x 20000 positions and 8 heads 309 us; 334 with the outputs'
-// kernel less its outputs, one tile of each kind.  At width 64 two blocks share an SM and the
-// second tiles change nothing (52 us for 288 segments of 22 chunks).
+// Measured: 96 walks of 40 chunks at width 128 in 111 us, 2.8 us a chunk (of which the matrix
+// unit is busy a third); at width 64, where two blocks share an SM, 51 us for 280 walks of 22
+// chunks.
 template <int D>
 struct StateCfg {
     static constexpr int kTile = D / 64 * 16384, NK = 3;   // (terms of K~)
