@@ -411,8 +411,8 @@ semicrf_status semicrf_group_norm_backward(const semicrf_norm_dims *dims, const 
  * A code's value is scale times a small float of 3 mantissa bits: m has a sign bit
  * and 4 exponent bits (bias 15), v 5 exponent bits (bias 31); a block's scale is its
  * largest magnitude / 1.875, codes are nearest even, and a v above 0 has a code above 0.
- * A block in which a moment is not finite (or passes float32, as the square of a gradient
- * above 1e20 does) reads as NaN from then on, all 256 values of it.
+ * A block in which a moment is not finite, or passes float32 as (1-beta2) g^2 may, reads as
+ * NaN from then on, all 256 values of it.
  * A float64 gradient is scaled before it is rounded.  eps, and with float32 states the
  * grad_scale of other gradients, are 0 or within float32's normal range.
  * step counts from 1; step_ptr (int64) and lr_ptr (float32), where not NULL, are

@@ -121,3 +121,28 @@ def test_the_largest_values_of_float32(dk, dv, T):
         o, s = sc.linear_attention(q, k, v, ld, scale=1.0, initial_state=s0, return_state=True)
         assert torch.allclose(s[0, 0, 0, 5].double(), s0[0, 0, 0, 5].double() * torch.exp(ld.double() * T)[0], rtol=2.0 ** -16)
         assert torch.allclose(o[0, 0, 0, 5].double(), 0.5 * s0[0, 0, 0, 5].double() * torch.exp(ld.double())[0], rtol=2.0 ** -16)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [3, 300])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_what_is_not_finite_is_not_lost(dtype, d, T, value):
+    # wherever it stands in a valid position, its own outputs and the state show it, and other
+    # sequences and heads do not
+    g = torch.Generator(device="cuda").manual_seed(15)
+    ld = torch.tensor([-0.1, -0.001], device="cuda")
+    for which in range(4):
+        x = [torch.randn(2, T, 2, d, generator=g, device="cuda").to(dtype) for _ in range(3)]
+        s0 = torch.randn(2, 2, d, d, generator=g, device="cuda")
+        if which < 3:
+            x[which][1, T - 2, 1, 5] = value
+        else:
+            s0[1, 1, 5, 7] = value
+        o, s = sc.linear_attention(*x, ld, initial_state=s0, return_state=True)
+        bad = o[1, T - 2, 1]
+        assert not torch.isfinite(bad).all()
+        if which > 0:
+            assert not torch.isfinite(s[1, 1]).all()
+        assert torch.isfinite(o[0]).all() and torch.isfinite(o[1, :, 0]).all()
+        assert torch.isfinite(s[0]).all() and torch.isfinite(s[1, 0]).all()
